@@ -454,6 +454,168 @@ size_t misa_prefill_workspace_bytes(const misa_shape* shape, misa_kdtype kdtype,
                                     int32_t k_prime, int32_t chunk);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The paged serving step around misa_indexer_paged: page planning from request
+ * lengths, rotary positions, the write of new keys and values into their
+ * pages, and attention over the pages or over the tokens the indexer picked.
+ *
+ * Ragged batches.  These calls take the new tokens of n_seq sequences as rows
+ * 0 .. q_start[n_seq]-1 of token-major tensors: sequence b's new tokens are
+ * rows q_start[b] .. q_start[b+1]-1, in order, and are the last ones of its
+ * kv_lens[b] tokens, so new token i of m sits at position kv_lens[b] - m + i.
+ * Lengths live on the GPU and are read there; rows from q_start[n_seq] on
+ * (a padded batch) are left as they were.
+ * Strided inputs.  Where a stride is given it counts elements; the last
+ * dimension is dense.
+ * Slots.  Row r of page p of a pool with page_keys rows a page is slot
+ * p * page_keys + r.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Block tables and slot maps from request lengths.  Sequence b holds
+ * cached_lens[b] tokens in pages its table row already names, and gets
+ * new_lens[b] more.  With have = ceil(cached / page_keys) and need =
+ * ceil((cached + new) / page_keys) - have, the call takes `need` pages for
+ * each sequence from free_pages, in sequence order, writes them to
+ * block_table[b][have .. have+need-1] (the row's other entries stay as they
+ * were), and writes
+ *   q_start[0..n_seq]  first new token of each sequence (exclusive sums of new_lens)
+ *   kv_lens[b]         cached + new
+ *   slots[t]           slot of new token t, -1 for t >= q_start[n_seq]
+ *   positions[t]       its position in its sequence, -1 for t >= q_start[n_seq]
+ *   n_taken[0]         pages needed: free_pages[0 .. n_taken-1] are in use now
+ * Negative lengths count as 0.  Where free_pages is too short (n_taken >
+ * n_free) the entries without a page become -1 and so do the slots in them;
+ * tokens past the table (max_pages * page_keys) get slot -1 and no page.
+ * Tokens past n_tokens (slots / positions too short) get no slot.
+ * cached_lens, new_lens: int32 [n_seq].  free_pages: int32 [n_free], NULL when
+ * n_free = 0.  block_table: int32 [n_seq][max_pages].  slots: int64 [n_tokens],
+ * positions: int32 [n_tokens].  1 <= n_seq <= 65535, page_keys >= 1,
+ * max_pages >= 1, n_tokens <= 2^26 (larger: MISA_ERR_UNSUPPORTED).
+ */
+misa_status misa_plan_pages(int32_t n_seq, const int32_t* cached_lens, const int32_t* new_lens, int32_t page_keys,
+                            const int32_t* free_pages, int32_t n_free, int32_t* block_table, int64_t max_pages,
+                            int32_t* q_start, int32_t* kv_lens, int64_t* slots, int32_t* positions,
+                            int64_t n_tokens, int32_t* n_taken, void* stream);
+
+typedef enum { MISA_T_BF16 = 0, MISA_T_FP16 = 1, MISA_T_FP32 = 2 } misa_dtype;
+typedef enum {
+  MISA_ROPE_HALF = 0,         /* pair j: elements j and j + rotary_dim/2 */
+  MISA_ROPE_INTERLEAVED = 1   /* pair j: elements 2j and 2j + 1 */
+} misa_rope_layout;
+
+/* The rotation of a head's rotary part: elements rot_start ..
+ * rot_start+rotary_dim-1; the rest of the head is copied.  Pair j of a token
+ * at position p turns by the angle p * inv_freq[j] (radians) and is scaled by
+ * mscale (the attention factor of a context-stretched model; 1 otherwise):
+ *   (a, b) -> mscale * (a cos - b sin, a sin + b cos)
+ * backward != 0: the transposed map (a cos + b sin, b cos - a sin) * mscale,
+ * which takes the gradient of the output to the gradient of the input.
+ * inv_freq: double [rotary_dim/2], positions: int32 [n_tokens], both on the
+ * GPU.  Angles are formed and reduced in fp64, so far positions keep their
+ * precision; the rotation runs in fp32 (or wider) and rounds once. */
+typedef struct {
+  const double* inv_freq;
+  const int32_t* positions;
+  int32_t rotary_dim;   /* even, 2 .. 1024 */
+  int32_t rot_start;    /* >= 0, rot_start + rotary_dim <= head_dim */
+  int32_t layout;       /* misa_rope_layout */
+  int32_t backward;
+  double mscale;
+} misa_rope_spec;
+
+/* Rotary positions of x [n_tokens][n_heads][head_dim] into out (same type).
+ * out == x with the same strides rotates in place; any other overlap is a
+ * precondition violation.  Strides must keep the heads apart. */
+misa_status misa_rope(const misa_rope_spec* spec, const void* x, misa_dtype dtype, int64_t n_tokens, int32_t n_heads,
+                      int32_t head_dim, int64_t x_stride_token, int64_t x_stride_head, void* out,
+                      int64_t out_stride_token, int64_t out_stride_head, void* stream);
+
+/*
+ * New keys (and values) into their pages.  Row (t, h) of k goes to
+ * k_pages[slot / page_keys][slot % page_keys][h][:], slot = slots[t]; v, when
+ * given, to v_pages likewise.  spec != NULL rotates k first (v never; spec's
+ * backward must be 0).
+ * Rows are rounded (bf16) or quantised (e4m3) once, after the rotation:
+ * scale_pages[...][h] = fp32(amax / 448) of the row (1 for a zero row) and
+ * codes = e4m3fn round-to-nearest-even of fp32(row / scale), the rule of
+ * misa_quantize_q.
+ * Slots outside [0, n_pages * page_keys) write nothing (padding); slots are
+ * distinct, else which of the rows a slot holds is not defined.  With
+ * n_heads = 1 and head_dim = 128 the pages are those of misa_indexer_paged.
+ * k, v: bf16, strides in elements and multiples of 8, 16-byte aligned.
+ * head_dim: a multiple of 8 up to 512 (else MISA_ERR_UNSUPPORTED).
+ */
+misa_status misa_write_pages(int64_t n_tokens, int32_t n_heads, int32_t head_dim, const uint16_t* k,
+                             int64_t k_stride_token, int64_t k_stride_head, const uint16_t* v,
+                             int64_t v_stride_token, int64_t v_stride_head, const int64_t* slots,
+                             const misa_rope_spec* spec, void* k_pages, void* v_pages, misa_kdtype kdtype,
+                             float* k_scale_pages, float* v_scale_pages, int64_t n_pages, int32_t page_keys,
+                             void* stream);
+
+/* Paged keys and values: row (token t of sequence b, kv head g) is
+ * k[block_table[b][t / page_keys]][t % page_keys][g][:], of kdtype, with fp8
+ * rows' scales in k_scale [n_pages][page_keys][n_kv_heads] (v likewise).
+ * page_keys >= 1, any; n_pages * page_keys < 2^31 (else
+ * MISA_ERR_UNSUPPORTED).  Table entries of pages that hold visible keys are a
+ * precondition (in [0, n_pages); out-of-range ones are clamped, never
+ * faulting); rows behind a sequence's end may hold anything. */
+typedef struct {
+  const void* k;
+  const void* v;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_table;   /* [n_seq][max_pages] */
+  int64_t max_pages, n_pages;
+  int32_t page_keys;
+  int32_t kdtype;               /* misa_kdtype */
+} misa_kv_pages;
+
+typedef struct {
+  int32_t n_seq;                /* 1..65535 */
+  int32_t n_heads;              /* query heads, a multiple of n_kv_heads, <= 1024 */
+  int32_t n_kv_heads;
+  int32_t head_dim;             /* 64 or 128 */
+  int64_t n_tokens;             /* rows of q and out, 0..2^26 */
+  int64_t q_stride_token, q_stride_head;   /* multiples of 8 */
+  int32_t max_new;              /* no sequence has more new tokens than this; 0: not known */
+  float scale;                  /* on q . k, usually 1/sqrt(head_dim) */
+} misa_attn_shape;
+
+/*
+ * Causal attention of the new tokens of a ragged batch over their sequences'
+ * pages (the new keys written already): query head h of a token at position p
+ * reads kv head h / (n_heads / n_kv_heads),
+ *   out = sum_{s <= p} softmax_s(scale * q . k[s]) v[s]
+ *   lse = log sum_{s <= p} exp(scale * q . k[s])
+ * A row that sees no key (kv_lens[b] = 0) gives out = 0, lse = -inf.
+ * One call takes decodes (one new token), chunks and both mixed.  Products
+ * accumulate in fp32; softmax statistics are fp32; the softmax weights are
+ * rounded to bf16 for the product with v.
+ * q: bf16.  out: bf16 [n_tokens][n_heads][head_dim] dense, lse: float
+ * [n_tokens][n_heads] or NULL.  kv_lens[b] past max_pages * page_keys counts
+ * as that.  ws: misa_attention_paged_workspace_bytes() bytes (16-byte
+ * aligned; may be NULL when that is 0); nothing in it outlives the call.
+ */
+misa_status misa_attention_paged(const misa_attn_shape* shape, const misa_kv_pages* pages, const uint16_t* q,
+                                 const int32_t* q_start, const int32_t* kv_lens, uint16_t* out, float* lse, void* ws,
+                                 size_t ws_bytes, void* stream);
+size_t misa_attention_paged_workspace_bytes(const misa_attn_shape* shape, const misa_kv_pages* pages);
+
+/*
+ * The same over the tokens that the indexer picked: new token t reads only
+ * tokens idx[t][0..topk-1] of its sequence (an indexer call's idx viewed as
+ * [n_tokens][topk]).  Entries that are negative or lie behind the token's own
+ * position count as absent; an id listed twice counts twice.
+ * idx: int32 [n_tokens][topk], 1 <= topk <= MISA_MAX_TOPK.
+ */
+misa_status misa_attention_selected(const misa_attn_shape* shape, const misa_kv_pages* pages, const uint16_t* q,
+                                    const int32_t* q_start, const int32_t* kv_lens, const int32_t* idx, int32_t topk,
+                                    uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+size_t misa_attention_selected_workspace_bytes(const misa_attn_shape* shape, const misa_kv_pages* pages, int32_t topk);
+
+/*
  * Profiling.  The stages of misa_indexer (and of the calls that run parts of
  * it: misa_sparse_head_topk[_q8], misa_indexer_cached, misa_indexer_q8,
  * misa_indexer_noalloc, misa_prefill_chunked) whose kernels a caller can time

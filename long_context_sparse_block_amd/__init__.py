@@ -15,3 +15,8 @@ from ._lib import (  # noqa: F401
     misa_gather_keys_paged, status_str, misa_indexer_noalloc, NOALLOC_SCRATCH_BYTES, MISA_ERR_SCRATCH,
     misa_profile_stage, STAGES, misa_indexer_paged, misa_indexer_paged_workspace_bytes,
 )
+from .serving import (  # noqa: F401
+    AttnShape, KvPages, PagePlan, RopeSpec, misa_attention_paged, misa_attention_paged_workspace_bytes,
+    misa_attention_selected, misa_attention_selected_workspace_bytes, misa_plan_pages, misa_rope, misa_write_pages,
+    rope_inv_freq,
+)

@@ -34,7 +34,10 @@ EXPORTED = ("misa_status_str", "misa_pool_keys", "misa_route_heads", "misa_spars
             "misa_pool_keys_cached", "misa_indexer_cached", "misa_indexer_cached_workspace_bytes",
             "misa_prefill_chunked", "misa_prefill_workspace_bytes", "misa_indexer_q8",
             "misa_indexer_q8_workspace_bytes", "misa_gather_keys_paged", "misa_indexer_noalloc",
-            "misa_profile_stage", "misa_indexer_paged", "misa_indexer_paged_workspace_bytes")
+            "misa_profile_stage", "misa_indexer_paged", "misa_indexer_paged_workspace_bytes",
+            "misa_plan_pages", "misa_rope", "misa_write_pages", "misa_attention_paged",
+            "misa_attention_paged_workspace_bytes", "misa_attention_selected",
+            "misa_attention_selected_workspace_bytes")
 STAGES = dict(pool=1, route=2, score_sample=3, sample_threshold=4, score_candidates=5, region_select=6,
               rescore=7, rerank=8, final_topk=9, score_logits=10, logits_topk=11)
 MISA_ERR_SCRATCH = -5
@@ -91,6 +94,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "misa_gather_keys_paged": [S, P, ctypes.c_int, P, P, i64, i64, i32, P, P, P],
         "misa_indexer_paged": [S, P, P, P, ctypes.c_int, P, P, i64, i64, i32, i32, i32, i64, P, P, i64, P, P, P,
                                sz, P],
+        "misa_plan_pages": [i32, P, P, i32, P, i32, P, i64, P, P, P, P, i64, P, P],
+        "misa_rope": [P, P, ctypes.c_int, i64, i32, i32, i64, i64, P, i64, i64, P],
+        "misa_write_pages": [i64, i32, i32, P, i64, i64, P, i64, i64, P, P, P, P, ctypes.c_int, P, P, i64, i32, P],
+        "misa_attention_paged": [P, P, P, P, P, P, P, P, sz, P],
+        "misa_attention_selected": [P, P, P, P, P, P, i32, P, P, P, sz, P],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -112,6 +120,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.misa_prefill_workspace_bytes.restype = sz
     lib.misa_indexer_paged_workspace_bytes.argtypes = [S, ctypes.c_int, i32, i32]
     lib.misa_indexer_paged_workspace_bytes.restype = sz
+    lib.misa_attention_paged_workspace_bytes.argtypes = [P, P]
+    lib.misa_attention_paged_workspace_bytes.restype = sz
+    lib.misa_attention_selected_workspace_bytes.argtypes = [P, P, i32]
+    lib.misa_attention_selected_workspace_bytes.restype = sz
     _lib = lib
     return lib
 

@@ -162,4 +162,43 @@ hipError_t launch_score_q8_cands(const misa_shape& s, const uint8_t* q8, const f
 hipError_t launch_topk_flagged(const misa_shape& s, int k, const float* slab, int64_t ld, const SlabBatch& sb,
                                const uint32_t* row_flag, int32_t* idx, float* vals, bool sorted, hipStream_t st);
 
+// ---------------------------------------------------------------------------
+// The paged serving step (misa.h): page planning, rotary positions, page
+// writes, attention.
+// ---------------------------------------------------------------------------
+hipError_t launch_plan_pages(int n_seq, const int32_t* cached_lens, const int32_t* new_lens, int page_keys,
+                             const int32_t* free_pages, int n_free, int32_t* block_table, int64_t max_pages,
+                             int32_t* q_start, int32_t* kv_lens, int64_t* slots, int32_t* positions, int64_t n_tokens,
+                             int32_t* n_taken, hipStream_t st);
+hipError_t launch_rope(const misa_rope_spec& spec, const void* x, int dtype, int64_t n_tokens, int H, int D,
+                       int64_t x_st, int64_t x_sh, void* out, int64_t o_st, int64_t o_sh, hipStream_t st);
+hipError_t launch_write_pages(int64_t n_tokens, int H, int D, const uint16_t* k, int64_t k_st, int64_t k_sh,
+                              const uint16_t* v, int64_t v_st, int64_t v_sh, const int64_t* slots,
+                              const misa_rope_spec* spec, void* k_pages, void* v_pages, int kdtype, float* k_scale,
+                              float* v_scale, int64_t n_slots, hipStream_t st);
+
+// What the attention kernels take (strides in elements; scale_log2 = scale * log2 e)
+struct AttnArgs {
+  const uint16_t* q;
+  int64_t q_st, q_sh;
+  const void *k, *v;
+  const float *k_scale, *v_scale;
+  const int32_t* table;
+  int64_t max_pages, n_pages;
+  int page_keys;
+  const int32_t *q_start, *kv_lens;
+  const int32_t* idx;   // nullable: the selected tokens [n_tokens][topk]
+  int topk;
+  uint16_t* out;
+  float* lse;           // nullable
+  float scale_log2;
+  int n_seq, n_heads, n_kv_heads;
+  int64_t n_tokens;
+};
+// topk = 0: over every visible key
+size_t attn_workspace_bytes(const misa_attn_shape& s, const misa_kv_pages& pg, int topk);
+hipError_t launch_attention(const misa_attn_shape& s, const misa_kv_pages& pg, const uint16_t* q,
+                            const int32_t* q_start, const int32_t* kv_lens, const int32_t* idx, int topk,
+                            uint16_t* out, float* lse, void* ws, hipStream_t st);
+
 }  // namespace misa

@@ -1,0 +1,288 @@
+// Rotary positions (misa_rope) and the write of new rows into a paged cache
+// (misa_write_pages, which rotates the keys on their way).
+//
+// Pair j of a token at position p turns by p * inv_freq[j].  The angle is
+// formed in fp64 as turns (p * inv_freq / 2 pi) and reduced by dropping its
+// whole turns, so a position of 10^6 costs no precision; cos and sin are then
+// those of a fraction of a turn.  They depend on (token, pair) alone: a
+// workgroup takes a few tokens, forms their table once in LDS and uses it for
+// every head.
+//
+// Both kernels are bound by HBM: each value is read once and written once, 16
+// bytes a lane and access where the sizes are multiples of it.
+#include <algorithm>
+
+#include "misa_common.h"
+#include "misa_launch.h"
+
+namespace misa {
+
+namespace {
+constexpr int kThreads = 256;
+constexpr int64_t kMaxGroups = 1 << 20;   // workgroups of a launch (it holds fewer than 2^32 threads)
+constexpr double kInv2Pi = 0.15915494309189533576888;
+
+// cos and sin of `turns` whole turns, times m
+__device__ __forceinline__ float2 turn_f32(double turns, double m) {
+  const float r = (float)(2.0 * (turns - __builtin_rint(turns)));   // half turns in [-1, 1]
+  float s, c;
+  sincospif(r, &s, &c);
+  return make_float2((float)(c * m), (float)(s * m));
+}
+__device__ __forceinline__ double2 turn_f64(double turns, double m) {
+  double s, c;
+  sincospi(2.0 * (turns - __builtin_rint(turns)), &s, &c);
+  return make_double2(c * m, s * m);
+}
+
+template <int DT> struct Elem;
+template <> struct Elem<MISA_T_BF16> {
+  using T = uint16_t;
+  static __device__ __forceinline__ float load(T x) { return bf16_bits_to_f32(x); }
+  static __device__ __forceinline__ T store(float x) { return (T)(pk_bf16(x, 0.f) & 0xFFFFu); }
+};
+template <> struct Elem<MISA_T_FP16> {
+  using T = uint16_t;
+  static __device__ __forceinline__ float load(T x) { return (float)__builtin_bit_cast(_Float16, x); }
+  static __device__ __forceinline__ T store(float x) { return __builtin_bit_cast(uint16_t, (_Float16)x); }
+};
+template <> struct Elem<MISA_T_FP32> {
+  using T = float;
+  static __device__ __forceinline__ float load(T x) { return x; }
+  static __device__ __forceinline__ T store(float x) { return x; }
+};
+
+struct RopeArgs {
+  const double* inv_freq;
+  const int32_t* positions;
+  int half, start, layout;
+  double mscale;
+  float sign;   // -1: the transposed rotation
+};
+
+RopeArgs rope_args(const misa_rope_spec& r) {
+  return RopeArgs{r.inv_freq, r.positions, r.rotary_dim / 2, r.rot_start, r.layout, r.mscale,
+                  r.backward ? -1.f : 1.f};
+}
+}  // namespace
+
+// The table of TT tokens in LDS, then every (token, head) in units of V
+// elements (V = 16 bytes' worth, or 1 where sizes or alignment do not divide):
+// a unit of the rotary part is V pairs' elements (two pieces of V for the half
+// layout, one for the interleaved, with pairs inside it; two single elements
+// when V = 1), any other unit a copy.  In place, copies are skipped.
+template <int DT, int V>
+__global__ void __launch_bounds__(kThreads) k_rope(const typename Elem<DT>::T* x, int64_t x_st, int64_t x_sh,
+                                                   typename Elem<DT>::T* out, int64_t o_st, int64_t o_sh,
+                                                   int64_t n_tokens, int H, int D, int TT, int in_place, RopeArgs r) {
+  using E = Elem<DT>;
+  using T = typename E::T;
+  extern __shared__ float2 s_cs[];   // [TT][half]
+  struct alignas(V * sizeof(T)) Vec { T v[V]; };
+  const bool split = r.layout == MISA_ROPE_HALF || V == 1;   // a unit's two sides are apart
+  const int rot_units = split ? r.half / V : 2 * r.half / V;
+  const int pre = r.start / V;                               // copied units before the rotary part
+  const int units = rot_units + (in_place ? 0 : (D - 2 * r.half) / V);
+  for (int64_t t0 = (int64_t)blockIdx.x * TT; t0 < n_tokens; t0 += (int64_t)gridDim.x * TT) {
+    const int nt = (int)min((int64_t)TT, n_tokens - t0);
+    for (int i = threadIdx.x; i < nt * r.half; i += kThreads) {
+      const int t = i / r.half, j = i - t * r.half;
+      s_cs[i] = turn_f32((double)r.positions[t0 + t] * (r.inv_freq[j] * kInv2Pi), r.mscale);
+    }
+    __syncthreads();
+    const int total = nt * H * units;
+    for (int i = threadIdx.x; i < total; i += kThreads) {
+      const int row = i / units, u = i - row * units;
+      const int t = row / H, h = row - t * H;
+      const T* xr = x + (t0 + t) * x_st + h * x_sh;
+      T* orow = out + (t0 + t) * o_st + h * o_sh;
+      const float2* cs = s_cs + t * r.half;
+      if (u < rot_units) {
+        if (split) {
+          const int j = u * V;
+          const int ia = r.layout == MISA_ROPE_HALF ? r.start + j : r.start + 2 * j;
+          const int ib = r.layout == MISA_ROPE_HALF ? ia + r.half : ia + 1;
+          const Vec a = *reinterpret_cast<const Vec*>(xr + ia), b = *reinterpret_cast<const Vec*>(xr + ib);
+          Vec ya, yb;
+  #pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float c = cs[j + e].x, s = cs[j + e].y * r.sign, fa = E::load(a.v[e]), fb = E::load(b.v[e]);
+            ya.v[e] = E::store(__builtin_fmaf(fa, c, -(fb * s)));
+            yb.v[e] = E::store(__builtin_fmaf(fa, s, fb * c));
+          }
+          *reinterpret_cast<Vec*>(orow + ia) = ya;
+          *reinterpret_cast<Vec*>(orow + ib) = yb;
+        } else {
+          const int at = r.start + u * V;
+          const Vec a = *reinterpret_cast<const Vec*>(xr + at);
+          Vec y;
+  #pragma unroll
+          for (int e = 0; e < V / 2; ++e) {
+            const float2 k = cs[u * (V / 2) + e];
+            const float c = k.x, s = k.y * r.sign, fa = E::load(a.v[2 * e]), fb = E::load(a.v[2 * e + 1]);
+            y.v[2 * e] = E::store(__builtin_fmaf(fa, c, -(fb * s)));
+            y.v[2 * e + 1] = E::store(__builtin_fmaf(fa, s, fb * c));
+          }
+          *reinterpret_cast<Vec*>(orow + at) = y;
+        }
+      } else {
+        const int w = u - rot_units;
+        const int at = (w < pre ? w : w + 2 * r.half / V) * V;
+        *reinterpret_cast<Vec*>(orow + at) = *reinterpret_cast<const Vec*>(xr + at);
+      }
+    }
+    __syncthreads();   // the table is free for the next tokens
+  }
+}
+
+namespace {
+template <int DT>
+hipError_t rope_type(const RopeArgs& r, const void* x, int64_t x_st, int64_t x_sh, void* out, int64_t o_st,
+                     int64_t o_sh, int64_t n, int H, int D, hipStream_t st) {
+  using T = typename Elem<DT>::T;
+  constexpr int V = 16 / (int)sizeof(T);
+  const bool in_place = x == out;
+  const int side = r.layout == MISA_ROPE_HALF ? r.half : 2 * r.half;
+  const bool vec = side % V == 0 && r.start % V == 0 && D % V == 0 && x_st % V == 0 && x_sh % V == 0 &&
+                   o_st % V == 0 && o_sh % V == 0 && ((uintptr_t)x & 15) == 0 && ((uintptr_t)out & 15) == 0;
+  // tokens of a workgroup: about 4 units a thread, but no fewer than four
+  // workgroups to a CU where the call has them, and a table within 32 KB
+  const int units = (D - (in_place ? D - 2 * r.half : 0)) / (vec ? V : 1);
+  int64_t TT = std::max<int64_t>(1, 4 * kThreads / std::max<int64_t>(1, (int64_t)H * units));
+  TT = std::min<int64_t>(TT, std::max<int64_t>(1, n / 1024));
+  TT = std::min<int64_t>(TT, std::max<int64_t>(1, 32768 / (r.half * (int64_t)sizeof(float2))));
+  const dim3 grid((unsigned)std::min<int64_t>((n + TT - 1) / TT, kMaxGroups));
+  const size_t lds = (size_t)TT * r.half * sizeof(float2);
+  if (vec)
+    hipLaunchKernelGGL((k_rope<DT, V>), grid, dim3(kThreads), lds, st, static_cast<const T*>(x), x_st, x_sh,
+                       static_cast<T*>(out), o_st, o_sh, n, H, D, (int)TT, (int)in_place, r);
+  else
+    hipLaunchKernelGGL((k_rope<DT, 1>), grid, dim3(kThreads), lds, st, static_cast<const T*>(x), x_st, x_sh,
+                       static_cast<T*>(out), o_st, o_sh, n, H, D, (int)TT, (int)in_place, r);
+  return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_rope(const misa_rope_spec& spec, const void* x, int dtype, int64_t n_tokens, int H, int D,
+                       int64_t x_st, int64_t x_sh, void* out, int64_t o_st, int64_t o_sh, hipStream_t st) {
+  const RopeArgs r = rope_args(spec);
+  if (dtype == MISA_T_BF16) return rope_type<MISA_T_BF16>(r, x, x_st, x_sh, out, o_st, o_sh, n_tokens, H, D, st);
+  if (dtype == MISA_T_FP16) return rope_type<MISA_T_FP16>(r, x, x_st, x_sh, out, o_st, o_sh, n_tokens, H, D, st);
+  return rope_type<MISA_T_FP32>(r, x, x_st, x_sh, out, o_st, o_sh, n_tokens, H, D, st);
+}
+
+// One row (token, head, k or v) to LPR lanes (LPR = D / 8 rounded up to a power
+// of two), 8 values a lane.  The rotation runs in fp64: few rows share a
+// rotation here (one head of indexer keys), and a value that lands on the other
+// side of an e4m3 border is an error of half a step, so the value that meets
+// the border should be the true one.
+template <bool FP8>
+__global__ void __launch_bounds__(kThreads) k_write_pages(
+    const uint16_t* __restrict__ k, int64_t k_st, int64_t k_sh, const uint16_t* __restrict__ v, int64_t v_st,
+    int64_t v_sh, const int64_t* __restrict__ slots, int64_t n_tokens, int H, int D, int lpr_log2, int TT,
+    int64_t n_slots, void* __restrict__ k_pages, void* __restrict__ v_pages, float* __restrict__ k_scale,
+    float* __restrict__ v_scale, RopeArgs r) {
+  extern __shared__ double2 s_cs2[];   // [TT][half]
+  const int lpr = 1 << lpr_log2;
+  const int p = threadIdx.x & (lpr - 1);
+  const int e0 = p * 8;
+  const int sides = v != nullptr ? 2 : 1;
+  const int rows_per_pass = kThreads >> lpr_log2;
+  for (int64_t t0 = (int64_t)blockIdx.x * TT; t0 < n_tokens; t0 += (int64_t)gridDim.x * TT) {
+    const int nt = (int)min((int64_t)TT, n_tokens - t0);
+    if (r.half > 0) {
+      for (int i = threadIdx.x; i < nt * r.half; i += kThreads) {
+        const int t = i / r.half, j = i - t * r.half;
+        s_cs2[i] = turn_f64((double)r.positions[t0 + t] * (r.inv_freq[j] * kInv2Pi), r.mscale);
+      }
+      __syncthreads();
+    }
+    const int rows = nt * H * sides;
+    for (int row0 = 0; row0 < rows; row0 += rows_per_pass) {
+      const int row = row0 + (int)(threadIdx.x >> lpr_log2);
+      if (row >= rows) continue;   // uniform over a row's lanes
+      const int t = row / (H * sides), hs = row - t * (H * sides);
+      const bool is_v = hs >= H;
+      const int h = is_v ? hs - H : hs;
+      const int64_t slot = slots[t0 + t];
+      if (slot < 0 || slot >= n_slots) continue;
+      const uint16_t* src = is_v ? v + (t0 + t) * v_st + h * v_sh : k + (t0 + t) * k_st + h * k_sh;
+      const bool live = e0 < D;
+      float x[8];
+      {
+        const uint4 w4 = live ? *reinterpret_cast<const uint4*>(src + e0) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+  #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
+          x[2 * i + 1] = bf16_bits_to_f32(w[i] >> 16);
+        }
+      }
+      if (r.half > 0 && !is_v && live && e0 + 8 > r.start && e0 < r.start + 2 * r.half) {
+        const double2* cs = s_cs2 + t * r.half;
+  #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int q = e0 + i - r.start;   // element of the rotary part
+          if (q < 0 || q >= 2 * r.half) continue;
+          const bool hl = r.layout == MISA_ROPE_HALF;
+          const bool second = hl ? q >= r.half : (q & 1);
+          const int j = hl ? (second ? q - r.half : q) : q >> 1;
+          const int other = hl ? (second ? q - r.half : q + r.half) : q ^ 1;
+          const double mine = x[i], his = bf16_bits_to_f32(src[r.start + other]);
+          // first: a c - b s; second: b c + a s
+          x[i] = (float)(mine * cs[j].x + (second ? his : -his) * cs[j].y);
+        }
+      }
+      const int64_t dst_row = slot * H + h;
+      if constexpr (FP8) {
+        float amax = 0.f;
+  #pragma unroll
+        for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(x[i]));
+        for (int o = lpr >> 1; o >= 1; o >>= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o, lpr));
+        const float s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+        uint32_t c[2];
+  #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          int u = 0;
+          u = __builtin_amdgcn_cvt_pk_fp8_f32(__fdiv_rn(x[4 * i], s), __fdiv_rn(x[4 * i + 1], s), u, false);
+          u = __builtin_amdgcn_cvt_pk_fp8_f32(__fdiv_rn(x[4 * i + 2], s), __fdiv_rn(x[4 * i + 3], s), u, true);
+          c[i] = (uint32_t)u;
+        }
+        uint8_t* pool = static_cast<uint8_t*>(is_v ? v_pages : k_pages);
+        if (live) *reinterpret_cast<uint2*>(pool + dst_row * D + e0) = make_uint2(c[0], c[1]);
+        if (p == 0) (is_v ? v_scale : k_scale)[dst_row] = s;
+      } else {
+        uint16_t* pool = static_cast<uint16_t*>(is_v ? v_pages : k_pages);
+        if (live)
+          *reinterpret_cast<uint4*>(pool + dst_row * D + e0) =
+              make_uint4(pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3]), pk_bf16(x[4], x[5]), pk_bf16(x[6], x[7]));
+      }
+    }
+    __syncthreads();   // the table is free for the next tokens
+  }
+}
+
+hipError_t launch_write_pages(int64_t n_tokens, int H, int D, const uint16_t* k, int64_t k_st, int64_t k_sh,
+                              const uint16_t* v, int64_t v_st, int64_t v_sh, const int64_t* slots,
+                              const misa_rope_spec* spec, void* k_pages, void* v_pages, int kdtype, float* k_scale,
+                              float* v_scale, int64_t n_slots, hipStream_t st) {
+  RopeArgs r{};
+  if (spec != nullptr) r = rope_args(*spec);
+  int lpr_log2 = 0;
+  while ((8 << lpr_log2) < D) ++lpr_log2;
+  // tokens of a workgroup: about one pass of its threads, table within 32 KB
+  const int64_t lanes = ((int64_t)H * (v != nullptr ? 2 : 1)) << lpr_log2;
+  int64_t TT = std::max<int64_t>(1, kThreads / lanes);
+  if (r.half > 0) TT = std::min<int64_t>(TT, std::max<int64_t>(1, 32768 / (r.half * (int64_t)sizeof(double2))));
+  const dim3 grid((unsigned)std::min<int64_t>((n_tokens + TT - 1) / TT, kMaxGroups));
+  const size_t lds = (size_t)TT * r.half * sizeof(double2);
+  if (kdtype == MISA_K_FP8_E4M3)
+    hipLaunchKernelGGL(k_write_pages<true>, grid, dim3(kThreads), lds, st, k, k_st, k_sh, v, v_st, v_sh, slots,
+                       n_tokens, H, D, lpr_log2, (int)TT, n_slots, k_pages, v_pages, k_scale, v_scale, r);
+  else
+    hipLaunchKernelGGL(k_write_pages<false>, grid, dim3(kThreads), lds, st, k, k_st, k_sh, v, v_st, v_sh, slots,
+                       n_tokens, H, D, lpr_log2, (int)TT, n_slots, k_pages, v_pages, k_scale, v_scale, r);
+  return hipGetLastError();
+}
+
+}  // namespace misa
