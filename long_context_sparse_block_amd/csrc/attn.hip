@@ -1,119 +1,126 @@
-// Causal attention of new tokens over a paged cache (misa_attention_paged) and
-// over the tokens the indexer selected (misa_attention_selected).
+// Host side of the attention calls: which kernel takes which rows, how the keys
+// are split, and the workspace the splits need.
 //
-//   out = sum_s softmax_s(scale q . k[s]) v[s],   lse = log sum_s exp(scale q . k[s])
-//
-// One wave for each (token, query head).  Keys in runs of 64: lane l holds key
-// l of the run, its score and (after the run's maximum) its weight; then the
-// lanes turn to output elements, D / 64 of them each, and walk the run's
-// values.  One pass over the keys with the running maximum and sum.
-#include <math.h>
+// The lengths live on the GPU, so the plan is made from what the host knows:
+// the tokens, the heads, the table's width and the caller's bound on a
+// sequence's new tokens.
+#include <algorithm>
+#include <cmath>
 
-#include "misa_common.h"
-#include "misa_launch.h"
+#include "attn_device.h"
 
 namespace misa {
 
+hipError_t launch_attn_tile(const AttnArgs& a, const AttnLaunch& L, int D, bool fp8, int NW, hipStream_t st);
+hipError_t launch_attn_wave(const AttnArgs& a, const AttnLaunch& L, int D, bool fp8, int RT, hipStream_t st);
+
 namespace {
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttnPlan {
+  int RT = 0, wave_units = 0, wave_splits = 1;   // RT = 0: attn_wave does not run
+  int NW = 0, tile_units = 0, tile_splits = 1;   // NW = 0: attn_tile does not run
+  int rows_min = 0;
+  size_t wave_o = 0, wave_ml = 0, tile_o = 0, tile_ml = 0, total = 0;
+  int64_t groups = 0;   // workgroups of the larger launch
+};
+
+inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+AttnPlan make_plan(const misa_attn_shape& s, const misa_kv_pages& pg, int topk) {
+  AttnPlan p;
+  const int64_t G = s.n_heads / s.n_kv_heads, T = s.n_tokens, KH = s.n_kv_heads;
+  const int64_t ctx = topk > 0 ? topk : pg.max_pages * pg.page_keys;
+  if (T == 0) return p;
+  int64_t wave_units = 0, tile_units = 0;
+  if (topk > 0) {
+    if (G <= 32) {
+      p.RT = G <= 16 ? 1 : 2;
+      wave_units = T;
+    } else {
+      p.NW = G <= 64 ? 2 : 4;
+      tile_units = T * ((G + p.NW * 32 - 1) / (p.NW * 32));
+    }
+  } else {
+    const int64_t new_max = s.max_new > 0 ? std::min<int64_t>(s.max_new, T) : T;
+    const int64_t rows = new_max * G;
+    if (rows <= 32) {
+      p.RT = rows <= 16 ? 1 : 2;
+    } else {
+      // one sequence of many rows needs attn_tile alone
+      if (s.n_seq > 1 && G <= 32) p.RT = G <= 16 ? 1 : 2;
+      p.NW = rows <= 64 ? 2 : 4;
+    }
+    p.rows_min = 16 * p.RT;
+    if (p.RT > 0) wave_units = s.n_seq;
+    if (p.NW > 0) tile_units = T * G / (p.NW * 32) + std::min<int64_t>(s.n_seq, T * G / (p.rows_min + 1));
+  }
+  p.groups = std::max(wave_units, tile_units) * KH;
+  if (p.groups > ((int64_t)1 << 23)) return p;   // refused by the caller
+  p.wave_units = (int)wave_units;
+  p.tile_units = (int)tile_units;
+  // splits of at least 512 keys (by the widest the table allows), about 4
+  // workgroups to a CU of attn_wave and 2 of attn_tile, which is what its LDS
+  // lets stay resident
+  const int64_t most = std::max<int64_t>(1, (ctx + 511) / 512);
+  if (p.RT > 0) p.wave_splits = (int)std::clamp<int64_t>(1024 / (wave_units * KH), 1, std::min<int64_t>(64, most));
+  if (p.NW > 0) {
+    const int64_t BM = p.NW * 32;
+    const int64_t est = topk > 0 ? tile_units : (T * G + BM - 1) / BM;
+    p.tile_splits = (int)std::clamp<int64_t>(512 / (est * KH), 1, std::min<int64_t>(32, most));
+  }
+  p.groups = std::max(wave_units * p.wave_splits, tile_units * p.tile_splits) * KH;
+  size_t off = 0;
+  if (p.RT > 0 && p.wave_splits > 1) {
+    const size_t rows = (size_t)p.wave_units * KH * p.wave_splits * 16 * p.RT;
+    p.wave_o = off;
+    off += align_up(rows * s.head_dim * sizeof(float));
+    p.wave_ml = off;
+    off += align_up(rows * sizeof(float2));
+  }
+  if (p.NW > 0 && p.tile_splits > 1) {
+    const size_t rows = (size_t)p.tile_units * KH * p.tile_splits * 32 * p.NW;
+    p.tile_o = off;
+    off += align_up(rows * s.head_dim * sizeof(float));
+    p.tile_ml = off;
+    off += align_up(rows * sizeof(float2));
+  }
+  p.total = off;
+  return p;
+}
+
 }  // namespace
 
-// The pool row of token t of sequence b (entries clamped, see misa_kv_pages)
-__device__ __forceinline__ int64_t kv_row(const AttnArgs& a, int b, int t) {
-  const uint32_t p = (uint32_t)t / (uint32_t)a.page_keys;
-  int64_t e = a.table[(int64_t)b * a.max_pages + min((int64_t)p, a.max_pages - 1)];
-  e = e < 0 ? 0 : (e >= a.n_pages ? a.n_pages - 1 : e);
-  return e * a.page_keys + (t - (int64_t)p * a.page_keys);
+bool attn_fits(const misa_attn_shape& s, const misa_kv_pages& pg, int topk) {
+  return make_plan(s, pg, topk).groups <= ((int64_t)1 << 23);
 }
 
-template <bool FP8>
-__device__ __forceinline__ float kv_elem(const void* pool, int64_t i) {
-  if constexpr (FP8) return e4m3_to_f32(static_cast<const uint8_t*>(pool)[i]);
-  else return bf16_bits_to_f32(static_cast<const uint16_t*>(pool)[i]);
-}
-
-template <int D, bool FP8, bool SEL>
-__global__ void __launch_bounds__(kWave) k_attn_row(AttnArgs a) {
-  __shared__ float s_q[D];
-  const int64_t t = blockIdx.x;
-  const int h = blockIdx.y, g = h / (a.n_heads / a.n_kv_heads);
-  const int lane = threadIdx.x;
-  if (t >= a.q_start[a.n_seq]) return;
-  int lo = 0, hi = a.n_seq;   // last b with q_start[b] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.q_start[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  const int b = lo;
-  const int64_t len = min((int64_t)max(a.kv_lens[b], 0), a.max_pages * a.page_keys);
-  const int64_t pos = (int64_t)a.kv_lens[b] - (a.q_start[b + 1] - t);
-  const int n = (int)max((int64_t)0, min(len, pos + 1));   // visible keys: tokens 0 .. n-1
-  for (int d = lane; d < D; d += kWave) s_q[d] = bf16_bits_to_f32(a.q[t * a.q_st + h * a.q_sh + d]);
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, o[D / kWave] = {};
-  const int count = SEL ? a.topk : n;
-  for (int j0 = 0; j0 < count; j0 += kWave) {
-    const int j = j0 + lane;
-    int tok = SEL ? (j < count ? a.idx[t * a.topk + j] : -1) : j;
-    const bool seen = tok >= 0 && tok < n && j < count;
-    int64_t row = 0;
-    float s = -INFINITY, vs = 1.f;
-    if (seen) {
-      row = kv_row(a, b, tok) * a.n_kv_heads + g;
-      float acc = 0.f;
-      for (int d = 0; d < D; ++d) acc = __builtin_fmaf(s_q[d], kv_elem<FP8>(a.k, row * D + d), acc);
-      if (FP8) {
-        acc *= a.k_scale[row];
-        vs = a.v_scale[row];
-      }
-      s = acc * a.scale_log2;
-    }
-    float top = s;
-    for (int x = 32; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-    if (top == -INFINITY) continue;
-    const float mn = fmaxf(m, top), keep = exp2f(m - mn);
-    const float p = seen ? exp2f(s - mn) : 0.f;
-    float sum = p;
-    for (int x = 32; x >= 1; x >>= 1) sum += __shfl_xor(sum, x);
-    l = l * keep + sum;
-    m = mn;
-    for (int i = 0; i < D / kWave; ++i) o[i] *= keep;
-    const float pv = p * vs;
-    for (int x = 0; x < kWave; ++x) {
-      const float w = __shfl(pv, x);
-      const int64_t r = __shfl(row, x);
-      if (w == 0.f) continue;
-      for (int i = 0; i < D / kWave; ++i)
-        o[i] = __builtin_fmaf(w, kv_elem<FP8>(a.v, r * D + i * kWave + lane), o[i]);
-    }
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  for (int i = 0; i < D / kWave; ++i)
-    a.out[(t * a.n_heads + h) * D + i * kWave + lane] = (uint16_t)(pk_bf16(o[i] * inv, 0.f) & 0xFFFFu);
-  if (a.lse != nullptr && lane == 0) a.lse[t * a.n_heads + h] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-}
-
-size_t attn_workspace_bytes(const misa_attn_shape&, const misa_kv_pages&, int) { return 0; }
-
-template <int D, bool FP8>
-static void launch_rows(const AttnArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)a.n_tokens, (unsigned)a.n_heads);
-  if (a.idx != nullptr) hipLaunchKernelGGL((k_attn_row<D, FP8, true>), grid, dim3(kWave), 0, st, a);
-  else hipLaunchKernelGGL((k_attn_row<D, FP8, false>), grid, dim3(kWave), 0, st, a);
+size_t attn_workspace_bytes(const misa_attn_shape& s, const misa_kv_pages& pg, int topk) {
+  return make_plan(s, pg, topk).total;
 }
 
 hipError_t launch_attention(const misa_attn_shape& s, const misa_kv_pages& pg, const uint16_t* q,
                             const int32_t* q_start, const int32_t* kv_lens, const int32_t* idx, int topk,
                             uint16_t* out, float* lse, void* ws, hipStream_t st) {
+  const AttnPlan p = make_plan(s, pg, topk);
+  const bool pow2 = (pg.page_keys & (pg.page_keys - 1)) == 0;
   const AttnArgs a{q, s.q_stride_token, s.q_stride_head, pg.k, pg.v, pg.k_scale, pg.v_scale, pg.block_table,
-                   pg.max_pages, pg.n_pages, pg.page_keys, q_start, kv_lens, idx, topk, out, lse,
-                   s.scale * kLog2e, s.n_seq, s.n_heads, s.n_kv_heads, s.n_tokens};
+                   pg.max_pages, (int)pg.n_pages, pg.page_keys, pow2 ? __builtin_ctz((unsigned)pg.page_keys) : -1, q_start,
+                   kv_lens, idx, topk, out, lse, s.scale * 1.4426950408889634f, s.n_seq, s.n_heads, s.n_kv_heads,
+                   s.n_tokens};
   const bool fp8 = pg.kdtype == MISA_K_FP8_E4M3;
-  if (s.head_dim == 128) fp8 ? launch_rows<128, true>(a, st) : launch_rows<128, false>(a, st);
-  else fp8 ? launch_rows<64, true>(a, st) : launch_rows<64, false>(a, st);
-  return hipGetLastError();
+  char* base = static_cast<char*>(ws);
+  hipError_t e = hipSuccess;
+  if (p.NW > 0) {
+    const AttnLaunch L{p.tile_units, p.tile_splits, p.rows_min, reinterpret_cast<float*>(base + p.tile_o),
+                       reinterpret_cast<float2*>(base + p.tile_ml)};
+    e = launch_attn_tile(a, L, s.head_dim, fp8, p.NW, st);
+  }
+  if (e == hipSuccess && p.RT > 0) {
+    const AttnLaunch L{p.wave_units, p.wave_splits, p.rows_min, reinterpret_cast<float*>(base + p.wave_o),
+                       reinterpret_cast<float2*>(base + p.wave_ml)};
+    e = launch_attn_wave(a, L, s.head_dim, fp8, p.RT, st);
+  }
+  return e;
 }
 
 }  // namespace misa

@@ -184,8 +184,9 @@ struct AttnArgs {
   const void *k, *v;
   const float *k_scale, *v_scale;
   const int32_t* table;
-  int64_t max_pages, n_pages;
-  int page_keys;
+  int64_t max_pages;
+  int n_pages, page_keys;
+  int page_shift;       // log2 of page_keys where it is a power of two, else -1
   const int32_t *q_start, *kv_lens;
   const int32_t* idx;   // nullable: the selected tokens [n_tokens][topk]
   int topk;
@@ -195,7 +196,8 @@ struct AttnArgs {
   int n_seq, n_heads, n_kv_heads;
   int64_t n_tokens;
 };
-// topk = 0: over every visible key
+// topk = 0: over every visible key.  attn_fits: the launch's grid is in range.
+bool attn_fits(const misa_attn_shape& s, const misa_kv_pages& pg, int topk);
 size_t attn_workspace_bytes(const misa_attn_shape& s, const misa_kv_pages& pg, int topk);
 hipError_t launch_attention(const misa_attn_shape& s, const misa_kv_pages& pg, const uint16_t* q,
                             const int32_t* q_start, const int32_t* kv_lens, const int32_t* idx, int topk,

@@ -75,6 +75,7 @@ misa_status attention(const misa_attn_shape* s, const misa_kv_pages* p, const ui
                       const int32_t* kv_lens, const int32_t* idx, int32_t topk, uint16_t* out, float* lse, void* ws,
                       size_t ws_bytes, void* stream) {
   MISA_TRY(check_attn_pointers(p, q, q_start, kv_lens, out));
+  if (!misa::attn_fits(*s, *p, topk)) return MISA_ERR_UNSUPPORTED;
   const size_t need = misa::attn_workspace_bytes(*s, *p, topk);
   if (need > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < need)) return MISA_ERR_WORKSPACE;
   if (s->n_tokens == 0) return MISA_OK;
