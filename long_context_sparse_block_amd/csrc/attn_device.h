@@ -86,9 +86,9 @@ struct SeqSpan {
   int64_t pos0;
   int len;
 };
-__device__ __forceinline__ SeqSpan seq_span(const AttnArgs& a, int b) {
-  const int64_t s = a.q_start[b], e = a.q_start[b + 1], n = a.n_tokens;
-  const int64_t kv = max(a.kv_lens[b], 0);
+__device__ __forceinline__ SeqSpan make_span(const AttnArgs& a, int64_t s, int64_t e, int kv_len) {
+  const int64_t n = a.n_tokens;
+  const int64_t kv = max(kv_len, 0);
   SeqSpan r;
   const int64_t t0 = min(max(s, (int64_t)0), n);
   r.t0 = (int)t0;
@@ -97,20 +97,39 @@ __device__ __forceinline__ SeqSpan seq_span(const AttnArgs& a, int b) {
   r.len = (int)min(kv, a.max_pages * a.page_keys);
   return r;
 }
+__device__ __forceinline__ SeqSpan seq_span(const AttnArgs& a, int b) {
+  return make_span(a, a.q_start[b], a.q_start[b + 1], a.kv_lens[b]);
+}
 
-// The sequence of token t (q_start[0] <= t < q_start[n_seq]): 64 lanes probe at
-// a time.  Uniform.
-__device__ __forceinline__ int seq_of_token(const AttnArgs& a, int64_t t, int lane) {
+// The sequence of token t, its span, or false where t is no sequence's token.
+// Up to 64 sequences are looked over in one go, so that the search and the
+// span's own loads are one trip to memory; more are narrowed 64-fold at a time.
+// Uniform.
+__device__ __forceinline__ bool seq_of_token(const AttnArgs& a, int64_t t, int lane, int* b_out, SeqSpan* out) {
   int lo = 0, n = a.n_seq;   // the answer is in [lo, lo + n)
-  while (n > 1) {
-    const int step = (n + 63) / 64;
-    const int at = lo + lane * step;
-    const uint64_t m = __ballot(lane * step < n && a.q_start[min(at, a.n_seq)] <= t);
-    const int j = max(63 - (int)__builtin_clzll(m | 1), 0);   // last probe at or before t
+  while (n > kWave) {
+    const int step = (n + kWave - 1) / kWave;
+    const int at = lo + min(lane * step, n - 1);
+    const uint64_t m = __ballot(lane * step < n && a.q_start[at] <= t);
+    const int j = 63 - (int)__builtin_clzll(m | 1);   // last probe at or before t
     n = min(step, n - j * step);
     lo += j * step;
   }
-  return lo;
+  const int b = lo + min(lane, n - 1);
+  const int64_t s = a.q_start[b], e = a.q_start[b + 1];
+  const int kv = a.kv_lens[b];
+  const uint64_t m = __ballot(lane < n && s <= t && t < e);
+  if (m == 0) return false;
+  const int src = (int)__builtin_ctzll(m);
+  const int64_t s0 = __builtin_amdgcn_readlane((int)s, src), e0 = __builtin_amdgcn_readlane((int)e, src);
+  *b_out = lo + src;
+  *out = make_span(a, s0, e0, __builtin_amdgcn_readlane(kv, src));
+  return true;
+}
+
+// Entry j of token t's list, -1 behind its end
+__device__ __forceinline__ int pick(const AttnArgs& a, int64_t t, int j) {
+  return j < a.topk ? a.idx[t * a.topk + j] : -1;
 }
 
 // -scale is folded into the sign of q, so that a maximum of scores is a maximum
@@ -123,67 +142,173 @@ __device__ __forceinline__ bf16x8 load_q(const uint16_t* p, uint32_t flip) {
 // What a launch adds to the arguments
 struct AttnLaunch {
   int n_units;      // row tiles (attn_tile), or sequences / tokens (attn_wave)
-  int n_splits;     // key splits of a unit
+  int n_splits;     // key splits of a unit, at most
+  int slots;        // workgroups that the GPU holds at a time
   int rows_min;     // dense: attn_tile takes sequences with more rows than this, attn_wave the others
   float* part_o;    // n_splits > 1: unnormalised outputs [unit][kv head][split][row][D]
   float2* part_ml;  // and (maximum, sum) of each
+  int4* unit_info;  // dense attn_tile: (first token, first row, rows in all, splits in use) of each unit
 };
 
-// Dense row tiles of BM rows, numbered over the sequences with more than
-// rows_min rows: tile -> sequence and first row.  64 lanes take four sequences
-// each at a time.  False: no such tile.  Uniform.
-__device__ __forceinline__ bool find_tile(const AttnArgs& a, int G, int rows_min, int BM, int tile, int lane, int* b_out,
-                                          int* r0_out) {
+#ifndef ROUNDS
+#define ROUNDS 3
+#endif
+constexpr int kRounds = ROUNDS;
+// Sums over the sequences of a dense launch, for one kv head
+struct DenseScan {
+  float steps;   // key tiles of all units together
+  int units;
+  int longest;   // key tiles of one unit, at most
+};
+
+// Key tiles of a split.  Lengths differ within a batch, and a unit's share of
+// the splits should follow its own: all splits are equally long, three to each
+// workgroup that the GPU holds.  No splits where the units are one full round
+// of nearly equal length (they would only add rounds), or so many that they
+// balance by themselves.
+__device__ __forceinline__ int split_tiles(const DenseScan& w, const AttnLaunch& L, int kv_heads, int n, int least) {
+  if (w.units == 0) return (n + L.n_splits - 1) / L.n_splits;   // selected tokens, or no scan: even shares
+  const float fair = w.steps * (float)kv_heads / (float)L.slots;
+  const float units = (float)w.units * (float)kv_heads;
+  int p = max(least, (int)ceilf(fair * (1.f / kRounds)));
+  if (((float)w.longest <= 1.25f * fair && units <= 1.05f * (float)L.slots) || units >= 6.f * (float)L.slots)
+    p = max(p, w.longest);
+  return max(p, (n + L.n_splits - 1) / L.n_splits);
+}
+
+// Up to this many sequences a workgroup sums them all; more share their splits evenly
+constexpr int kScanSeqs = 4096;
+
+// Dense units.  TILES: row tiles of BM rows, numbered over the sequences with
+// more than rows_min rows; finds unit's sequence, span and first row (false: no
+// such tile).  Else unit is the sequence (false: not attn_wave's).  Fills
+// `scan` over the sequences of the launch's kind where splits need it.
+// Uniform.
+template <bool TILES, int KEYS>
+__device__ __forceinline__ bool find_unit(const AttnArgs& a, const AttnLaunch& L, int G, int BM, int unit, int lane,
+                                          SeqSpan* span, int* b_out, int* r0_out, DenseScan* scan) {
+  const bool sums = L.n_splits > 1 && a.n_seq <= kScanSeqs;
+  bool found = false;
   int64_t base = 0;
-  for (int b0 = 0; b0 < a.n_seq; b0 += 256) {
-    int c[4], sum = 0;
+  float steps = 0.f;
+  int longest = 0, units = 0;
+  const int first = TILES || sums ? 0 : unit / 256 * 256;
+  for (int b0 = first; b0 < a.n_seq; b0 += 256) {
+    int c[4], sum = 0, s[5], kv[4];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) s[i] = a.q_start[min(b0 + lane * 4 + i, a.n_seq)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) kv[i] = a.kv_lens[min(b0 + lane * 4 + i, a.n_seq - 1)];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int b = b0 + lane * 4 + i;
-      c[i] = 0;
-      if (b < a.n_seq) {
-        const int64_t n = a.n_tokens;
-        const int64_t t0 = min(max((int64_t)a.q_start[b], (int64_t)0), n);
-        const int64_t rows = max((int64_t)0, min((int64_t)a.q_start[b + 1], n) - t0) * G;
-        c[i] = rows > rows_min ? (int)((rows + BM - 1) / BM) : 0;
-      }
+      const SeqSpan sp = make_span(a, s[i], s[i + 1], kv[i]);
+      const int64_t rows = (int64_t)sp.m * G;
+      const bool in = b0 + lane * 4 + i < a.n_seq && rows > 0 && (rows > L.rows_min) == TILES;
+      c[i] = in ? (TILES ? (int)((rows + BM - 1) / BM) : 1) : 0;
       sum += c[i];
+      if (in) {
+        const int n = (sp.len + KEYS - 1) / KEYS;
+        steps += (float)c[i] * (float)n;
+        longest = max(longest, n);
+      }
     }
-    int inc = sum;
+    units += sum;
+    int src = -1, i = 0, left = 0;
+    if (TILES) {
+      int inc = sum;
 #pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-      const int x = __shfl_up(inc, o);
-      if (lane >= o) inc += x;
+      for (int o = 1; o < kWave; o <<= 1) {
+        const int x = __shfl_up(inc, o);
+        if (lane >= o) inc += x;
+      }
+      const int total = __builtin_amdgcn_readlane(inc, 63);
+      if (!found && unit < base + total) {
+        const int rel = (int)(unit - base);
+        src = (int)__builtin_ctzll(__ballot(inc > rel));
+        left = rel - (inc - sum);   // valid on lane src
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          if (i == k && left >= c[k]) {
+            left -= c[k];
+            i = k + 1;
+          }
+        i = __builtin_amdgcn_readlane(i, src);
+        left = __builtin_amdgcn_readlane(left, src);
+      }
+      base += total;
+    } else if (unit >= b0 && unit < b0 + 256) {
+      src = (unit - b0) / 4;
+      i = (unit - b0) % 4;
+      // not ours?  (c is 0 there)
+      int ci = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i == k) ci = c[k];
+      if (__builtin_amdgcn_readlane(ci, src) == 0) return false;
     }
-    const int total = __builtin_amdgcn_readlane(inc, 63);
-    if (tile < base + total) {
-      const int rel = (int)(tile - base);
-      const uint64_t m = __ballot(inc > rel);
-      const int src = (int)__builtin_ctzll(m);
-      int left = rel - (inc - sum), i = 0;   // valid on lane src
+    if (src >= 0) {
+      int si = 0, ei = 0, ki = 0;
 #pragma unroll
-      for (int k = 0; k < 3; ++k)
-        if (i == k && left >= c[k]) {
-          left -= c[k];
-          i = k + 1;
+      for (int k = 0; k < 4; ++k)
+        if (i == k) {
+          si = s[k];
+          ei = s[k + 1];
+          ki = kv[k];
         }
-      *b_out = b0 + src * 4 + __builtin_amdgcn_readlane(i, src);
-      *r0_out = __builtin_amdgcn_readlane(left, src) * BM;
-      return true;
+      *span = make_span(a, __builtin_amdgcn_readlane(si, src), __builtin_amdgcn_readlane(ei, src),
+                        __builtin_amdgcn_readlane(ki, src));
+      *b_out = b0 + src * 4 + i;
+      *r0_out = left * BM;
+      found = true;
     }
-    base += total;
+    if (found && !sums) break;
   }
-  return false;
+  if (!found) return false;
+  if (sums) {
+#pragma unroll
+    for (int x = 32; x >= 1; x >>= 1) {
+      steps += __shfl_xor(steps, x);
+      longest = max(longest, __shfl_xor(longest, x));
+      units += __shfl_xor(units, x);
+    }
+    *scan = DenseScan{steps, units, longest};
+  } else {
+    *scan = DenseScan{0.f, 0, 0};
+  }
+  return true;
+}
+
+// Workgroup -> (unit, kv head, split).  Workgroup i runs on XCD i mod 8, and the
+// units of one (kv head, split) read the same keys: where there are a
+// multiple of 8 such pairs, each goes to one XCD, whose L2 then holds the keys
+// for all its units; else neighbours go round the XCDs.
+struct Place {
+  int unit, g, split;
+};
+__device__ __forceinline__ Place place_of(const AttnLaunch& L, int kv_heads, uint32_t i) {
+  const uint32_t n = (uint32_t)L.n_units, pairs = (uint32_t)(kv_heads * L.n_splits);
+  uint32_t pair, unit;
+  if (pairs % 8 == 0) {
+    const uint32_t j = i / 8;
+    pair = i % 8 + 8 * (j / n);
+    unit = j % n;
+  } else {
+    pair = i / n;
+    unit = i % n;
+  }
+  return Place{(int)unit, (int)(pair % (uint32_t)kv_heads), (int)(pair / (uint32_t)kv_heads)};
 }
 
 // The splits of one output row: partial rows pr, pr + step, ...; out_row is the
-// row of out and lse.  Lane s holds split s's weight, then every lane D / 64
-// output elements.  Fixed order.
+// row of out and lse.  Lane s first holds split s's weight; then D / 4 lanes
+// read a split's row, 16 bytes each, and the wave's groups of such lanes take
+// the splits in turn.  Fixed order.
 template <int D>
-__device__ __forceinline__ void join_row(const AttnArgs& a, const AttnLaunch& L, int64_t pr, int64_t step, int64_t out_row,
-                                         int lane) {
+__device__ __forceinline__ void join_row(const AttnArgs& a, const AttnLaunch& L, int n_splits, int64_t pr, int64_t step,
+                                         int64_t out_row, int lane) {
+  constexpr int LR = D / 4, kGroups = kWave / LR;
   float2 ml = make_float2(-INFINITY, 0.f);
-  if (lane < L.n_splits) ml = L.part_ml[pr + lane * step];
+  if (lane < n_splits) ml = L.part_ml[pr + lane * step];
   float top = ml.y > 0.f ? ml.x : -INFINITY;
 #pragma unroll
   for (int x = 32; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
@@ -191,19 +316,24 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, const AttnLaunch& L,
   float sum = w * ml.y;
 #pragma unroll
   for (int x = 32; x >= 1; x >>= 1) sum += __shfl_xor(sum, x);
-  constexpr int E = D / kWave;
-  float o[E] = {};
-  for (int s = 0; s < L.n_splits; ++s) {
-    const float ws = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), s));
-    if (ws == 0.f) continue;   // an empty split wrote no output
-    const float* src = L.part_o + (pr + s * step) * D + lane * E;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s0 = 0; s0 < n_splits; s0 += kGroups) {
+    const int s = min(s0 + lane / LR, n_splits - 1);
+    const float ws = s0 + lane / LR < n_splits ? __shfl(w, s) : 0.f;
+    const f32x4 v = *reinterpret_cast<const f32x4*>(L.part_o + (pr + s * step) * D + (lane % LR) * 4);
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(ws, src[e], o[e]);
+    for (int e = 0; e < 4; ++e)   // an empty split wrote no output: whatever is there is not used
+      o[e] = ws == 0.f ? o[e] : __builtin_fmaf(ws, v[e], o[e]);
   }
+#pragma unroll
+  for (int x = LR; x < kWave; x <<= 1)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], x);
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  uint16_t* dst = a.out + out_row * D + lane * E;
-  if constexpr (E == 2) *reinterpret_cast<uint32_t*>(dst) = pk_bf16(o[0] * inv, o[1] * inv);
-  else dst[0] = (uint16_t)(pk_bf16(o[0] * inv, 0.f) & 0xFFFFu);
+  if (lane < LR)
+    *reinterpret_cast<uint2*>(a.out + out_row * D + lane * 4) =
+        make_uint2(pk_bf16(o[0] * inv, o[1] * inv), pk_bf16(o[2] * inv, o[3] * inv));
   if (a.lse != nullptr && lane == 0) a.lse[out_row] = sum > 0.f ? (top + __log2f(sum)) * kLn2 : -INFINITY;
 }
 

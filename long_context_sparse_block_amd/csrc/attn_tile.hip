@@ -11,7 +11,14 @@
 
 namespace misa {
 
+#ifndef KSCHED
+#define KSCHED 11
+#endif
+#ifndef LEAST
+#define LEAST 8
+#endif
 namespace {
+constexpr int kSched = KSCHED;
 constexpr int kBN = 64;          // keys of a tile
 constexpr float kGrow = 8.f;     // log2 of the growth that forces a rescale
 
@@ -26,7 +33,7 @@ struct Fp8Stage {
 }  // namespace
 
 template <int D, bool FP8, bool SEL, int NW>
-__global__ void __launch_bounds__(NW * kWave, 2) k_attn_tile(const AttnArgs a, const AttnLaunch L) {
+__global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const AttnArgs a, const AttnLaunch L) {
   constexpr int NT = NW * kWave, BM = NW * 32;
   constexpr int RB = D * 2;            // bytes of a bf16 row
   constexpr int P = D / 8;             // its 16-byte pieces
@@ -34,6 +41,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_tile(const AttnArgs a, c
   constexpr int kLoads = kBN / RPI / NW;
   constexpr int KS = D / 16;           // MFMA steps of a dot product
   constexpr int DB = D / 32;           // 32-wide blocks of the output
+  constexpr int PC = D / 16;           // 16-byte pieces of a row of e4m3 codes
   __shared__ __attribute__((aligned(16))) unsigned char s_k0[kBN * RB], s_k1[kBN * RB], s_v0[kBN * RB], s_v1[kBN * RB];
   __shared__ __attribute__((aligned(16))) float s_ks0[kBN], s_ks1[kBN], s_vs0[kBN], s_vs1[kBN];
 
@@ -42,40 +50,65 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_tile(const AttnArgs a, c
   const int h = lane >> 5, c32 = lane & 31;
   const int G = a.n_heads / a.n_kv_heads;
 
-  // unit order: kv head, split, row tile (an XCD then walks row tiles of the
-  // same keys), the tiles with the longest prefixes first
-  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
-  const int rest = (int)(id / L.n_units);
-  int unit = (int)(id % L.n_units);
-  const int split = rest % L.n_splits, g = rest / L.n_splits;
+#ifdef PRIO
+  {
+    const int slot = __builtin_amdgcn_s_getreg(4 | (0 << 6) | (3 << 11));
+    if (PRIO == 1) { if (slot & 1) __builtin_amdgcn_s_setprio(1); }
+    if (PRIO == 2) { if (slot & 1) __builtin_amdgcn_s_setprio(3); }
+    if (PRIO == 3) { if (slot == 1) __builtin_amdgcn_s_setprio(1); else if (slot == 2) __builtin_amdgcn_s_setprio(2); else if (slot >= 3) __builtin_amdgcn_s_setprio(3); }
+  }
+#endif
+  const Place at = place_of(L, a.n_kv_heads, blockIdx.x);
+  const int split = at.split, g = at.g;
+  int unit = at.unit;
   int b, r0, nrows, tok0;      // sequence, first row, its rows in all, its first token
   int64_t pos0;                // position of tok0
   int kend, kfull;             // keys some row sees, keys every row sees
+  int jt0, jt1;                // the tiles of this split
+  int in_use = 1;              // its unit's splits in use
+  auto range = [&](const DenseScan& w) {
+    const int n = (kend + kBN - 1) / kBN;
+    const int per = max(1, L.n_splits == 1 ? n : split_tiles(w, L, a.n_kv_heads, n, LEAST));
+    in_use = max(1, (n + per - 1) / per);
+    jt0 = split * per;
+    jt1 = min(n, jt0 + per);
+  };
+  int pick0 = 0, pick1 = 0, pick2 = 0;   // SEL: this lane's listed tokens of the first three tiles
   if (SEL) {
     const int sub = (G + BM - 1) / BM;
     tok0 = unit / sub;
     r0 = (unit % sub) * BM;
-    if (tok0 >= a.q_start[a.n_seq] || tok0 < a.q_start[0]) return;
-    b = seq_of_token(a, tok0, lane);
-    const SeqSpan sp = seq_span(a, b);
     nrows = G;
+    kend = a.topk;
+    range(DenseScan{0.f, 0, 0});
+    // on their way while the sequence is looked up
+    pick0 = pick(a, tok0, jt0 * kBN + lane);
+    pick1 = pick(a, tok0, jt0 * kBN + kBN + lane);
+    pick2 = pick(a, tok0, jt0 * kBN + 2 * kBN + lane);
+    SeqSpan sp;
+    if (!seq_of_token(a, tok0, lane, &b, &sp)) return;
     pos0 = sp.pos0 + (tok0 - sp.t0);
     kfull = (int)max((int64_t)0, min((int64_t)sp.len, pos0 + 1));   // tokens the row may list
-    kend = kfull > 0 ? a.topk : 0;
+    if (kfull == 0) jt1 = jt0;
   } else {
-    unit = L.n_units - 1 - unit;
-    if (!find_tile(a, G, L.rows_min, BM, unit, lane, &b, &r0)) return;
-    const SeqSpan sp = seq_span(a, b);
+    unit = L.n_units - 1 - unit;   // the longest prefixes of a prompt first
+    SeqSpan sp;
+    DenseScan scan;
+    const bool tell = L.n_splits > 1 && split == 0 && g == 0 && tid == 0;   // the join's directions
+    if (!find_unit<true, kBN>(a, L, G, BM, unit, lane, &sp, &b, &r0, &scan)) {
+      if (tell) L.unit_info[unit] = make_int4(0, 0, 0, 0);
+      return;
+    }
     tok0 = sp.t0;
     nrows = sp.m * G;
     pos0 = sp.pos0;
     const int last = (min(r0 + BM, nrows) - 1) / G, first = r0 / G;
     kend = (int)max((int64_t)0, min((int64_t)sp.len, pos0 + last + 1));
     kfull = (int)max((int64_t)0, min((int64_t)sp.len, pos0 + first + 1));
+    range(scan);
+    if (tell) L.unit_info[unit] = make_int4(tok0, r0, nrows, in_use);
+    if (split >= in_use) return;
   }
-  const int n_tiles_all = (kend + kBN - 1) / kBN;
-  const int per = (n_tiles_all + L.n_splits - 1) / L.n_splits;
-  const int jt0 = split * per, jt1 = min(n_tiles_all, jt0 + per);
 
   // this lane's query row (rows past the end repeat the last one and are not written)
   const int r = r0 + wave * 32 + c32;
@@ -95,53 +128,62 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_tile(const AttnArgs a, c
   // Staging.  Lane k of every wave looks up key k of a tile two tiles ahead:
   // the listed token (SEL) three tiles ahead, its table entry two, so that no
   // load is waited for in the iteration that issues it.
-  const int64_t row_stride = (int64_t)a.n_kv_heads * D;   // elements of a pool row
   auto token_at = [&](int jt) -> int {
     const int j = jt * kBN + lane;
-    if (SEL) return j < a.topk ? a.idx[qrow * a.topk + j] : -1;
-    return min(j, kend - 1);
+    return SEL ? pick(a, tok0, j) : min(j, kend - 1);
   };
   auto clamp_tok = [&](int t) -> int { return SEL ? (t >= 0 && t < kfull ? t : 0) : t; };
-  int tok_n = 0, ent_n = 0;       // tile in flight: token, table entry
-  int row_c = 0;                  // pool row of the next tile's key `lane`
-  uint64_t mask_n = ~0ull, mask_c = ~0ull;
-  Fp8Stage<D, NT> st;
-
-  auto issue = [&](unsigned char* dk, unsigned char* dv) {   // tile of row_c
-    if constexpr (!FP8) {
+  using Stage = Fp8Stage<D, NT>;
+  // Lane k of every wave knows where key k's pool row starts (bytes); a load's
+  // lanes fetch that from the lane of their row.  Which piece of the row a lane
+  // moves is the same for all its loads where their rows are 16 apart (every
+  // other one where they are 8 apart), so the rest of the address is fixed.
+  const int64_t row_bytes = (int64_t)a.n_kv_heads * D * (FP8 ? 1 : 2);
+  const int lrow = FP8 ? tid / PC : wave * RPI + lane / P;   // row of the first load
+  const int lpiece = FP8 ? tid % PC : (lane % P) ^ swizzle<D>(lrow);
+  const char* const kl = static_cast<const char*>(a.k) + g * D * (FP8 ? 1 : 2) + lpiece * 16;
+  const char* const vl = static_cast<const char*>(a.v) + g * D * (FP8 ? 1 : 2) + lpiece * 16;
+  constexpr int kStepRows = FP8 ? NT / PC : NW * RPI;        // rows between a lane's loads
+  static_assert(kStepRows % 16 == 0 || (kStepRows == 8 && !FP8), "a lane's piece and its place in LDS repeat");
+  const int lodd = kStepRows % 16 == 0 ? 0 : (((lane % P) ^ swizzle<D>(lrow + 8)) - lpiece) * 16;   // of odd loads
+  auto fetch = [&](int64_t off, int from) -> int64_t {
+    const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)off, from), hi = (uint32_t)__shfl((int)(off >> 32), from);
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+  };
+  // a tile towards LDS: bf16 straight there, e4m3 codes into registers, from
+  // which land() widens them
+  auto issue = [&](int row_of, unsigned char* dk, unsigned char* dv, Stage& st) {
+    const int64_t mine = (int64_t)row_of * row_bytes;
+    constexpr int N = FP8 ? Stage::kLoads : kLoads;
+    int64_t off[N];
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u) {
-        const int base = (u * NW + wave) * RPI;
-        const int row = base + lane / P;
-        const int64_t off = ((int64_t)__shfl(row_c, row) * row_stride + g * D) * 2 + ((lane % P) ^ swizzle<D>(row)) * 16;
-        load_lds16(static_cast<const char*>(a.k) + off, dk + base * RB);
-        load_lds16(static_cast<const char*>(a.v) + off, dv + base * RB);
-      }
-    } else {
-      constexpr int PC = Fp8Stage<D, NT>::kPieces;
+    for (int u = 0; u < N; ++u) off[u] = fetch(mine, (lrow + u * kStepRows) & 63) + (kStepRows == 8 && (u & 1) ? lodd : 0);
 #pragma unroll
-      for (int u = 0; u < Fp8Stage<D, NT>::kLoads; ++u) {
-        const int i = u * NT + tid;
-        const int64_t off = (int64_t)__shfl(row_c, i / PC) * row_stride + g * D + (i % PC) * 16;
-        st.k[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.k) + off);
-        st.v[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.v) + off);
+    for (int u = 0; u < N; ++u) {
+      if constexpr (!FP8) {
+        load_lds16(kl + off[u], dk + (u * NW + wave) * RPI * RB);
+        load_lds16(vl + off[u], dv + (u * NW + wave) * RPI * RB);
+      } else {
+        st.k[u] = *reinterpret_cast<const uint4*>(kl + off[u]);
+        st.v[u] = *reinterpret_cast<const uint4*>(vl + off[u]);
       }
-      if (wave == 0) st.scale = a.k_scale[(int64_t)row_c * a.n_kv_heads + g];
-      if (wave == NW - 1 && wave != 0) st.scale = a.v_scale[(int64_t)row_c * a.n_kv_heads + g];
+    }
+    if constexpr (FP8) {
+      if (wave == 0) st.scale = a.k_scale[(int64_t)row_of * a.n_kv_heads + g];
+      if (wave == NW - 1 && wave != 0) st.scale = a.v_scale[(int64_t)row_of * a.n_kv_heads + g];
     }
   };
-  auto land = [&](unsigned char* dk, unsigned char* dv, float* dks, float* dvs) {   // FP8: registers -> LDS
+  const int lf = swizzle<D>(lrow);
+  const int land0 = lrow * RB + (((2 * lpiece) ^ lf) << 4), land1 = lrow * RB + (((2 * lpiece + 1) ^ lf) << 4);
+  auto land = [&](const Stage& st, unsigned char* dk, unsigned char* dv, float* dks, float* dvs) {
     if constexpr (FP8) {
-      constexpr int PC = Fp8Stage<D, NT>::kPieces;
 #pragma unroll
-      for (int u = 0; u < Fp8Stage<D, NT>::kLoads; ++u) {
-        const int i = u * NT + tid, row = i / PC, c = 2 * (i % PC);
-        const int f = swizzle<D>(row);
+      for (int u = 0; u < Stage::kLoads; ++u) {
         auto put = [&](unsigned char* d, uint4 x) {
           const uint2 w0 = e4m3x4_to_bf16x4(x.x), w1 = e4m3x4_to_bf16x4(x.y);
           const uint2 w2 = e4m3x4_to_bf16x4(x.z), w3 = e4m3x4_to_bf16x4(x.w);
-          *reinterpret_cast<uint4*>(d + row * RB + ((c ^ f) << 4)) = make_uint4(w0.x, w0.y, w1.x, w1.y);
-          *reinterpret_cast<uint4*>(d + row * RB + (((c + 1) ^ f) << 4)) = make_uint4(w2.x, w2.y, w3.x, w3.y);
+          *reinterpret_cast<uint4*>(d + u * kStepRows * RB + land0) = make_uint4(w0.x, w0.y, w1.x, w1.y);
+          *reinterpret_cast<uint4*>(d + u * kStepRows * RB + land1) = make_uint4(w2.x, w2.y, w3.x, w3.y);
         };
         put(dk, st.k[u]);
         put(dv, st.v[u]);
@@ -183,6 +225,15 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_tile(const AttnArgs a, c
         const bf16x8 kf = as_bf16x8(*reinterpret_cast<const uint4*>(sk + kb * 32 * RB + (k_base ^ (ks << 5))));
         s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[ks], s[kb], 0, 0, 0);
       }
+    }
+    if (kSched & 1) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+#pragma unroll
+      for (int i = 0; i < 2 * KS - 6; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x8, 6, 0);
     }
     // key of s[kb][4 j + i]: kb 32 + 8 j + 4 h + i
     if constexpr (FP8) {
@@ -252,54 +303,95 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_tile(const AttnArgs a, c
         pf[2 * kb + q] = as_bf16x8(make_uint4(pk_bf16(p[8 * q], p[8 * q + 1]), pk_bf16(p[8 * q + 2], p[8 * q + 3]),
                                               pk_bf16(p[8 * q + 4], p[8 * q + 5]), pk_bf16(p[8 * q + 6], p[8 * q + 7])));
     }
+    if (kSched & 8) __builtin_amdgcn_sched_barrier(0);
+    if (kSched & 4) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int db = 0; db < DB; ++db) {
-      const int x = (db ^ vx) << 6;
+    for (int t = 0; t < 4; ++t) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int db = 0; db < DB; ++db) {
+        const int x = (db ^ vx) << 6;
         const uint2 lo = lds_read_tr(sv + t * 16 * RB + v_base[0] + x), hi = lds_read_tr(sv + t * 16 * RB + v_base[1] + x);
         o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y)), pf[t], o[db], 0, 0, 0);
       }
     }
+    if (kSched & 4) __builtin_amdgcn_s_setprio(0);
+    if (kSched & 2) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+      for (int i = 0; i < 4 * DB - 4; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x8, 4, 0);
+    }
   };
 
   if (jt0 < jt1) {
-    // first tile's rows, second tile's entries, third tile's tokens
     const int last = jt1 - 1;
-    int t = token_at(jt0);
-    if (SEL) mask_n = __ballot(t >= 0 && t < kfull);
-    t = clamp_tok(t);
-    row_c = pool_row(a, table_entry(a, b, t), t);
-    uint64_t mask_first = mask_n;
-    issue(s_k0, s_v0);
-    land(s_k0, s_v0, s_ks0, s_vs0);
-    tok_n = token_at(min(jt0 + 1, last));
-    if (SEL) mask_n = __ballot(tok_n >= 0 && tok_n < kfull);
-    tok_n = clamp_tok(tok_n);
-    ent_n = table_entry(a, b, tok_n);
-    int tok_nn = token_at(min(jt0 + 2, last));
-    mask_c = mask_first;
-    auto step = [&](int jt, unsigned char* ck, unsigned char* cv, float* cks, float* cvs, unsigned char* nk,
-                    unsigned char* nv, float* nks, float* nvs) {
-      __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();   // tile jt is in LDS, and nobody reads the other buffer any more
-      const bool more = jt + 1 < jt1;
-      const uint64_t mask_next = mask_n;
-      if (more) {
-        row_c = pool_row(a, ent_n, tok_n);
-        issue(nk, nv);
-        if (SEL) mask_n = __ballot(tok_nn >= 0 && tok_nn < kfull);
-        tok_n = clamp_tok(tok_nn);
-        ent_n = table_entry(a, b, tok_n);
-        tok_nn = token_at(min(jt + 3, last));
-      }
-      compute(ck, cv, cks, cvs, jt, mask_c);
-      if (more) land(nk, nv, nks, nvs);
-      mask_c = mask_next;
+    auto look = [&](int t, uint64_t& mask) -> int {
+      if (SEL) mask = __ballot(t >= 0 && t < kfull);
+      return clamp_tok(t);
     };
-    for (int jt = jt0; jt < jt1; jt += 2) {
-      step(jt, s_k0, s_v0, s_ks0, s_vs0, s_k1, s_v1, s_ks1, s_vs1);
-      if (jt + 1 < jt1) step(jt + 1, s_k1, s_v1, s_ks1, s_vs1, s_k0, s_v0, s_ks0, s_vs0);
+    uint64_t m0 = ~0ull, m1 = ~0ull, m2 = ~0ull;   // of this tile and the next two
+    const int t0 = look(SEL ? pick0 : token_at(jt0), m0);
+    const int t1 = look(SEL ? pick1 : token_at(min(jt0 + 1, last)), m1);
+    const int e0 = table_entry(a, b, t0), e1 = table_entry(a, b, t1);
+    if constexpr (!FP8) {
+      // One tile ahead, straight into the other buffer; look-ups run a tile
+      // further ahead each (the table entry, then the listed token).
+      Stage none;
+      issue(pool_row(a, e0, t0), s_k0, s_v0, none);
+      int tok_n = t1, ent_n = e1, tok_nn = SEL ? pick2 : token_at(min(jt0 + 2, last));
+      auto step = [&](int jt, const unsigned char* ck, const unsigned char* cv, unsigned char* nk, unsigned char* nv) {
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();   // tile jt is in LDS, and nobody reads the other buffer any more
+        if (jt + 1 < jt1) {
+          issue(pool_row(a, ent_n, tok_n), nk, nv, none);
+          tok_n = look(tok_nn, m2);
+          ent_n = table_entry(a, b, tok_n);
+          tok_nn = token_at(min(jt + 3, last));
+        }
+        compute(ck, cv, s_ks0, s_vs0, jt, m0);
+        m0 = m1;
+        m1 = m2;
+      };
+      for (int jt = jt0; jt < jt1; jt += 2) {
+        step(jt, s_k0, s_v0, s_k1, s_v1);
+        if (jt + 1 < jt1) step(jt + 1, s_k1, s_v1, s_k0, s_v0);
+      }
+    } else {
+      // Codes two tiles ahead in registers, widened into the other buffer after
+      // the tile before is done with.  Loads return in order, so a step's
+      // look-ups go out before its codes: waiting for them then waits for no
+      // codes but the oldest.
+      Stage sa, sb;
+      int tok_n = look(SEL ? pick2 : token_at(min(jt0 + 2, last)), m2);
+      int ent_n = table_entry(a, b, tok_n);
+      int tok_nn = token_at(min(jt0 + 3, last));
+      issue(pool_row(a, e0, t0), nullptr, nullptr, sa);
+      issue(pool_row(a, e1, t1), nullptr, nullptr, sb);
+      land(sa, s_k0, s_v0, s_ks0, s_vs0);
+      auto step = [&](int jt, const unsigned char* ck, const unsigned char* cv, const float* cks, const float* cvs,
+                      unsigned char* nk, unsigned char* nv, float* nks, float* nvs, Stage& free, const Stage& next) {
+        __syncthreads();   // tile jt is in LDS, and nobody reads the other buffer any more
+        uint64_t m3 = ~0ull;
+        if (jt + 2 < jt1) {
+          const int row = pool_row(a, ent_n, tok_n);
+          tok_n = look(tok_nn, m3);
+          ent_n = table_entry(a, b, tok_n);
+          tok_nn = token_at(min(jt + 4, last));
+          issue(row, nullptr, nullptr, free);
+        }
+        compute(ck, cv, cks, cvs, jt, m0);
+        if (jt + 1 < jt1) land(next, nk, nv, nks, nvs);
+        m0 = m1;
+        m1 = m2;
+        m2 = m3;
+      };
+      for (int jt = jt0; jt < jt1; jt += 2) {
+        step(jt, s_k0, s_v0, s_ks0, s_vs0, s_k1, s_v1, s_ks1, s_vs1, sa, sb);
+        if (jt + 1 < jt1) step(jt + 1, s_k1, s_v1, s_ks1, s_vs1, s_k0, s_v0, s_ks0, s_vs0, sb, sa);
+      }
     }
   }
 
@@ -330,33 +422,31 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_tile(const AttnArgs a, c
   }
 }
 
-// The splits of a row joined: one wave a row, lane s first holds split s's
-// (maximum, sum), then D / 64 output elements.  Fixed order, so the same call
-// gives the same bits.
+// The splits of a unit's rows joined, a row a wave
 template <int D, bool SEL>
 __global__ void __launch_bounds__(256) k_attn_tile_join(const AttnArgs a, const AttnLaunch L, int BM) {
   const int lane = threadIdx.x & 63;
   const int unit = blockIdx.x, g = blockIdx.y;
   const int G = a.n_heads / a.n_kv_heads;
-  const int rr = blockIdx.z * 4 + (threadIdx.x >> 6);   // row of the tile
-  int b, r0, nrows, tok0;
+  int r0, nrows, tok0, n_splits = L.n_splits;
   if (SEL) {
     const int sub = (G + BM - 1) / BM;
     tok0 = unit / sub;
     r0 = (unit % sub) * BM;
-    if (tok0 >= a.q_start[a.n_seq] || tok0 < a.q_start[0]) return;
+    if (tok0 >= a.q_start[a.n_seq] || tok0 < a.q_start[0]) return;   // no sequence's token: nothing was written
     nrows = G;
   } else {
-    if (!find_tile(a, G, L.rows_min, BM, unit, lane, &b, &r0)) return;
-    const SeqSpan sp = seq_span(a, b);
-    tok0 = sp.t0;
-    nrows = sp.m * G;
+    const int4 u = L.unit_info[unit];
+    tok0 = u.x;
+    r0 = u.y;
+    nrows = u.z;
+    n_splits = u.w;
   }
-  const int r = r0 + rr;
+  const int rr = blockIdx.z * 4 + (threadIdx.x >> 6), r = r0 + rr;
   if (r >= nrows) return;
   const int qi = SEL ? 0 : r / G, qh = g * G + (SEL ? r : r - qi * G);
-  join_row<D>(a, L, (((int64_t)unit * a.n_kv_heads + g) * L.n_splits) * BM + rr, BM, ((int64_t)tok0 + qi) * a.n_heads + qh,
-              lane);
+  join_row<D>(a, L, n_splits, (((int64_t)unit * a.n_kv_heads + g) * L.n_splits) * BM + rr, BM,
+              ((int64_t)tok0 + qi) * a.n_heads + qh, lane);
 }
 
 template <int D, bool FP8, bool SEL>

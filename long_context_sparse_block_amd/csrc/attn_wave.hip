@@ -41,35 +41,53 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 ? 2 : 1) k_attn_wave(const
   const int g4 = lane >> 4, c16 = lane & 15;
   const int G = a.n_heads / a.n_kv_heads;
 
-  // unit order: kv head, unit, split
-  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
-  const int split = (int)(id % L.n_splits);
-  const int64_t rest = id / L.n_splits;
-  const int unit = (int)(rest % L.n_units), g = (int)(rest / L.n_units);
-  int b, tok0, nrows, kend, kfull;
+  const Place at = place_of(L, a.n_kv_heads, blockIdx.x);
+  const int split = at.split, g = at.g, unit = at.unit;
+  int b, tok0, nrows, kend, kfull;   // sequence, first token, rows; keys some row sees, keys every row sees
   int64_t pos0;
+  int jt0, jt1;                      // this wave's tiles: jt0, jt0 + 4, ... below jt1
+  int in_use = 1;                    // the unit's splits in use
+  auto range = [&](const DenseScan& w) {
+    const int n = (kend + kWT - 1) / kWT;
+    const int per = max(1, L.n_splits == 1 ? n : split_tiles(w, L, a.n_kv_heads, n, 4 * kWaves));
+    in_use = max(1, (n + per - 1) / per);
+    jt0 = split * per + wave;
+    jt1 = min(n, (split + 1) * per);
+  };
+  const int k32 = lane & 31;
+  int pick0 = 0, pick1 = 0, pick2 = 0, pick3 = 0;   // SEL: this lane's listed tokens of the first tiles
   if (SEL) {
     tok0 = unit;
-    if (tok0 >= a.q_start[a.n_seq] || tok0 < a.q_start[0]) return;
-    b = seq_of_token(a, tok0, lane);
-    const SeqSpan sp = seq_span(a, b);
     nrows = G;
+    kend = a.topk;
+    range(DenseScan{0.f, 0, 0});
+    // on their way while the sequence is looked up
+    pick0 = pick(a, tok0, jt0 * kWT + k32);
+    pick1 = pick(a, tok0, (jt0 + kWaves) * kWT + k32);
+    pick2 = pick(a, tok0, (jt0 + 2 * kWaves) * kWT + k32);
+    pick3 = pick(a, tok0, (jt0 + 3 * kWaves) * kWT + k32);
+    SeqSpan sp;
+    if (!seq_of_token(a, tok0, lane, &b, &sp)) return;
     pos0 = sp.pos0 + (tok0 - sp.t0);
     kfull = (int)max((int64_t)0, min((int64_t)sp.len, pos0 + 1));   // tokens the row may list
-    kend = kfull > 0 ? a.topk : 0;
+    if (kfull == 0) jt1 = jt0;
   } else {
-    b = unit;
-    const SeqSpan sp = seq_span(a, b);
-    if (sp.m == 0 || (int64_t)sp.m * G > L.rows_min) return;
+    SeqSpan sp;
+    DenseScan scan;
+    int none;
+    if (!find_unit<false, kWT>(a, L, G, 1, unit, lane, &sp, &b, &none, &scan)) return;
     tok0 = sp.t0;
     nrows = sp.m * G;
     pos0 = sp.pos0;
     kend = (int)max((int64_t)0, min((int64_t)sp.len, pos0 + sp.m));
     kfull = (int)max((int64_t)0, min((int64_t)sp.len, pos0 + 1));
+    range(scan);
+    if (split >= in_use) {   // the join finds an empty split
+      const int64_t part = (((int64_t)unit * a.n_kv_heads + g) * L.n_splits + split) * ROWS;
+      if (tid < nrows) L.part_ml[part + tid] = make_float2(-INFINITY, 0.f);
+      return;
+    }
   }
-  const int n_tiles = (kend + kWT - 1) / kWT;
-  const int per = (n_tiles + L.n_splits - 1) / L.n_splits;
-  const int jt0 = split * per + wave, jt1 = min(n_tiles, (split + 1) * per);
 
   int vis[RT];
   bf16x8 qf[RT][KS];
@@ -89,39 +107,44 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 ? 2 : 1) k_attn_wave(const
   unsigned char* const kb_ = s_b + (FP8 ? 0 : wave * 2 * kTile);
   float* const sks = s_sc + (FP8 ? wave * 2 * kWT : 0);
   const int64_t row_stride = (int64_t)a.n_kv_heads * D;
-  const int k32 = lane & 31;
   auto token_at = [&](int jt) -> int {
     const int j = jt * kWT + k32;
-    if (SEL) return j < a.topk ? a.idx[(int64_t)tok0 * a.topk + j] : -1;
-    return min(j, kend - 1);
+    return SEL ? pick(a, tok0, j) : min(j, kend - 1);
   };
   auto seen = [&](int t) -> bool { return t >= 0 && t < kfull; };
   auto clamp_tok = [&](int t) -> int { return SEL ? (seen(t) ? t : 0) : t; };
 
-  uint4 r8k[FP8 ? kLoads8 : 1], r8v[FP8 ? kLoads8 : 1];
-  float r8s = 1.f;
-  int row_c = 0;
-  auto issue = [&](unsigned char* dst) {   // tile of row_c: K, then V
+  // a tile's K and V towards LDS: bf16 straight there, e4m3 codes into
+  // registers, from which land() widens them
+  struct Codes {
+    uint4 k[FP8 ? kLoads8 : 1], v[FP8 ? kLoads8 : 1];
+    float scale;
+  };
+  auto issue = [&](int row_of, unsigned char* dst, Codes& r8) {
     if constexpr (!FP8) {
+      int64_t off[kLoads];
 #pragma unroll
       for (int u = 0; u < kLoads; ++u) {
         const int row = u * RPI + lane / P;
-        const int64_t off = ((int64_t)__shfl(row_c, row) * row_stride + g * D) * 2 + ((lane % P) ^ swizzle<D>(row)) * 16;
-        load_lds16(static_cast<const char*>(a.k) + off, dst + u * RPI * RB);
-        load_lds16(static_cast<const char*>(a.v) + off, dst + kTile + u * RPI * RB);
+        off[u] = ((int64_t)__shfl(row_of, row) * row_stride + g * D) * 2 + ((lane % P) ^ swizzle<D>(row)) * 16;
+      }
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        load_lds16(static_cast<const char*>(a.k) + off[u], dst + u * RPI * RB);
+        load_lds16(static_cast<const char*>(a.v) + off[u], dst + kTile + u * RPI * RB);
       }
     } else {
 #pragma unroll
       for (int u = 0; u < kLoads8; ++u) {
         const int i = u * kWave + lane;
-        const int64_t off = (int64_t)__shfl(row_c, i / PC) * row_stride + g * D + (i % PC) * 16;
-        r8k[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.k) + off);
-        r8v[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.v) + off);
+        const int64_t off = (int64_t)__shfl(row_of, i / PC) * row_stride + g * D + (i % PC) * 16;
+        r8.k[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.k) + off);
+        r8.v[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.v) + off);
       }
-      r8s = (lane < kWT ? a.k_scale : a.v_scale)[(int64_t)row_c * a.n_kv_heads + g];
+      r8.scale = (lane < kWT ? a.k_scale : a.v_scale)[(int64_t)row_of * a.n_kv_heads + g];
     }
   };
-  auto land = [&](unsigned char* dst) {
+  auto land = [&](unsigned char* dst, const Codes& r8) {
     if constexpr (FP8) {
 #pragma unroll
       for (int u = 0; u < kLoads8; ++u) {
@@ -133,10 +156,10 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 ? 2 : 1) k_attn_wave(const
           *reinterpret_cast<uint4*>(d + row * RB + ((c ^ f) << 4)) = make_uint4(w0.x, w0.y, w1.x, w1.y);
           *reinterpret_cast<uint4*>(d + row * RB + (((c + 1) ^ f) << 4)) = make_uint4(w2.x, w2.y, w3.x, w3.y);
         };
-        put(dst, r8k[u]);
-        put(dst + kTile, r8v[u]);
+        put(dst, r8.k[u]);
+        put(dst + kTile, r8.v[u]);
       }
-      sks[lane] = r8s;   // 32 key scales, 32 value scales
+      sks[lane] = r8.scale;   // 32 key scales, 32 value scales
     }
   };
 
@@ -230,35 +253,61 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 ? 2 : 1) k_attn_wave(const
 
   if (jt0 < jt1) {
     const int last = jt1 - 1;
-    int t = token_at(jt0);
-    uint32_t mask_c = (uint32_t)__ballot(seen(t)), mask_n;
-    t = clamp_tok(t);
-    row_c = pool_row(a, table_entry(a, b, t), t);
-    issue(ka);
-    int tok_n = token_at(min(jt0 + kWaves, last));
-    mask_n = (uint32_t)__ballot(seen(tok_n));
-    tok_n = clamp_tok(tok_n);
-    int ent_n = table_entry(a, b, tok_n);
-    int tok_nn = token_at(min(jt0 + 2 * kWaves, last));
-    // (the codes of an e4m3 tile land right before their use, from registers)
-    auto step = [&](int jt, unsigned char* cur, unsigned char* nxt) {
-      __builtin_amdgcn_s_waitcnt(0);   // the tile, and the look-ups of the next ones
-      if constexpr (FP8) land(cur);
-      const uint32_t mask_next = mask_n;
-      if (jt + kWaves < jt1) {
-        row_c = pool_row(a, ent_n, tok_n);
-        issue(nxt);
-        mask_n = (uint32_t)__ballot(seen(tok_nn));
-        tok_n = clamp_tok(tok_nn);
-        ent_n = table_entry(a, b, tok_n);
-        tok_nn = token_at(min(jt + 3 * kWaves, last));
-      }
-      compute(cur, jt, mask_c);
-      mask_c = mask_next;
+    auto look = [&](int t, uint32_t& mask) -> int {
+      if (SEL) mask = (uint32_t)__ballot(seen(t));
+      return clamp_tok(t);
     };
+    auto next = [&](int i) { return min(jt0 + i * kWaves, last); };
+    uint32_t m0 = 0, m1 = 0, m2 = 0;   // of this tile and the next two
+    const int t0 = look(SEL ? pick0 : token_at(jt0), m0);
+    const int t1 = look(SEL ? pick1 : token_at(next(1)), m1);
+    const int e0 = table_entry(a, b, t0), e1 = table_entry(a, b, t1);
     if constexpr (FP8) {
-      for (int jt = jt0; jt < jt1; jt += kWaves) step(jt, ka, ka);
+      // codes two tiles ahead in registers; they land right before their use
+      // (one tile ahead, a wave spent most of its time waiting for gathers).
+      // Loads return in order, so a step's look-ups go out before its codes:
+      // waiting for them then waits for no codes but the oldest.
+      Codes ra, rb;
+      int tok_n = look(SEL ? pick2 : token_at(next(2)), m2);
+      int ent_n = table_entry(a, b, tok_n);
+      int tok_nn = SEL ? pick3 : token_at(next(3));
+      issue(pool_row(a, e0, t0), ka, ra);
+      issue(pool_row(a, e1, t1), ka, rb);
+      auto step = [&](int jt, Codes& r) {
+        land(ka, r);
+        uint32_t m3 = 0;
+        if (jt + 2 * kWaves < jt1) {
+          const int row = pool_row(a, ent_n, tok_n);
+          tok_n = look(tok_nn, m3);
+          ent_n = table_entry(a, b, tok_n);
+          tok_nn = token_at(min(jt + 4 * kWaves, last));
+          issue(row, ka, r);
+        }
+        compute(ka, jt, m0);
+        m0 = m1;
+        m1 = m2;
+        m2 = m3;
+      };
+      for (int jt = jt0; jt < jt1; jt += 2 * kWaves) {
+        step(jt, ra);
+        if (jt + kWaves < jt1) step(jt + kWaves, rb);
+      }
     } else {
+      Codes none;
+      issue(pool_row(a, e0, t0), ka, none);
+      int tok_n = t1, ent_n = e1, tok_nn = SEL ? pick2 : token_at(next(2));
+      auto step = [&](int jt, unsigned char* cur, unsigned char* nxt) {
+        __builtin_amdgcn_s_waitcnt(0);   // the tile, and the look-ups of the next ones
+        if (jt + kWaves < jt1) {
+          issue(pool_row(a, ent_n, tok_n), nxt, none);
+          tok_n = look(tok_nn, m2);
+          ent_n = table_entry(a, b, tok_n);
+          tok_nn = token_at(min(jt + 3 * kWaves, last));
+        }
+        compute(cur, jt, m0);
+        m0 = m1;
+        m1 = m2;
+      };
       for (int jt = jt0; jt < jt1; jt += 2 * kWaves) {
         step(jt, ka, kb_);
         if (jt + kWaves < jt1) step(jt + kWaves, kb_, ka);
@@ -325,7 +374,7 @@ __global__ void __launch_bounds__(256) k_attn_wave_join(const AttnArgs a, const 
   int tok0, nrows;
   if (SEL) {
     tok0 = unit;
-    if (tok0 >= a.q_start[a.n_seq] || tok0 < a.q_start[0]) return;
+    if (tok0 >= a.q_start[a.n_seq] || tok0 < a.q_start[0]) return;   // no sequence's token: nothing was written
     nrows = G;
   } else {
     const SeqSpan sp = seq_span(a, unit);
@@ -335,7 +384,7 @@ __global__ void __launch_bounds__(256) k_attn_wave_join(const AttnArgs a, const 
   }
   if (row >= nrows) return;
   const int qi = SEL ? 0 : row / G, qh = g * G + (SEL ? row : row - qi * G);
-  join_row<D>(a, L, (((int64_t)unit * a.n_kv_heads + g) * L.n_splits) * ROWS + row, ROWS,
+  join_row<D>(a, L, L.n_splits, (((int64_t)unit * a.n_kv_heads + g) * L.n_splits) * ROWS + row, ROWS,
               ((int64_t)tok0 + qi) * a.n_heads + qh, lane);
 }
 

@@ -172,28 +172,59 @@ hipError_t launch_rope(const misa_rope_spec& spec, const void* x, int dtype, int
 }
 
 // One row (token, head, k or v) to LPR lanes (LPR = D / 8 rounded up to a power
-// of two), 8 values a lane.  The rotation runs in fp64: few rows share a
-// rotation here (one head of indexer keys), and a value that lands on the other
+// of two), 8 values a lane; a pair's other value lies in the lane's own piece
+// (interleaved) or in one other piece (half layout), or anywhere (odd offsets).
+// Rows that become codes are rotated in fp64: a value that lands on the other
 // side of an e4m3 border is an error of half a step, so the value that meets
 // the border should be the true one.
+template <bool FP8>
+struct Turn {
+  using T = double;
+  using T2 = double2;
+  static __device__ __forceinline__ double2 of(double turns, double m) { return turn_f64(turns, m); }
+};
+template <>
+struct Turn<false> {
+  using T = float;
+  using T2 = float2;
+  static __device__ __forceinline__ float2 of(double turns, double m) { return turn_f32(turns, m); }
+};
+
+__device__ __forceinline__ void unpack8(uint4 w4, float* x) {
+  const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
+    x[2 * i + 1] = bf16_bits_to_f32(w[i] >> 16);
+  }
+}
+
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads) k_write_pages(
     const uint16_t* __restrict__ k, int64_t k_st, int64_t k_sh, const uint16_t* __restrict__ v, int64_t v_st,
     int64_t v_sh, const int64_t* __restrict__ slots, int64_t n_tokens, int H, int D, int lpr_log2, int TT,
     int64_t n_slots, void* __restrict__ k_pages, void* __restrict__ v_pages, float* __restrict__ k_scale,
     float* __restrict__ v_scale, RopeArgs r) {
-  extern __shared__ double2 s_cs2[];   // [TT][half]
+  using Tn = Turn<FP8>;
+  using T = typename Tn::T;
+  extern __shared__ double2 s_raw[];
+  typename Tn::T2* const s_cs = reinterpret_cast<typename Tn::T2*>(s_raw);   // [TT][half]
   const int lpr = 1 << lpr_log2;
   const int p = threadIdx.x & (lpr - 1);
   const int e0 = p * 8;
+  const bool live = e0 < D;
   const int sides = v != nullptr ? 2 : 1;
   const int rows_per_pass = kThreads >> lpr_log2;
+  const bool hl = r.layout == MISA_ROPE_HALF;
+  // whole pieces: all 8 values of a piece are on one side, their partners in one other piece
+  const bool whole = hl ? r.start % 8 == 0 && r.half % 8 == 0 : r.start % 2 == 0;
+  const bool turns = r.half > 0 && live && e0 + 8 > r.start && e0 < r.start + 2 * r.half;   // (of k rows)
   for (int64_t t0 = (int64_t)blockIdx.x * TT; t0 < n_tokens; t0 += (int64_t)gridDim.x * TT) {
     const int nt = (int)min((int64_t)TT, n_tokens - t0);
     if (r.half > 0) {
       for (int i = threadIdx.x; i < nt * r.half; i += kThreads) {
         const int t = i / r.half, j = i - t * r.half;
-        s_cs2[i] = turn_f64((double)r.positions[t0 + t] * (r.inv_freq[j] * kInv2Pi), r.mscale);
+        s_cs[i] = Tn::of((double)r.positions[t0 + t] * (r.inv_freq[j] * kInv2Pi), r.mscale);
       }
       __syncthreads();
     }
@@ -207,41 +238,50 @@ __global__ void __launch_bounds__(kThreads) k_write_pages(
       const int64_t slot = slots[t0 + t];
       if (slot < 0 || slot >= n_slots) continue;
       const uint16_t* src = is_v ? v + (t0 + t) * v_st + h * v_sh : k + (t0 + t) * k_st + h * k_sh;
-      const bool live = e0 < D;
       float x[8];
-      {
-        const uint4 w4 = live ? *reinterpret_cast<const uint4*>(src + e0) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-  #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
-          x[2 * i + 1] = bf16_bits_to_f32(w[i] >> 16);
-        }
-      }
-      if (r.half > 0 && !is_v && live && e0 + 8 > r.start && e0 < r.start + 2 * r.half) {
-        const double2* cs = s_cs2 + t * r.half;
-  #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int q = e0 + i - r.start;   // element of the rotary part
-          if (q < 0 || q >= 2 * r.half) continue;
-          const bool hl = r.layout == MISA_ROPE_HALF;
-          const bool second = hl ? q >= r.half : (q & 1);
-          const int j = hl ? (second ? q - r.half : q) : q >> 1;
-          const int other = hl ? (second ? q - r.half : q + r.half) : q ^ 1;
-          const double mine = x[i], his = bf16_bits_to_f32(src[r.start + other]);
-          // first: a c - b s; second: b c + a s
-          x[i] = (float)(mine * cs[j].x + (second ? his : -his) * cs[j].y);
+      unpack8(live ? *reinterpret_cast<const uint4*>(src + e0) : make_uint4(0, 0, 0, 0), x);
+      if (turns && !is_v) {
+        const typename Tn::T2* cs = s_cs + t * r.half;
+        const int q0 = e0 - r.start;   // first value's place in the rotary part
+        if (whole && hl) {
+          const bool second = q0 >= r.half;
+          const int j0 = second ? q0 - r.half : q0;
+          float y[8];
+          unpack8(*reinterpret_cast<const uint4*>(src + (second ? e0 - r.half : e0 + r.half)), y);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)   // first: a c - b s; second: b c + a s
+            x[i] = (float)((T)x[i] * cs[j0 + i].x + (T)(second ? y[i] : -y[i]) * cs[j0 + i].y);
+        } else if (whole) {
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const int q = q0 + i;
+            if (q < 0 || q >= 2 * r.half) continue;
+            const T a = x[i], b = x[i + 1], c = cs[q >> 1].x, s = cs[q >> 1].y;
+            x[i] = (float)(a * c - b * s);
+            x[i + 1] = (float)(b * c + a * s);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int q = q0 + i;
+            if (q < 0 || q >= 2 * r.half) continue;
+            const bool second = hl ? q >= r.half : (q & 1);
+            const int j = hl ? (second ? q - r.half : q) : q >> 1;
+            const int other = hl ? (second ? q - r.half : q + r.half) : q ^ 1;
+            const T mine = x[i], his = bf16_bits_to_f32(src[r.start + other]);
+            x[i] = (float)(mine * cs[j].x + (second ? his : -his) * cs[j].y);
+          }
         }
       }
       const int64_t dst_row = slot * H + h;
       if constexpr (FP8) {
         float amax = 0.f;
-  #pragma unroll
+#pragma unroll
         for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(x[i]));
         for (int o = lpr >> 1; o >= 1; o >>= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o, lpr));
         const float s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
         uint32_t c[2];
-  #pragma unroll
+#pragma unroll
         for (int i = 0; i < 2; ++i) {
           int u = 0;
           u = __builtin_amdgcn_cvt_pk_fp8_f32(__fdiv_rn(x[4 * i], s), __fdiv_rn(x[4 * i + 1], s), u, false);
@@ -258,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) k_write_pages(
               make_uint4(pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3]), pk_bf16(x[4], x[5]), pk_bf16(x[6], x[7]));
       }
     }
-    __syncthreads();   // the table is free for the next tokens
+    if (r.half > 0) __syncthreads();   // the table is free for the next tokens
   }
 }
 
@@ -272,10 +312,11 @@ hipError_t launch_write_pages(int64_t n_tokens, int H, int D, const uint16_t* k,
   while ((8 << lpr_log2) < D) ++lpr_log2;
   // tokens of a workgroup: about one pass of its threads, table within 32 KB
   const int64_t lanes = ((int64_t)H * (v != nullptr ? 2 : 1)) << lpr_log2;
+  const int64_t cs_bytes = kdtype == MISA_K_FP8_E4M3 ? sizeof(double2) : sizeof(float2);
   int64_t TT = std::max<int64_t>(1, kThreads / lanes);
-  if (r.half > 0) TT = std::min<int64_t>(TT, std::max<int64_t>(1, 32768 / (r.half * (int64_t)sizeof(double2))));
+  if (r.half > 0) TT = std::min<int64_t>(TT, std::max<int64_t>(1, 32768 / (r.half * cs_bytes)));
   const dim3 grid((unsigned)std::min<int64_t>((n_tokens + TT - 1) / TT, kMaxGroups));
-  const size_t lds = (size_t)TT * r.half * sizeof(double2);
+  const size_t lds = (size_t)TT * r.half * cs_bytes;
   if (kdtype == MISA_K_FP8_E4M3)
     hipLaunchKernelGGL(k_write_pages<true>, grid, dim3(kThreads), lds, st, k, k_st, k_sh, v, v_st, v_sh, slots,
                        n_tokens, H, D, lpr_log2, (int)TT, n_slots, k_pages, v_pages, k_scale, v_scale, r);

@@ -9,17 +9,18 @@ fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
+import struct
 from typing import NamedTuple
 
 import torch
 
-from ._lib import MISA_K_BF16, MISA_K_FP8_E4M3, _check, _kdtype, _need, _ptr, load
+from ._lib import MISA_K_FP8_E4M3, _check, _kdtype, _need, load
 
 MISA_T_BF16, MISA_T_FP16, MISA_T_FP32 = 0, 1, 2
 _DTYPES = {torch.bfloat16: MISA_T_BF16, torch.float16: MISA_T_FP16, torch.float32: MISA_T_FP32}
+_BF16 = (torch.bfloat16,)
 _LAYOUTS = {"half": 0, "interleaved": 1}
 
 
@@ -50,34 +51,64 @@ class PagePlan(NamedTuple):
     n_taken: torch.Tensor     # int32 [1]
 
 
-def _on(t, stream):
-    """The device guard for t's device and the stream handle of a call on it."""
-    dev = t.device
-    guard = contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    return guard, ctypes.c_void_p(s.cuda_stream)
+# The C structures as bytes (native layout: the ctypes classes above); packing
+# is several times cheaper than filling a ctypes object, which counts where a
+# whole call takes a few microseconds.
+_PACK_ROPE = struct.Struct("@PPiiiid")
+_PACK_PAGES = struct.Struct("@PPPPPqqii")
+_PACK_ATTN = struct.Struct("@iiiiqqqif")
+assert _PACK_ROPE.size == ctypes.sizeof(RopeSpec) and _PACK_PAGES.size == ctypes.sizeof(KvPages)
+assert _PACK_ATTN.size == ctypes.sizeof(AttnShape)
+
+_raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle, without a Stream object
 
 
-def _same_device(first, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
-
-
-def _rows(t, dtypes, name, shape=None):
-    """A [tokens, heads, head_dim] tensor whose last dimension is dense; its token and head strides."""
+def _dev(t, name):
+    """Index of the GPU t is on."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if not t.is_cuda:
+    d = t.get_device()
+    if d < 0:
         raise ValueError(f"{name} must be a GPU tensor")
+    return d
+
+
+def _dense(t, dtype, shape, name, dev):
+    """Pointer of a dense tensor of this type and shape on GPU `dev`."""
+    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _need(t, dtype, shape, name)
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    return t.data_ptr()
+
+
+def _rows(t, dtypes, name, dev, shape=None):
+    """Pointer, token and head strides of a [tokens, heads, head_dim] tensor whose
+    last dimension is dense."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}" if t.is_cuda else f"{name} must be a GPU tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected one of {tuple(dtypes)}")
-    if t.dim() != 3 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {'[tokens, heads, head_dim]' if shape is None else tuple(shape)}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        want = "[tokens, heads, head_dim]" if shape is None else tuple(shape)
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {want}")
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if sd != 1 and D > 1:
         raise ValueError(f"{name}: the last dimension must be dense")
     # the strides of dimensions of one element mean nothing
-    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
+    return t.data_ptr(), (st if T > 1 else 0), (sh if H > 1 else 0)
+
+
+def _call(name, fn, dev, stream, *args):
+    """fn(*args, stream handle) on GPU `dev`."""
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return _call(name, fn, dev, stream, *args)
+    st = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st != 0:
+        _check(st, name)
 
 
 def misa_plan_pages(cached_lens, new_lens, free_pages, block_table, page_keys: int, n_tokens: int,
@@ -86,33 +117,25 @@ def misa_plan_pages(cached_lens, new_lens, free_pages, block_table, page_keys: i
     block_table [n_seq, max_pages] (int32, in place) from free_pages (int32) and
     returns the PagePlan.  n_tokens: length of the slot map (at least the sum of
     new_lens; entries behind the last token get slot -1)."""
-    n = int(cached_lens.shape[0])
-    _need(cached_lens, torch.int32, (n,), "cached_lens")
-    _need(new_lens, torch.int32, (n,), "new_lens")
-    _need(free_pages, torch.int32, (free_pages.shape[0],), "free_pages")
-    _need(block_table, torch.int32, (n, block_table.shape[-1]), "block_table")
-    dev = cached_lens.device
+    dev = _dev(cached_lens, "cached_lens")
+    n = cached_lens.shape[0]
+    i32 = torch.int32
     if plan is None:
-        plan = PagePlan(torch.empty(n + 1, dtype=torch.int32, device=dev),
-                        torch.empty(n, dtype=torch.int32, device=dev),
-                        torch.empty(n_tokens, dtype=torch.int64, device=dev),
-                        torch.empty(n_tokens, dtype=torch.int32, device=dev),
-                        torch.empty(1, dtype=torch.int32, device=dev))
+        slots = torch.empty(n_tokens, dtype=torch.int64, device=cached_lens.device)
+        rest = torch.empty(2 * n + 2 + n_tokens, dtype=i32, device=cached_lens.device)
+        q_start, kv_lens, positions, n_taken = rest.split((n + 1, n, n_tokens, 1))
+        plan = PagePlan(q_start, kv_lens, slots, positions, n_taken)
+        at = rest.data_ptr()
+        outs = (at, at + 4 * (n + 1), slots.data_ptr(), at + 4 * (2 * n + 1), n_tokens, at + 4 * (2 * n + 1 + n_tokens))
     else:
-        _need(plan.q_start, torch.int32, (n + 1,), "q_start")
-        _need(plan.kv_lens, torch.int32, (n,), "kv_lens")
-        _need(plan.slots, torch.int64, (n_tokens,), "slots")
-        _need(plan.positions, torch.int32, (n_tokens,), "positions")
-        _need(plan.n_taken, torch.int32, (1,), "n_taken")
-    _same_device(cached_lens, new_lens=new_lens, free_pages=free_pages, block_table=block_table, q_start=plan.q_start,
-                 kv_lens=plan.kv_lens, slots=plan.slots, positions=plan.positions, n_taken=plan.n_taken)
-    guard, s = _on(cached_lens, stream)
-    with guard:
-        st = load().misa_plan_pages(n, _ptr(cached_lens), _ptr(new_lens), int(page_keys), _ptr(free_pages),
-                                    int(free_pages.shape[0]), _ptr(block_table), int(block_table.shape[1]),
-                                    _ptr(plan.q_start), _ptr(plan.kv_lens), _ptr(plan.slots), _ptr(plan.positions),
-                                    int(n_tokens), _ptr(plan.n_taken), s)
-    _check(st, "misa_plan_pages")
+        outs = (_dense(plan.q_start, i32, (n + 1,), "q_start", dev), _dense(plan.kv_lens, i32, (n,), "kv_lens", dev),
+                _dense(plan.slots, torch.int64, (n_tokens,), "slots", dev),
+                _dense(plan.positions, i32, (n_tokens,), "positions", dev), n_tokens,
+                _dense(plan.n_taken, i32, (1,), "n_taken", dev))
+    n_free, width = free_pages.shape[0], block_table.shape[-1]
+    _call("misa_plan_pages", load().misa_plan_pages, dev, stream, n, _dense(cached_lens, i32, (n,), "cached_lens", dev),
+          _dense(new_lens, i32, (n,), "new_lens", dev), page_keys, _dense(free_pages, i32, (n_free,), "free_pages", dev),
+          n_free, _dense(block_table, i32, (n, width), "block_table", dev), width, *outs)
     return plan
 
 
@@ -154,14 +177,14 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str | None = 
     return f.to(device), mscale
 
 
-def _rope_spec(positions, inv_freq, layout, rot_start, mscale, backward, n_tokens, like):
+def _rope_spec(positions, inv_freq, layout, rot_start, mscale, backward, n_tokens, dev):
     if layout not in _LAYOUTS:
         raise ValueError(f"layout: {layout!r}, expected 'half' or 'interleaved'")
-    _need(positions, torch.int32, (n_tokens,), "positions")
-    _need(inv_freq, torch.float64, (inv_freq.shape[0],), "inv_freq")
-    _same_device(like, positions=positions, inv_freq=inv_freq)
-    return RopeSpec(inv_freq.data_ptr(), positions.data_ptr(), 2 * int(inv_freq.shape[0]), int(rot_start),
-                    _LAYOUTS[layout], int(bool(backward)), float(mscale))
+    _dev(inv_freq, "inv_freq")
+    half = inv_freq.shape[0]
+    return _PACK_ROPE.pack(_dense(inv_freq, torch.float64, (half,), "inv_freq", dev),
+                           _dense(positions, torch.int32, (n_tokens,), "positions", dev), 2 * half, rot_start,
+                           _LAYOUTS[layout], 1 if backward else 0, mscale)
 
 
 def misa_rope(x, positions, inv_freq, layout: str = "half", rot_start: int = 0, mscale: float = 1.0,
@@ -171,41 +194,36 @@ def misa_rope(x, positions, inv_freq, layout: str = "half", rot_start: int = 0, 
     rotary part is elements rot_start .. rot_start + 2 len(inv_freq) - 1 of a
     head.  backward: the gradient with respect to x of x -> misa_rope(x, ...),
     given the gradient of its output.  out may be x (in place)."""
-    xst, xsh = _rows(x, _DTYPES, "x")
+    dev = _dev(x, "x")
+    xp, xst, xsh = _rows(x, _DTYPES, "x", dev)
     T, H, D = x.shape
     if out is None:
         out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-    ost, osh = _rows(out, (x.dtype,), "out", x.shape)
-    _same_device(x, out=out)
-    spec = _rope_spec(positions, inv_freq, layout, rot_start, mscale, backward, T, x)
-    if T == 0:
-        return out
-    guard, s = _on(x, stream)
-    with guard:
-        st = load().misa_rope(ctypes.byref(spec), _ptr(x), _DTYPES[x.dtype], T, H, D, xst, xsh, _ptr(out), ost, osh, s)
-    _check(st, "misa_rope")
+    op, ost, osh = _rows(out, (x.dtype,), "out", dev, x.shape)
+    spec = _rope_spec(positions, inv_freq, layout, rot_start, mscale, backward, T, dev)
+    if T > 0:
+        _call("misa_rope", load().misa_rope, dev, stream, spec, xp, _DTYPES[x.dtype], T, H, D, xst, xsh, op, ost, osh)
     return out
 
 
-def _pool(pages, heads, head_dim, name):
-    """kdtype, n_pages, page_keys of a page pool [n_pages, page_keys, heads, head_dim]
-    (or [n_pages, page_keys, head_dim] of one head)."""
+def _pool(pages, heads, head_dim, name, dev):
+    """Pointer, kdtype, n_pages, page_keys of a page pool [n_pages, page_keys, heads,
+    head_dim] (or [n_pages, page_keys, head_dim] of one head)."""
     if pages is None:
         raise ValueError(f"{name} is required")
     kd = _kdtype(pages)
-    n_pages, page_keys = int(pages.shape[0]), int(pages.shape[1])
-    if pages.dim() == 3 and heads == 1:
-        _need(pages, pages.dtype, (n_pages, page_keys, head_dim), name)
-    else:
-        _need(pages, pages.dtype, (n_pages, page_keys, heads, head_dim), name)
-    return kd, n_pages, page_keys
+    shape = pages.shape
+    want = (shape[0], shape[1], heads, head_dim)
+    if len(shape) == 3 and heads == 1:
+        want = (shape[0], shape[1], head_dim)
+    return _dense(pages, pages.dtype, want, name, dev), kd, shape[0], shape[1]
 
 
-def _pool_scale(scale, n_pages, page_keys, heads, name):
-    if scale is not None and scale.dim() == 2 and heads == 1:
-        _need(scale, torch.float32, (n_pages, page_keys), name)
-    else:
-        _need(scale, torch.float32, (n_pages, page_keys, heads), name)
+def _pool_scale(scale, n_pages, page_keys, heads, name, dev):
+    want = (n_pages, page_keys, heads)
+    if scale is not None and heads == 1 and scale.dim() == 2:
+        want = (n_pages, page_keys)
+    return _dense(scale, torch.float32, want, name, dev)
 
 
 def misa_write_pages(k, slots, k_pages, k_scale_pages=None, v=None, v_pages=None, v_scale_pages=None, positions=None,
@@ -216,55 +234,30 @@ def misa_write_pages(k, slots, k_pages, k_scale_pages=None, v=None, v_pages=None
     head dimension out, as misa_indexer_paged takes them.  Given positions and
     inv_freq, k is rotated first (misa_rope).  Slots outside the pool are
     skipped."""
-    kst, ksh = _rows(k, (torch.bfloat16,), "k")
+    dev = _dev(k, "k")
+    kp, kst, ksh = _rows(k, _BF16, "k", dev)
     T, H, D = k.shape
-    kd, n_pages, page_keys = _pool(k_pages, H, D, "k_pages")
-    _need(slots, torch.int64, (T,), "slots")
-    vst = vsh = 0
+    kpool, kd, n_pages, page_keys = _pool(k_pages, H, D, "k_pages", dev)
+    sp = _dense(slots, torch.int64, (T,), "slots", dev)
     if (v is None) != (v_pages is None):
         raise ValueError("v and v_pages go together")
-    if v is not None:
-        vst, vsh = _rows(v, (torch.bfloat16,), "v", k.shape)
-        if _pool(v_pages, H, D, "v_pages") != (kd, n_pages, page_keys):
-            raise ValueError("v_pages must match k_pages")
-    if kd == MISA_K_FP8_E4M3:
-        _pool_scale(k_scale_pages, n_pages, page_keys, H, "k_scale_pages")
-        if v is not None:
-            _pool_scale(v_scale_pages, n_pages, page_keys, H, "v_scale_pages")
-    _same_device(k, slots=slots, k_pages=k_pages, k_scale_pages=k_scale_pages, v=v, v_pages=v_pages,
-                 v_scale_pages=v_scale_pages)
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
-    spec = None
-    if inv_freq is not None:
-        spec = ctypes.byref(_rope_spec(positions, inv_freq, layout, rot_start, mscale, False, T, k))
-    if T == 0:
-        return
-    guard, s = _on(k, stream)
-    with guard:
-        st = load().misa_write_pages(T, H, D, _ptr(k), kst, ksh, _ptr(v), vst, vsh, _ptr(slots), spec, _ptr(k_pages),
-                                     _ptr(v_pages), kd, _ptr(k_scale_pages), _ptr(v_scale_pages), n_pages, page_keys,
-                                     s)
-    _check(st, "misa_write_pages")
-
-
-def _attn_structs(q, k_pages, v_pages, block_table, n_kv_heads, k_scale, v_scale, scale, max_new):
-    qst, qsh = _rows(q, (torch.bfloat16,), "q")
-    T, H, D = q.shape
-    kd, n_pages, page_keys = _pool(k_pages, n_kv_heads, D, "k_pages")
-    if _pool(v_pages, n_kv_heads, D, "v_pages") != (kd, n_pages, page_keys):
-        raise ValueError("v_pages must match k_pages")
+    vp = vst = vsh = vpool = ks = vs = spec = None
+    if v is not None:
+        vp, vst, vsh = _rows(v, _BF16, "v", dev, k.shape)
+        vpool, *like = _pool(v_pages, H, D, "v_pages", dev)
+        if like != [kd, n_pages, page_keys]:
+            raise ValueError("v_pages must match k_pages")
     if kd == MISA_K_FP8_E4M3:
-        _pool_scale(k_scale, n_pages, page_keys, n_kv_heads, "k_scale_pages")
-        _pool_scale(v_scale, n_pages, page_keys, n_kv_heads, "v_scale_pages")
-    n_seq = int(block_table.shape[0])
-    _need(block_table, torch.int32, (n_seq, block_table.shape[-1]), "block_table")
-    shape = AttnShape(n_seq, H, n_kv_heads, D, T, qst, qsh, int(max_new),
-                      1.0 / math.sqrt(D) if scale is None else float(scale))
-    pages = KvPages(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr() if kd == MISA_K_FP8_E4M3 else None,
-                    v_scale.data_ptr() if kd == MISA_K_FP8_E4M3 else None, block_table.data_ptr(),
-                    int(block_table.shape[1]), n_pages, page_keys, kd)
-    return shape, pages
+        ks = _pool_scale(k_scale_pages, n_pages, page_keys, H, "k_scale_pages", dev)
+        if v is not None:
+            vs = _pool_scale(v_scale_pages, n_pages, page_keys, H, "v_scale_pages", dev)
+    if inv_freq is not None:
+        spec = _rope_spec(positions, inv_freq, layout, rot_start, mscale, False, T, dev)
+    if T > 0:
+        _call("misa_write_pages", load().misa_write_pages, dev, stream, T, H, D, kp, kst, ksh, vp, vst or 0, vsh or 0, sp,
+              spec, kpool, vpool, kd, ks, vs, n_pages, page_keys)
 
 
 def misa_attention_paged_workspace_bytes(shape: AttnShape, pages: KvPages) -> int:
@@ -277,50 +270,57 @@ def misa_attention_selected_workspace_bytes(shape: AttnShape, pages: KvPages, to
 
 def _attention(name, q, k_pages, v_pages, block_table, q_start, kv_lens, idx, k_scale, v_scale, scale, max_new, out, lse,
                want_lse, ws, stream):
-    if k_pages is None:
-        raise ValueError("k_pages is required")
-    n_kv = int(k_pages.shape[2]) if k_pages.dim() == 4 else 1
-    shape, pages = _attn_structs(q, k_pages, v_pages, block_table, n_kv, k_scale, v_scale, scale, max_new)
+    dev = _dev(q, "q")
+    qp, qst, qsh = _rows(q, _BF16, "q", dev)
     T, H, D = q.shape
-    _need(q_start, torch.int32, (shape.n_seq + 1,), "q_start")
-    _need(kv_lens, torch.int32, (shape.n_seq,), "kv_lens")
-    topk = 0
+    KH = k_pages.shape[2] if k_pages is not None and k_pages.dim() == 4 else 1
+    kpool, kd, n_pages, page_keys = _pool(k_pages, KH, D, "k_pages", dev)
+    vpool, *like = _pool(v_pages, KH, D, "v_pages", dev)
+    if like != [kd, n_pages, page_keys]:
+        raise ValueError("v_pages must match k_pages")
+    ks = vs = 0
+    if kd == MISA_K_FP8_E4M3:
+        ks = _pool_scale(k_scale, n_pages, page_keys, KH, "k_scale_pages", dev)
+        vs = _pool_scale(v_scale, n_pages, page_keys, KH, "v_scale_pages", dev)
+    _dev(block_table, "block_table")
+    n_seq, width = block_table.shape[0], block_table.shape[-1]
+    i32 = torch.int32
+    shape = _PACK_ATTN.pack(n_seq, H, KH, D, T, qst, qsh, max_new, D ** -0.5 if scale is None else scale)
+    pages = _PACK_PAGES.pack(kpool, vpool, ks, vs, _dense(block_table, i32, (n_seq, width), "block_table", dev), width,
+                             n_pages, page_keys, kd)
+    args = [shape, pages, qp, _dense(q_start, i32, (n_seq + 1,), "q_start", dev),
+            _dense(kv_lens, i32, (n_seq,), "kv_lens", dev)]
+    lib = load()
     if name == "misa_attention_selected":
-        if idx is None:
-            raise ValueError("idx is required")
-        topk = int(idx.shape[-1])
-        idx = idx.reshape(T, topk) if idx.dim() == 3 and idx.is_contiguous() and idx.shape[0] * idx.shape[1] == T else idx
-        _need(idx, torch.int32, (T, topk), "idx")
+        _dev(idx, "idx")
+        topk = idx.shape[-1]
+        if idx.dim() == 3 and idx.shape[0] * idx.shape[1] == T and idx.is_contiguous():
+            idx = idx.view(T, topk)
+        args += [_dense(idx, i32, (T, topk), "idx", dev), topk]
+        fn = lib.misa_attention_selected
+    else:
+        fn = lib.misa_attention_paged
     if out is None:
         out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
-    _need(out, torch.bfloat16, (T, H, D), "out")
+    args.append(_dense(out, torch.bfloat16, (T, H, D), "out", dev))
     if lse is None and want_lse:
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    if lse is not None:
-        _need(lse, torch.float32, (T, H), "lse")
-    _same_device(q, k_pages=k_pages, v_pages=v_pages, block_table=block_table, q_start=q_start, kv_lens=kv_lens, idx=idx,
-                 k_scale_pages=k_scale, v_scale_pages=v_scale, out=out, lse=lse, ws=ws)
-    lib = load()
-    sp, pp = ctypes.byref(shape), ctypes.byref(pages)
+    args.append(None if lse is None else _dense(lse, torch.float32, (T, H), "lse", dev))
     if T == 0:
         return out, lse
-    guard, s = _on(q, stream)
-    with guard:
-        if ws is None:
-            need = (lib.misa_attention_selected_workspace_bytes(sp, pp, topk) if idx is not None
-                    else lib.misa_attention_paged_workspace_bytes(sp, pp))
-            if need:
-                ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-                if stream is not None:   # the block may be reused once `stream` has passed this call
-                    ws.record_stream(stream)
-        nb = 0 if ws is None else ws.numel() * ws.element_size()
-        if idx is not None:
-            st = lib.misa_attention_selected(sp, pp, _ptr(q), _ptr(q_start), _ptr(kv_lens), _ptr(idx), topk, _ptr(out),
-                                             _ptr(lse), _ptr(ws), nb, s)
-        else:
-            st = lib.misa_attention_paged(sp, pp, _ptr(q), _ptr(q_start), _ptr(kv_lens), _ptr(out), _ptr(lse),
-                                          _ptr(ws), nb, s)
-    _check(st, name)
+    if ws is None:
+        need = (lib.misa_attention_paged_workspace_bytes(shape, pages) if idx is None
+                else lib.misa_attention_selected_workspace_bytes(shape, pages, topk))
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            if stream is not None:   # its memory may be handed on once `stream` has passed this call
+                ws.record_stream(stream)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a dense tensor on cuda:{dev}")
+    if ws is None:
+        _call(name, fn, dev, stream, *args, None, 0)
+    else:
+        _call(name, fn, dev, stream, *args, ws.data_ptr(), ws.numel() * ws.element_size())
     return out, lse
 
 
