@@ -16,11 +16,102 @@ hipError_t launch_attn_wave(const AttnArgs& a, const AttnLaunch& L, int D, bool 
 
 namespace {
 
+// The joins of a call's launches in one: workgroups below n_tile join
+// attn_tile's units (BM rows each), the others attn_wave's (16 RT rows), 16
+// rows a workgroup and 4 a wave, whose loads are all under way together (a row
+// a wave took four times as long: 46k rows of two to seven splits in 19 us).
+struct JoinSide {
+  AttnLaunch L;
+  int rows;   // of a unit's part of the workspace
+};
+
+template <int D, bool SEL>
+__global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a, const JoinSide tile, const JoinSide wave,
+                                                   uint32_t n_tile) {
+  constexpr int LR = D / 4, kGroups = kWave / LR, R = 4;   // lanes of a row, rows' splits read side by side, rows
+  const bool is_tile = blockIdx.x < n_tile;
+  const JoinSide& S = is_tile ? tile : wave;
+  const uint32_t i = is_tile ? blockIdx.x : blockIdx.x - n_tile;
+  const int lane = threadIdx.x & 63;
+  const int G = a.n_heads / a.n_kv_heads;
+  const uint32_t per = (uint32_t)S.rows / 16;   // workgroups of a unit and kv head
+  const int rr0 = (int)(i % per) * 16 + (int)(threadIdx.x >> 6) * R;
+  const int g = (int)(i / per % (uint32_t)a.n_kv_heads), unit = (int)(i / per / (uint32_t)a.n_kv_heads);
+  int r0, nrows, tok0, n = S.L.n_splits;
+  if (SEL) {
+    const int sub = is_tile ? (G + S.rows - 1) / S.rows : 1;
+    tok0 = unit / sub;
+    r0 = (unit % sub) * S.rows;
+    if (tok0 >= a.q_start[a.n_seq] || tok0 < a.q_start[0]) return;   // no sequence's token: nothing was written
+    nrows = G;
+  } else {
+    const int4 u = S.L.unit_info[unit];
+    tok0 = u.x;
+    r0 = u.y;
+    nrows = u.z;
+    n = u.w;
+  }
+  if (n <= 1 || r0 + rr0 >= nrows) return;   // written by the unit itself, or no row
+  const int64_t pr = (((int64_t)unit * a.n_kv_heads + g) * S.L.n_splits) * S.rows + rr0;
+  // lane s: split s's weight of each row
+  float2 ml[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k)
+    ml[k] = lane < n && r0 + rr0 + k < nrows ? S.L.part_ml[pr + (int64_t)lane * S.rows + k] : make_float2(-INFINITY, 0.f);
+  float w[R], top[R], sum[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    top[k] = ml[k].y > 0.f ? ml[k].x : -INFINITY;
+#pragma unroll
+    for (int x = 32; x >= 1; x >>= 1) top[k] = fmaxf(top[k], __shfl_xor(top[k], x));
+    w[k] = ml[k].y > 0.f ? exp2_raw(ml[k].x - top[k]) : 0.f;
+    sum[k] = w[k] * ml[k].y;
+#pragma unroll
+    for (int x = 32; x >= 1; x >>= 1) sum[k] += __shfl_xor(sum[k], x);
+  }
+  // D / 4 lanes read a split's row, 16 bytes each, the wave's groups of such
+  // lanes the splits in turn.  Fixed order.
+  f32x4 o[R] = {};
+#pragma unroll 2
+  for (int s0 = 0; s0 < n; s0 += kGroups) {
+    const int s = min(s0 + lane / LR, n - 1);
+    f32x4 v[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      v[k] = *reinterpret_cast<const f32x4*>(S.L.part_o + (pr + (int64_t)s * S.rows + k) * D + (lane % LR) * 4);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const float ws = s0 + lane / LR < n ? __shfl(w[k], s) : 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)   // an empty split wrote no output: whatever is there is not used
+        o[k][e] = ws == 0.f ? o[k][e] : __builtin_fmaf(ws, v[k][e], o[k][e]);
+    }
+  }
+#pragma unroll
+  for (int x = LR; x < kWave; x <<= 1)
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[k][e] += __shfl_xor(o[k][e], x);
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const int r = r0 + rr0 + k;
+    if (r >= nrows) return;
+    const int qi = SEL ? 0 : r / G, qh = g * G + (SEL ? r : r - qi * G);
+    const int64_t out_row = ((int64_t)tok0 + qi) * a.n_heads + qh;
+    const float inv = sum[k] > 0.f ? 1.f / sum[k] : 0.f;
+    if (lane < LR)
+      *reinterpret_cast<uint2*>(a.out + out_row * D + lane * 4) =
+          make_uint2(pk_bf16(o[k][0] * inv, o[k][1] * inv), pk_bf16(o[k][2] * inv, o[k][3] * inv));
+    if (a.lse != nullptr && lane == 0) a.lse[out_row] = sum[k] > 0.f ? (top[k] + __log2f(sum[k])) * kLn2 : -INFINITY;
+  }
+}
+
 struct AttnPlan {
   int RT = 0, wave_units = 0, wave_splits = 1, wave_slots = 0;   // RT = 0: attn_wave does not run
   int NW = 0, tile_units = 0, tile_splits = 1, tile_slots = 0;   // NW = 0: attn_tile does not run
   int rows_min = 0;
-  size_t wave_o = 0, wave_ml = 0, tile_o = 0, tile_ml = 0, tile_info = 0, total = 0;
+  size_t wave_o = 0, wave_ml = 0, wave_info = 0, tile_o = 0, tile_ml = 0, tile_info = 0, total = 0;
   int64_t groups = 0;   // workgroups of the larger launch
 };
 
@@ -33,11 +124,11 @@ inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 // tiles and about 4 tiles' time to start, plus the join, which reads every
 // split's rows again.
 // Dense: the lengths are known to the GPU only, which decides how many of the
-// splits a unit uses (split_tiles); this is the bound, three to a slot, by the
+// splits a unit uses (split_tiles); this is the bound, two to a slot, by the
 // widest the table allows.
 int choose_splits(int64_t units, int64_t slots, int64_t steps, int most, bool exact) {
   if (!exact) {
-    const int64_t s = units >= 3 * slots ? 1 : (3 * slots + units - 1) / units;
+    const int64_t s = units >= 2 * slots ? 1 : (2 * slots + units - 1) / units;
     return (int)std::max<int64_t>(1, std::min<int64_t>({s, most, steps / 4}));
   }
   int best = 1;
@@ -104,6 +195,8 @@ AttnPlan make_plan(const misa_attn_shape& s, const misa_kv_pages& pg, int topk) 
     off += align_up(rows * s.head_dim * sizeof(float));
     p.wave_ml = off;
     off += align_up(rows * sizeof(float2));
+    p.wave_info = off;
+    off += align_up((size_t)p.wave_units * sizeof(int4));
   }
   if (p.NW > 0 && p.tile_splits > 1) {
     const size_t rows = (size_t)p.tile_units * KH * p.tile_splits * 32 * p.NW;
@@ -139,19 +232,28 @@ hipError_t launch_attention(const misa_attn_shape& s, const misa_kv_pages& pg, c
                    s.n_tokens};
   const bool fp8 = pg.kdtype == MISA_K_FP8_E4M3;
   char* base = static_cast<char*>(ws);
+  const AttnLaunch T{p.tile_units, p.tile_splits, p.tile_slots, p.rows_min, reinterpret_cast<float*>(base + p.tile_o),
+                     reinterpret_cast<float2*>(base + p.tile_ml), reinterpret_cast<int4*>(base + p.tile_info)};
+  const AttnLaunch W{p.wave_units, p.wave_splits, p.wave_slots, p.rows_min, reinterpret_cast<float*>(base + p.wave_o),
+                     reinterpret_cast<float2*>(base + p.wave_ml), reinterpret_cast<int4*>(base + p.wave_info)};
   hipError_t e = hipSuccess;
-  if (p.NW > 0) {
-    const AttnLaunch L{p.tile_units, p.tile_splits, p.tile_slots, p.rows_min,
-                       reinterpret_cast<float*>(base + p.tile_o), reinterpret_cast<float2*>(base + p.tile_ml),
-                       reinterpret_cast<int4*>(base + p.tile_info)};
-    e = launch_attn_tile(a, L, s.head_dim, fp8, p.NW, st);
+  if (p.NW > 0) e = launch_attn_tile(a, T, s.head_dim, fp8, p.NW, st);
+  if (e == hipSuccess && p.RT > 0) e = launch_attn_wave(a, W, s.head_dim, fp8, p.RT, st);
+  const int64_t n_tile = p.NW > 0 && p.tile_splits > 1 ? (int64_t)p.tile_units * s.n_kv_heads * p.NW * 2 : 0;
+  const int64_t n_wave = p.RT > 0 && p.wave_splits > 1 ? (int64_t)p.wave_units * s.n_kv_heads * p.RT : 0;
+  if (e != hipSuccess || n_tile + n_wave == 0) return e;
+  const JoinSide jt{T, 32 * p.NW}, jw{W, 16 * p.RT};
+  const dim3 grid((unsigned)(n_tile + n_wave));
+  const uint32_t nt = (uint32_t)n_tile;
+  const bool sel = idx != nullptr;
+  if (s.head_dim == 128) {
+    if (sel) hipLaunchKernelGGL((k_attn_join<128, true>), grid, dim3(256), 0, st, a, jt, jw, nt);
+    else hipLaunchKernelGGL((k_attn_join<128, false>), grid, dim3(256), 0, st, a, jt, jw, nt);
+  } else {
+    if (sel) hipLaunchKernelGGL((k_attn_join<64, true>), grid, dim3(256), 0, st, a, jt, jw, nt);
+    else hipLaunchKernelGGL((k_attn_join<64, false>), grid, dim3(256), 0, st, a, jt, jw, nt);
   }
-  if (e == hipSuccess && p.RT > 0) {
-    const AttnLaunch L{p.wave_units, p.wave_splits, p.wave_slots, p.rows_min,
-                       reinterpret_cast<float*>(base + p.wave_o), reinterpret_cast<float2*>(base + p.wave_ml), nullptr};
-    e = launch_attn_wave(a, L, s.head_dim, fp8, p.RT, st);
-  }
-  return e;
+  return hipGetLastError();
 }
 
 }  // namespace misa

@@ -26,8 +26,12 @@
 namespace misa {
 
 constexpr float kLn2 = 0.6931471805599453f;
+// The outputs are rescaled only when a row's maximum has grown by more than this
+// (log2) since the last time: weights stay below 2^8, well inside bf16 and fp32.
+constexpr float kGrow = 8.f;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_void;
 typedef const __attribute__((address_space(1))) void* global_void;
 
@@ -44,6 +48,14 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ uint2 lds_read_tr(const unsigned char* p) {
   typedef __attribute__((address_space(3))) s16x4* ptr;
   return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)p));
+}
+
+// The same for bytes: lanes 2j, 2j + 1 name 8 consecutive bytes each of row j (j =
+// 0..7); lane i receives byte i of the eight rows.
+__device__ __forceinline__ uint2 lds_read_tr8(const unsigned char* p) {
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  typedef __attribute__((address_space(3))) i32x2* ptr;
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((ptr)p));
 }
 
 // 16 bytes a lane, global -> LDS (dst: the wave's 1 KB, lane order)
@@ -127,9 +139,11 @@ __device__ __forceinline__ bool seq_of_token(const AttnArgs& a, int64_t t, int l
   return true;
 }
 
-// Entry j of token t's list, -1 behind its end
+// Entry j of token t's list, -1 behind its end (always one load: a load behind
+// a branch makes the compiler wait for everything under way)
 __device__ __forceinline__ int pick(const AttnArgs& a, int64_t t, int j) {
-  return j < a.topk ? a.idx[t * a.topk + j] : -1;
+  const int v = a.idx[t * a.topk + min(j, a.topk - 1)];
+  return j < a.topk ? v : -1;
 }
 
 // -scale is folded into the sign of q, so that a maximum of scores is a maximum
@@ -147,13 +161,10 @@ struct AttnLaunch {
   int rows_min;     // dense: attn_tile takes sequences with more rows than this, attn_wave the others
   float* part_o;    // n_splits > 1: unnormalised outputs [unit][kv head][split][row][D]
   float2* part_ml;  // and (maximum, sum) of each
-  int4* unit_info;  // dense attn_tile: (first token, first row, rows in all, splits in use) of each unit
+  // dense: where a unit's rows are, for the join: (first token, first row, rows in all, splits in use)
+  int4* unit_info;
 };
 
-#ifndef ROUNDS
-#define ROUNDS 3
-#endif
-constexpr int kRounds = ROUNDS;
 // Sums over the sequences of a dense launch, for one kv head
 struct DenseScan {
   float steps;   // key tiles of all units together
@@ -162,7 +173,7 @@ struct DenseScan {
 };
 
 // Key tiles of a split.  Lengths differ within a batch, and a unit's share of
-// the splits should follow its own: all splits are equally long, three to each
+// the splits should follow its own: all splits are equally long, two to each
 // workgroup that the GPU holds.  No splits where the units are one full round
 // of nearly equal length (they would only add rounds), or so many that they
 // balance by themselves.
@@ -170,7 +181,7 @@ __device__ __forceinline__ int split_tiles(const DenseScan& w, const AttnLaunch&
   if (w.units == 0) return (n + L.n_splits - 1) / L.n_splits;   // selected tokens, or no scan: even shares
   const float fair = w.steps * (float)kv_heads / (float)L.slots;
   const float units = (float)w.units * (float)kv_heads;
-  int p = max(least, (int)ceilf(fair * (1.f / kRounds)));
+  int p = max(least, (int)ceilf(fair * 0.5f));
   if (((float)w.longest <= 1.25f * fair && units <= 1.05f * (float)L.slots) || units >= 6.f * (float)L.slots)
     p = max(p, w.longest);
   return max(p, (n + L.n_splits - 1) / L.n_splits);
@@ -297,44 +308,6 @@ __device__ __forceinline__ Place place_of(const AttnLaunch& L, int kv_heads, uin
     unit = i % n;
   }
   return Place{(int)unit, (int)(pair % (uint32_t)kv_heads), (int)(pair / (uint32_t)kv_heads)};
-}
-
-// The splits of one output row: partial rows pr, pr + step, ...; out_row is the
-// row of out and lse.  Lane s first holds split s's weight; then D / 4 lanes
-// read a split's row, 16 bytes each, and the wave's groups of such lanes take
-// the splits in turn.  Fixed order.
-template <int D>
-__device__ __forceinline__ void join_row(const AttnArgs& a, const AttnLaunch& L, int n_splits, int64_t pr, int64_t step,
-                                         int64_t out_row, int lane) {
-  constexpr int LR = D / 4, kGroups = kWave / LR;
-  float2 ml = make_float2(-INFINITY, 0.f);
-  if (lane < n_splits) ml = L.part_ml[pr + lane * step];
-  float top = ml.y > 0.f ? ml.x : -INFINITY;
-#pragma unroll
-  for (int x = 32; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-  const float w = ml.y > 0.f ? exp2_raw(ml.x - top) : 0.f;
-  float sum = w * ml.y;
-#pragma unroll
-  for (int x = 32; x >= 1; x >>= 1) sum += __shfl_xor(sum, x);
-  f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int s0 = 0; s0 < n_splits; s0 += kGroups) {
-    const int s = min(s0 + lane / LR, n_splits - 1);
-    const float ws = s0 + lane / LR < n_splits ? __shfl(w, s) : 0.f;
-    const f32x4 v = *reinterpret_cast<const f32x4*>(L.part_o + (pr + s * step) * D + (lane % LR) * 4);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)   // an empty split wrote no output: whatever is there is not used
-      o[e] = ws == 0.f ? o[e] : __builtin_fmaf(ws, v[e], o[e]);
-  }
-#pragma unroll
-  for (int x = LR; x < kWave; x <<= 1)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], x);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  if (lane < LR)
-    *reinterpret_cast<uint2*>(a.out + out_row * D + lane * 4) =
-        make_uint2(pk_bf16(o[0] * inv, o[1] * inv), pk_bf16(o[2] * inv, o[3] * inv));
-  if (a.lse != nullptr && lane == 0) a.lse[out_row] = sum > 0.f ? (top + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
 }  // namespace misa

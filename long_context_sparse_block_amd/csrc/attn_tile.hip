@@ -11,16 +11,9 @@
 
 namespace misa {
 
-#ifndef KSCHED
-#define KSCHED 11
-#endif
-#ifndef LEAST
-#define LEAST 8
-#endif
 namespace {
-constexpr int kSched = KSCHED;
 constexpr int kBN = 64;          // keys of a tile
-constexpr float kGrow = 8.f;     // log2 of the growth that forces a rescale
+constexpr int kMfma = 0x8, kDsRead = 0x100;   // instruction classes of sched_group_barrier
 
 // e4m3 codes of the tile, 16 bytes a load, on their way to bf16 rows in LDS
 template <int D, int NT>
@@ -50,14 +43,6 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
   const int h = lane >> 5, c32 = lane & 31;
   const int G = a.n_heads / a.n_kv_heads;
 
-#ifdef PRIO
-  {
-    const int slot = __builtin_amdgcn_s_getreg(4 | (0 << 6) | (3 << 11));
-    if (PRIO == 1) { if (slot & 1) __builtin_amdgcn_s_setprio(1); }
-    if (PRIO == 2) { if (slot & 1) __builtin_amdgcn_s_setprio(3); }
-    if (PRIO == 3) { if (slot == 1) __builtin_amdgcn_s_setprio(1); else if (slot == 2) __builtin_amdgcn_s_setprio(2); else if (slot >= 3) __builtin_amdgcn_s_setprio(3); }
-  }
-#endif
   const Place at = place_of(L, a.n_kv_heads, blockIdx.x);
   const int split = at.split, g = at.g;
   int unit = at.unit;
@@ -66,9 +51,9 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
   int kend, kfull;             // keys some row sees, keys every row sees
   int jt0, jt1;                // the tiles of this split
   int in_use = 1;              // its unit's splits in use
-  auto range = [&](const DenseScan& w) {
+  auto range = [&](const DenseScan& w) __attribute__((always_inline)) {
     const int n = (kend + kBN - 1) / kBN;
-    const int per = max(1, L.n_splits == 1 ? n : split_tiles(w, L, a.n_kv_heads, n, LEAST));
+    const int per = max(1, L.n_splits == 1 ? n : split_tiles(w, L, a.n_kv_heads, n, 8));
     in_use = max(1, (n + per - 1) / per);
     jt0 = split * per;
     jt1 = min(n, jt0 + per);
@@ -128,11 +113,11 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
   // Staging.  Lane k of every wave looks up key k of a tile two tiles ahead:
   // the listed token (SEL) three tiles ahead, its table entry two, so that no
   // load is waited for in the iteration that issues it.
-  auto token_at = [&](int jt) -> int {
+  auto token_at = [&](int jt) __attribute__((always_inline)) -> int {
     const int j = jt * kBN + lane;
     return SEL ? pick(a, tok0, j) : min(j, kend - 1);
   };
-  auto clamp_tok = [&](int t) -> int { return SEL ? (t >= 0 && t < kfull ? t : 0) : t; };
+  auto clamp_tok = [&](int t) __attribute__((always_inline)) -> int { return SEL ? (t >= 0 && t < kfull ? t : 0) : t; };
   using Stage = Fp8Stage<D, NT>;
   // Lane k of every wave knows where key k's pool row starts (bytes); a load's
   // lanes fetch that from the lane of their row.  Which piece of the row a lane
@@ -146,13 +131,13 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
   constexpr int kStepRows = FP8 ? NT / PC : NW * RPI;        // rows between a lane's loads
   static_assert(kStepRows % 16 == 0 || (kStepRows == 8 && !FP8), "a lane's piece and its place in LDS repeat");
   const int lodd = kStepRows % 16 == 0 ? 0 : (((lane % P) ^ swizzle<D>(lrow + 8)) - lpiece) * 16;   // of odd loads
-  auto fetch = [&](int64_t off, int from) -> int64_t {
+  auto fetch = [&](int64_t off, int from) __attribute__((always_inline)) -> int64_t {
     const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)off, from), hi = (uint32_t)__shfl((int)(off >> 32), from);
     return (int64_t)(((uint64_t)hi << 32) | lo);
   };
   // a tile towards LDS: bf16 straight there, e4m3 codes into registers, from
   // which land() widens them
-  auto issue = [&](int row_of, unsigned char* dk, unsigned char* dv, Stage& st) {
+  auto issue = [&](int row_of, unsigned char* dk, unsigned char* dv, Stage& st) __attribute__((always_inline)) {
     const int64_t mine = (int64_t)row_of * row_bytes;
     constexpr int N = FP8 ? Stage::kLoads : kLoads;
     int64_t off[N];
@@ -175,11 +160,11 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
   };
   const int lf = swizzle<D>(lrow);
   const int land0 = lrow * RB + (((2 * lpiece) ^ lf) << 4), land1 = lrow * RB + (((2 * lpiece + 1) ^ lf) << 4);
-  auto land = [&](const Stage& st, unsigned char* dk, unsigned char* dv, float* dks, float* dvs) {
+  auto land = [&](const Stage& st, unsigned char* dk, unsigned char* dv, float* dks, float* dvs) __attribute__((always_inline)) {
     if constexpr (FP8) {
 #pragma unroll
       for (int u = 0; u < Stage::kLoads; ++u) {
-        auto put = [&](unsigned char* d, uint4 x) {
+        auto put = [&](unsigned char* d, uint4 x) __attribute__((always_inline)) {
           const uint2 w0 = e4m3x4_to_bf16x4(x.x), w1 = e4m3x4_to_bf16x4(x.y);
           const uint2 w2 = e4m3x4_to_bf16x4(x.z), w3 = e4m3x4_to_bf16x4(x.w);
           *reinterpret_cast<uint4*>(d + u * kStepRows * RB + land0) = make_uint4(w0.x, w0.y, w1.x, w1.y);
@@ -212,7 +197,7 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
     v_base[e2] = (8 * e2 + 4 * h + vr) * RB + ((vc ^ (2 * e2 + h)) << 4) + (lane & 1) * 8;
 
   auto compute = [&](const unsigned char* sk, const unsigned char* sv, const float* sks, const float* svs, int jt,
-                     uint64_t mask) {
+                     uint64_t mask) __attribute__((always_inline)) {
     f32x16 s[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
@@ -226,15 +211,14 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
         s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[ks], s[kb], 0, 0, 0);
       }
     }
-    if (kSched & 1) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+    // six reads ahead of the products (left alone, the compiler waits for each)
+    __builtin_amdgcn_sched_group_barrier(kDsRead, 6, 0);
 #pragma unroll
-      for (int i = 0; i < 2 * KS - 6; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      }
-      __builtin_amdgcn_sched_group_barrier(0x8, 6, 0);
+    for (int i = 0; i < 2 * KS - 6; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
     }
+    __builtin_amdgcn_sched_group_barrier(kMfma, 6, 0);
     // key of s[kb][4 j + i]: kb 32 + 8 j + 4 h + i
     if constexpr (FP8) {
 #pragma unroll
@@ -303,8 +287,7 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
         pf[2 * kb + q] = as_bf16x8(make_uint4(pk_bf16(p[8 * q], p[8 * q + 1]), pk_bf16(p[8 * q + 2], p[8 * q + 3]),
                                               pk_bf16(p[8 * q + 4], p[8 * q + 5]), pk_bf16(p[8 * q + 6], p[8 * q + 7])));
     }
-    if (kSched & 8) __builtin_amdgcn_sched_barrier(0);
-    if (kSched & 4) __builtin_amdgcn_s_setprio(1);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
 #pragma unroll
@@ -314,21 +297,18 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
         o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(make_uint4(lo.x, lo.y, hi.x, hi.y)), pf[t], o[db], 0, 0, 0);
       }
     }
-    if (kSched & 4) __builtin_amdgcn_s_setprio(0);
-    if (kSched & 2) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+    __builtin_amdgcn_sched_group_barrier(kDsRead, 8, 0);
 #pragma unroll
-      for (int i = 0; i < 4 * DB - 4; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-      }
-      __builtin_amdgcn_sched_group_barrier(0x8, 4, 0);
+    for (int i = 0; i < 4 * DB - 4; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kDsRead, 2, 0);
     }
+    __builtin_amdgcn_sched_group_barrier(kMfma, 4, 0);
   };
 
   if (jt0 < jt1) {
     const int last = jt1 - 1;
-    auto look = [&](int t, uint64_t& mask) -> int {
+    auto look = [&](int t, uint64_t& mask) __attribute__((always_inline)) -> int {
       if (SEL) mask = __ballot(t >= 0 && t < kfull);
       return clamp_tok(t);
     };
@@ -342,7 +322,7 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
       Stage none;
       issue(pool_row(a, e0, t0), s_k0, s_v0, none);
       int tok_n = t1, ent_n = e1, tok_nn = SEL ? pick2 : token_at(min(jt0 + 2, last));
-      auto step = [&](int jt, const unsigned char* ck, const unsigned char* cv, unsigned char* nk, unsigned char* nv) {
+      auto step = [&](int jt, const unsigned char* ck, const unsigned char* cv, unsigned char* nk, unsigned char* nv) __attribute__((always_inline)) {
         __builtin_amdgcn_s_waitcnt(0);
         __syncthreads();   // tile jt is in LDS, and nobody reads the other buffer any more
         if (jt + 1 < jt1) {
@@ -363,41 +343,44 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
       // Codes two tiles ahead in registers, widened into the other buffer after
       // the tile before is done with.  Loads return in order, so a step's
       // look-ups go out before its codes: waiting for them then waits for no
-      // codes but the oldest.
+      // codes but the oldest.  Near the end the last tile is loaded again: loads
+      // behind a branch would make the compiler wait for all of them.
       Stage sa, sb;
       int tok_n = look(SEL ? pick2 : token_at(min(jt0 + 2, last)), m2);
       int ent_n = table_entry(a, b, tok_n);
       int tok_nn = token_at(min(jt0 + 3, last));
       issue(pool_row(a, e0, t0), nullptr, nullptr, sa);
+      __builtin_amdgcn_sched_barrier(0);   // in this order
       issue(pool_row(a, e1, t1), nullptr, nullptr, sb);
+      __builtin_amdgcn_sched_barrier(0);
       land(sa, s_k0, s_v0, s_ks0, s_vs0);
       auto step = [&](int jt, const unsigned char* ck, const unsigned char* cv, const float* cks, const float* cvs,
-                      unsigned char* nk, unsigned char* nv, float* nks, float* nvs, Stage& free, const Stage& next) {
+                      unsigned char* nk, unsigned char* nv, float* nks, float* nvs, Stage& free, const Stage& next) __attribute__((always_inline)) {
         __syncthreads();   // tile jt is in LDS, and nobody reads the other buffer any more
         uint64_t m3 = ~0ull;
-        if (jt + 2 < jt1) {
-          const int row = pool_row(a, ent_n, tok_n);
-          tok_n = look(tok_nn, m3);
-          ent_n = table_entry(a, b, tok_n);
-          tok_nn = token_at(min(jt + 4, last));
-          issue(row, nullptr, nullptr, free);
-        }
+        const int row = pool_row(a, ent_n, tok_n);
+        tok_n = look(tok_nn, m3);
+        ent_n = table_entry(a, b, tok_n);
+        tok_nn = token_at(min(jt + 4, last));
+        issue(row, nullptr, nullptr, free);
         compute(ck, cv, cks, cvs, jt, m0);
-        if (jt + 1 < jt1) land(next, nk, nv, nks, nvs);
+        land(next, nk, nv, nks, nvs);
         m0 = m1;
         m1 = m2;
         m2 = m3;
       };
-      for (int jt = jt0; jt < jt1; jt += 2) {
+      for (int jt = jt0;;) {   // (one way back to the top, for the compiler's count of loads under way)
         step(jt, s_k0, s_v0, s_ks0, s_vs0, s_k1, s_v1, s_ks1, s_vs1, sa, sb);
-        if (jt + 1 < jt1) step(jt + 1, s_k1, s_v1, s_ks1, s_vs1, s_k0, s_v0, s_ks0, s_vs0, sb, sa);
+        if (++jt >= jt1) break;
+        step(jt, s_k1, s_v1, s_ks1, s_vs1, s_k0, s_v0, s_ks0, s_vs0, sb, sa);
+        if (++jt >= jt1) break;
       }
     }
   }
 
   l = sum_halves(l);
   // o[db][4 j + i] of the lane: element db 32 + 8 j + 4 h + i of row r
-  if (L.n_splits == 1) {
+  if (in_use == 1) {
     if (!live) return;
     const float inv = l > 0.f ? 1.f / l : 0.f;
     uint16_t* dst = a.out + (qrow * a.n_heads + qh) * D;
@@ -422,40 +405,11 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
   }
 }
 
-// The splits of a unit's rows joined, a row a wave
-template <int D, bool SEL>
-__global__ void __launch_bounds__(256) k_attn_tile_join(const AttnArgs a, const AttnLaunch L, int BM) {
-  const int lane = threadIdx.x & 63;
-  const int unit = blockIdx.x, g = blockIdx.y;
-  const int G = a.n_heads / a.n_kv_heads;
-  int r0, nrows, tok0, n_splits = L.n_splits;
-  if (SEL) {
-    const int sub = (G + BM - 1) / BM;
-    tok0 = unit / sub;
-    r0 = (unit % sub) * BM;
-    if (tok0 >= a.q_start[a.n_seq] || tok0 < a.q_start[0]) return;   // no sequence's token: nothing was written
-    nrows = G;
-  } else {
-    const int4 u = L.unit_info[unit];
-    tok0 = u.x;
-    r0 = u.y;
-    nrows = u.z;
-    n_splits = u.w;
-  }
-  const int rr = blockIdx.z * 4 + (threadIdx.x >> 6), r = r0 + rr;
-  if (r >= nrows) return;
-  const int qi = SEL ? 0 : r / G, qh = g * G + (SEL ? r : r - qi * G);
-  join_row<D>(a, L, n_splits, (((int64_t)unit * a.n_kv_heads + g) * L.n_splits) * BM + rr, BM,
-              ((int64_t)tok0 + qi) * a.n_heads + qh, lane);
-}
-
 template <int D, bool FP8, bool SEL>
 static hipError_t launch_nw(const AttnArgs& a, const AttnLaunch& L, int NW, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)L.n_units * L.n_splits * a.n_kv_heads));
   if (NW == 2) hipLaunchKernelGGL((k_attn_tile<D, FP8, SEL, 2>), grid, dim3(128), 0, st, a, L);
   else hipLaunchKernelGGL((k_attn_tile<D, FP8, SEL, 4>), grid, dim3(256), 0, st, a, L);
-  if (L.n_splits > 1)
-    hipLaunchKernelGGL((k_attn_tile_join<D, SEL>), dim3(L.n_units, a.n_kv_heads, NW * 8), dim3(256), 0, st, a, L, NW * 32);
   return hipGetLastError();
 }
 
