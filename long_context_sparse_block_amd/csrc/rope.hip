@@ -180,13 +180,11 @@ hipError_t launch_rope(const misa_rope_spec& spec, const void* x, int dtype, int
 template <bool FP8>
 struct Turn {
   using T = double;
-  using T2 = double2;
   static __device__ __forceinline__ double2 of(double turns, double m) { return turn_f64(turns, m); }
 };
 template <>
 struct Turn<false> {
   using T = float;
-  using T2 = float2;
   static __device__ __forceinline__ float2 of(double turns, double m) { return turn_f32(turns, m); }
 };
 
@@ -199,66 +197,104 @@ __device__ __forceinline__ void unpack8(uint4 w4, float* x) {
   }
 }
 
-template <bool FP8>
-__global__ void __launch_bounds__(kThreads) k_write_pages(
-    const uint16_t* __restrict__ k, int64_t k_st, int64_t k_sh, const uint16_t* __restrict__ v, int64_t v_st,
-    int64_t v_sh, const int64_t* __restrict__ slots, int64_t n_tokens, int H, int D, int lpr_log2, int TT,
-    int64_t n_slots, void* __restrict__ k_pages, void* __restrict__ v_pages, float* __restrict__ k_scale,
-    float* __restrict__ v_scale, RopeArgs r) {
+// A thread keeps its head and side (k or v) and steps through tokens: the
+// divisions are done once, and a row's addresses are a product each.
+struct WriteArgs {
+  const uint16_t *k, *v;   // v nullable
+  int64_t k_st, k_sh, v_st, v_sh;
+  const int64_t* slots;
+  int64_t n_tokens, n_slots;
+  int H, D, lpr_log2, TT;
+  void *k_pages, *v_pages;
+  float *k_scale, *v_scale;
+};
+
+// How the keys turn: not at all; whole pieces, half layout (all 8 values of a
+// piece on one side, their partners in one other piece); whole pieces,
+// interleaved (partners side by side); any other offsets.
+enum { kStill = 0, kHalf = 1, kPairs = 2, kAny = 3 };
+
+template <bool FP8, int KIND>
+__global__ void __launch_bounds__(kThreads) k_write_pages(const WriteArgs a, const RopeArgs r) {
   using Tn = Turn<FP8>;
   using T = typename Tn::T;
-  extern __shared__ double2 s_raw[];
-  typename Tn::T2* const s_cs = reinterpret_cast<typename Tn::T2*>(s_raw);   // [TT][half]
-  const int lpr = 1 << lpr_log2;
-  const int p = threadIdx.x & (lpr - 1);
-  const int e0 = p * 8;
-  const bool live = e0 < D;
-  const int sides = v != nullptr ? 2 : 1;
-  const int rows_per_pass = kThreads >> lpr_log2;
+  extern __shared__ double s_raw[];
+  T* const s_c = reinterpret_cast<T*>(s_raw);   // [TT][half] cosines, then sines
+  T* const s_s = s_c + a.TT * r.half;
+  const int lpr = 1 << a.lpr_log2, p = threadIdx.x & (lpr - 1), e0 = p * 8;
+  const int grp = threadIdx.x >> a.lpr_log2, groups = kThreads >> a.lpr_log2;
+  // a token's rows over the groups of lanes: several tokens to a pass, or several passes to a token
+  const int rpt = a.H * (a.v != nullptr ? 2 : 1);
+  const int tpp = max(1, groups / rpt), chunks = (rpt + groups - 1) / groups;
+  const int sub = chunks == 1 ? grp / rpt : 0, hs0 = chunks == 1 ? grp - sub * rpt : grp;
+  const bool live = e0 < a.D;
   const bool hl = r.layout == MISA_ROPE_HALF;
-  // whole pieces: all 8 values of a piece are on one side, their partners in one other piece
-  const bool whole = hl ? r.start % 8 == 0 && r.half % 8 == 0 : r.start % 2 == 0;
-  const bool turns = r.half > 0 && live && e0 + 8 > r.start && e0 < r.start + 2 * r.half;   // (of k rows)
-  for (int64_t t0 = (int64_t)blockIdx.x * TT; t0 < n_tokens; t0 += (int64_t)gridDim.x * TT) {
-    const int nt = (int)min((int64_t)TT, n_tokens - t0);
-    if (r.half > 0) {
+  const int q0 = e0 - r.start;   // first value's place in the rotary part
+  const bool turns = KIND != kStill && live && q0 + 8 > 0 && q0 < 2 * r.half;   // (of k rows)
+  const bool second0 = q0 >= r.half;
+  struct Row {
+    uint4 mine, other;
+    int64_t slot;
+    const uint16_t* src;
+    int t, h;
+    bool is_v;
+  };
+  for (int64_t t0 = (int64_t)blockIdx.x * a.TT; t0 < a.n_tokens; t0 += (int64_t)gridDim.x * a.TT) {
+    const int nt = (int)min((int64_t)a.TT, a.n_tokens - t0);
+    const int items = (nt + tpp - 1) / tpp * chunks;
+    auto fetch = [&](int it) __attribute__((always_inline)) -> Row {
+      Row w;
+      const int pass = chunks == 1 ? it : it / chunks;
+      const int hs = chunks == 1 ? hs0 : hs0 + (it - pass * chunks) * groups;
+      const int t = pass * tpp + sub;
+      const bool in = it < items && sub < tpp && t < nt && hs < rpt;
+      w.t = min(t, nt - 1);
+      const int hc = min(hs, rpt - 1);
+      w.is_v = hc >= a.H;
+      w.h = w.is_v ? hc - a.H : hc;
+      const int64_t slot = a.slots[t0 + w.t];
+      w.slot = in ? slot : -1;
+      w.src = w.is_v ? a.v + (t0 + w.t) * a.v_st + w.h * a.v_sh : a.k + (t0 + w.t) * a.k_st + w.h * a.k_sh;
+      w.mine = live ? *reinterpret_cast<const uint4*>(w.src + e0) : make_uint4(0, 0, 0, 0);
+      w.other = w.mine;
+      if (KIND == kHalf && turns && !w.is_v)
+        w.other = *reinterpret_cast<const uint4*>(w.src + (second0 ? e0 - r.half : e0 + r.half));
+      return w;
+    };
+    // the first row's loads are under way while the table is formed (two or four
+    // rows' cost more in registers, and so in waves, than they gain)
+    Row w = fetch(0);
+    if (KIND != kStill) {
       for (int i = threadIdx.x; i < nt * r.half; i += kThreads) {
         const int t = i / r.half, j = i - t * r.half;
-        s_cs[i] = Tn::of((double)r.positions[t0 + t] * (r.inv_freq[j] * kInv2Pi), r.mscale);
+        const auto cs = Tn::of((double)r.positions[t0 + t] * (r.inv_freq[j] * kInv2Pi), r.mscale);
+        s_c[i] = cs.x;
+        s_s[i] = cs.y;
       }
       __syncthreads();
     }
-    const int rows = nt * H * sides;
-    for (int row0 = 0; row0 < rows; row0 += rows_per_pass) {
-      const int row = row0 + (int)(threadIdx.x >> lpr_log2);
-      if (row >= rows) continue;   // uniform over a row's lanes
-      const int t = row / (H * sides), hs = row - t * (H * sides);
-      const bool is_v = hs >= H;
-      const int h = is_v ? hs - H : hs;
-      const int64_t slot = slots[t0 + t];
-      if (slot < 0 || slot >= n_slots) continue;
-      const uint16_t* src = is_v ? v + (t0 + t) * v_st + h * v_sh : k + (t0 + t) * k_st + h * k_sh;
+    for (int it = 0; it < items; ++it) {
+      if (it > 0) w = fetch(it);
+      if (w.slot < 0 || w.slot >= a.n_slots) continue;   // uniform over a row's lanes
       float x[8];
-      unpack8(live ? *reinterpret_cast<const uint4*>(src + e0) : make_uint4(0, 0, 0, 0), x);
-      if (turns && !is_v) {
-        const typename Tn::T2* cs = s_cs + t * r.half;
-        const int q0 = e0 - r.start;   // first value's place in the rotary part
-        if (whole && hl) {
-          const bool second = q0 >= r.half;
-          const int j0 = second ? q0 - r.half : q0;
+      unpack8(w.mine, x);
+      if (turns && !w.is_v) {
+        const T *c = s_c + w.t * r.half, *s = s_s + w.t * r.half;
+        if constexpr (KIND == kHalf) {
+          const int j0 = second0 ? q0 - r.half : q0;
           float y[8];
-          unpack8(*reinterpret_cast<const uint4*>(src + (second ? e0 - r.half : e0 + r.half)), y);
+          unpack8(w.other, y);
 #pragma unroll
           for (int i = 0; i < 8; ++i)   // first: a c - b s; second: b c + a s
-            x[i] = (float)((T)x[i] * cs[j0 + i].x + (T)(second ? y[i] : -y[i]) * cs[j0 + i].y);
-        } else if (whole) {
+            x[i] = (float)((T)x[i] * c[j0 + i] + (T)(second0 ? y[i] : -y[i]) * s[j0 + i]);
+        } else if constexpr (KIND == kPairs) {
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
             const int q = q0 + i;
             if (q < 0 || q >= 2 * r.half) continue;
-            const T a = x[i], b = x[i + 1], c = cs[q >> 1].x, s = cs[q >> 1].y;
-            x[i] = (float)(a * c - b * s);
-            x[i + 1] = (float)(b * c + a * s);
+            const T a0 = x[i], b0 = x[i + 1], cj = c[q >> 1], sj = s[q >> 1];
+            x[i] = (float)(a0 * cj - b0 * sj);
+            x[i + 1] = (float)(b0 * cj + a0 * sj);
           }
         } else {
 #pragma unroll
@@ -268,12 +304,12 @@ __global__ void __launch_bounds__(kThreads) k_write_pages(
             const bool second = hl ? q >= r.half : (q & 1);
             const int j = hl ? (second ? q - r.half : q) : q >> 1;
             const int other = hl ? (second ? q - r.half : q + r.half) : q ^ 1;
-            const T mine = x[i], his = bf16_bits_to_f32(src[r.start + other]);
-            x[i] = (float)(mine * cs[j].x + (second ? his : -his) * cs[j].y);
+            const T mine = x[i], his = bf16_bits_to_f32(w.src[r.start + other]);
+            x[i] = (float)(mine * c[j] + (second ? his : -his) * s[j]);
           }
         }
       }
-      const int64_t dst_row = slot * H + h;
+      const int64_t dst_row = w.slot * a.H + w.h;
       if constexpr (FP8) {
         float amax = 0.f;
 #pragma unroll
@@ -288,17 +324,17 @@ __global__ void __launch_bounds__(kThreads) k_write_pages(
           u = __builtin_amdgcn_cvt_pk_fp8_f32(__fdiv_rn(x[4 * i + 2], s), __fdiv_rn(x[4 * i + 3], s), u, true);
           c[i] = (uint32_t)u;
         }
-        uint8_t* pool = static_cast<uint8_t*>(is_v ? v_pages : k_pages);
-        if (live) *reinterpret_cast<uint2*>(pool + dst_row * D + e0) = make_uint2(c[0], c[1]);
-        if (p == 0) (is_v ? v_scale : k_scale)[dst_row] = s;
+        uint8_t* pool = static_cast<uint8_t*>(w.is_v ? a.v_pages : a.k_pages);
+        if (live) *reinterpret_cast<uint2*>(pool + dst_row * a.D + e0) = make_uint2(c[0], c[1]);
+        if (p == 0) (w.is_v ? a.v_scale : a.k_scale)[dst_row] = s;
       } else {
-        uint16_t* pool = static_cast<uint16_t*>(is_v ? v_pages : k_pages);
+        uint16_t* pool = static_cast<uint16_t*>(w.is_v ? a.v_pages : a.k_pages);
         if (live)
-          *reinterpret_cast<uint4*>(pool + dst_row * D + e0) =
+          *reinterpret_cast<uint4*>(pool + dst_row * a.D + e0) =
               make_uint4(pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3]), pk_bf16(x[4], x[5]), pk_bf16(x[6], x[7]));
       }
     }
-    if (r.half > 0) __syncthreads();   // the table is free for the next tokens
+    if (KIND != kStill) __syncthreads();   // the table is free for the next tokens
   }
 }
 
@@ -310,19 +346,32 @@ hipError_t launch_write_pages(int64_t n_tokens, int H, int D, const uint16_t* k,
   if (spec != nullptr) r = rope_args(*spec);
   int lpr_log2 = 0;
   while ((8 << lpr_log2) < D) ++lpr_log2;
-  // tokens of a workgroup: about one pass of its threads, table within 32 KB
+  // tokens of a workgroup: a row for every group of lanes, up to four where that
+  // leaves four workgroups to a CU; table within 32 KB
   const int64_t lanes = ((int64_t)H * (v != nullptr ? 2 : 1)) << lpr_log2;
-  const int64_t cs_bytes = kdtype == MISA_K_FP8_E4M3 ? sizeof(double2) : sizeof(float2);
+  const int64_t cs_bytes = 2 * (kdtype == MISA_K_FP8_E4M3 ? sizeof(double) : sizeof(float));
   int64_t TT = std::max<int64_t>(1, kThreads / lanes);
+  TT = std::max<int64_t>(TT, std::min<int64_t>(4 * kThreads / lanes, n_tokens / 1024));
   if (r.half > 0) TT = std::min<int64_t>(TT, std::max<int64_t>(1, 32768 / (r.half * cs_bytes)));
   const dim3 grid((unsigned)std::min<int64_t>((n_tokens + TT - 1) / TT, kMaxGroups));
   const size_t lds = (size_t)TT * r.half * cs_bytes;
-  if (kdtype == MISA_K_FP8_E4M3)
-    hipLaunchKernelGGL(k_write_pages<true>, grid, dim3(kThreads), lds, st, k, k_st, k_sh, v, v_st, v_sh, slots,
-                       n_tokens, H, D, lpr_log2, (int)TT, n_slots, k_pages, v_pages, k_scale, v_scale, r);
-  else
-    hipLaunchKernelGGL(k_write_pages<false>, grid, dim3(kThreads), lds, st, k, k_st, k_sh, v, v_st, v_sh, slots,
-                       n_tokens, H, D, lpr_log2, (int)TT, n_slots, k_pages, v_pages, k_scale, v_scale, r);
+  const WriteArgs a{k, v, k_st, k_sh, v_st, v_sh, slots, n_tokens, n_slots, H, D, lpr_log2, (int)TT,
+                    k_pages, v_pages, k_scale, v_scale};
+  const int kind = r.half == 0 ? kStill
+                   : r.layout == MISA_ROPE_HALF ? (r.start % 8 == 0 && r.half % 8 == 0 ? kHalf : kAny)
+                                                : (r.start % 2 == 0 ? kPairs : kAny);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kThreads), lds, st, a, r); };
+  if (kdtype == MISA_K_FP8_E4M3) {
+    if (kind == kStill) go(k_write_pages<true, kStill>);
+    else if (kind == kHalf) go(k_write_pages<true, kHalf>);
+    else if (kind == kPairs) go(k_write_pages<true, kPairs>);
+    else go(k_write_pages<true, kAny>);
+  } else {
+    if (kind == kStill) go(k_write_pages<false, kStill>);
+    else if (kind == kHalf) go(k_write_pages<false, kHalf>);
+    else if (kind == kPairs) go(k_write_pages<false, kPairs>);
+    else go(k_write_pages<false, kAny>);
+  }
   return hipGetLastError();
 }
 
