@@ -589,10 +589,14 @@ typedef struct {
  * reads kv head h / (n_heads / n_kv_heads),
  *   out = sum_{s <= p} softmax_s(scale * q . k[s]) v[s]
  *   lse = log sum_{s <= p} exp(scale * q . k[s])
- * A row that sees no key (kv_lens[b] = 0) gives out = 0, lse = -inf.
+ * A row that sees no key (or none with a score above -inf) gives out = 0, lse =
+ * -inf.
  * One call takes decodes (one new token), chunks and both mixed.  Products
- * accumulate in fp32; softmax statistics are fp32; the softmax weights are
- * rounded to bf16 for the product with v.
+ * accumulate in fp32; softmax statistics are fp32; the softmax weights enter
+ * the product with v as bf16 (in two parts where a kv head has few rows).
+ * NaN and infinity in the keys and values that a row sees take their course
+ * through the formulas; in a value among a sequence's new tokens they may reach
+ * its earlier new tokens too, never another sequence.
  * q: bf16.  out: bf16 [n_tokens][n_heads][head_dim] dense, lse: float
  * [n_tokens][n_heads] or NULL.  kv_lens[b] past max_pages * page_keys counts
  * as that.  ws: misa_attention_paged_workspace_bytes() bytes (16-byte

@@ -61,10 +61,10 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a, const JoinS
   float w[R], top[R], sum[R];
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    top[k] = ml[k].y > 0.f ? ml[k].x : -INFINITY;
+    top[k] = ml[k].y != 0.f ? ml[k].x : -INFINITY;
 #pragma unroll
     for (int x = 32; x >= 1; x >>= 1) top[k] = fmaxf(top[k], __shfl_xor(top[k], x));
-    w[k] = ml[k].y > 0.f ? exp2_raw(ml[k].x - top[k]) : 0.f;
+    w[k] = ml[k].y != 0.f ? exp2_raw(ml[k].x - top[k]) : 0.f;
     sum[k] = w[k] * ml[k].y;
 #pragma unroll
     for (int x = 32; x >= 1; x >>= 1) sum[k] += __shfl_xor(sum[k], x);
@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a, const JoinS
       v[k] = *reinterpret_cast<const f32x4*>(S.L.part_o + (pr + (int64_t)s * S.rows + k) * D + (lane % LR) * 4);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      const float ws = s0 + lane / LR < n ? __shfl(w[k], s) : 0.f;
+      const float all = __shfl(w[k], s);   // (by every lane: the lane asked has to be there)
+      const float ws = s0 + lane / LR < n ? all : 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e)   // an empty split wrote no output: whatever is there is not used
         o[k][e] = ws == 0.f ? o[k][e] : __builtin_fmaf(ws, v[k][e], o[k][e]);
@@ -99,11 +100,11 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a, const JoinS
     if (r >= nrows) return;
     const int qi = SEL ? 0 : r / G, qh = g * G + (SEL ? r : r - qi * G);
     const int64_t out_row = ((int64_t)tok0 + qi) * a.n_heads + qh;
-    const float inv = sum[k] > 0.f ? 1.f / sum[k] : 0.f;
+    const float inv = sum[k] != 0.f ? 1.f / sum[k] : 0.f;
     if (lane < LR)
       *reinterpret_cast<uint2*>(a.out + out_row * D + lane * 4) =
           make_uint2(pk_bf16(o[k][0] * inv, o[k][1] * inv), pk_bf16(o[k][2] * inv, o[k][3] * inv));
-    if (a.lse != nullptr && lane == 0) a.lse[out_row] = sum[k] > 0.f ? (top[k] + __log2f(sum[k])) * kLn2 : -INFINITY;
+    if (a.lse != nullptr && lane == 0) a.lse[out_row] = sum[k] != 0.f ? (top[k] + __log2f(sum[k])) * kLn2 : -INFINITY;
   }
 }
 

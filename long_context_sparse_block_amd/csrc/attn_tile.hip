@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
   // o[db][4 j + i] of the lane: element db 32 + 8 j + 4 h + i of row r
   if (in_use == 1) {
     if (!live) return;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
     uint16_t* dst = a.out + (qrow * a.n_heads + qh) * D;
 #pragma unroll
     for (int db = 0; db < DB; ++db)
@@ -390,12 +390,12 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
       for (int j = 0; j < 4; ++j)
         *reinterpret_cast<uint2*>(dst + db * 32 + 8 * j + 4 * h) =
             make_uint2(pk_bf16(o[db][4 * j] * inv, o[db][4 * j + 1] * inv), pk_bf16(o[db][4 * j + 2] * inv, o[db][4 * j + 3] * inv));
-    if (a.lse != nullptr && h == 0) a.lse[qrow * a.n_heads + qh] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+    if (a.lse != nullptr && h == 0) a.lse[qrow * a.n_heads + qh] = l != 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
     return;
   }
   const int64_t pr = (((int64_t)unit * a.n_kv_heads + g) * L.n_splits + split) * BM + wave * 32 + c32;
   if (h == 0) L.part_ml[pr] = make_float2(m, l);
-  if (l > 0.f) {
+  if (l != 0.f) {
 #pragma unroll
     for (int db = 0; db < DB; ++db)
 #pragma unroll

@@ -17,11 +17,13 @@
 // takes one row a clock, 15 bytes a clock and CU; neighbours in the same row
 // make 28 to 44.)
 //
-// A tile of a wave is 8 RT + 8 RT (D = 128) v_mfma_f32_16x16x32_bf16.  Over bf16
-// pages, where the reading leaves the other units idle, the softmax weights
-// enter the second product as two bf16 parts (the rounded weight and what the
-// rounding left), so the weights keep 16 bits; over e4m3 pages, where the vector
-// unit is the busiest, as the rounded weight alone.
+// A tile of a wave is 8 RT + 16 RT (D = 128) v_mfma_f32_16x16x32_bf16: the softmax
+// weights enter the second product as two bf16 parts (the rounded weight and
+// what the rounding left), so the weights keep 16 bits.  The reading leaves the
+// other units room for it; one part alone took the same time for decodes (64 of
+// 8..16K keys, e4m3: 363 us) and 3% less over selected tokens (1000 x 2048,
+// e4m3: 243 to 249 us), but few rows with a few heavy keys average a weight's
+// rounding out too little.
 #include "attn_device.h"
 
 namespace misa {
@@ -264,11 +266,10 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 ? 2 : 1) k_attn_wave(const
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         hi[e] = pk_bf16(p[2 * e], p[2 * e + 1]);
-        if constexpr (!FP8)
-          lo[e] = pk_bf16(p[2 * e] - __uint_as_float(hi[e] << 16), p[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
+        lo[e] = pk_bf16(p[2 * e] - __uint_as_float(hi[e] << 16), p[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
       }
       ph[rt] = as_bf16x8(make_uint4(hi[0], hi[1], hi[2], hi[3]));
-      if constexpr (!FP8) pl[rt] = as_bf16x8(make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      pl[rt] = as_bf16x8(make_uint4(lo[0], lo[1], lo[2], lo[3]));
     }
 #pragma unroll
     for (int db = 0; db < DB; ++db) {
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 ? 2 : 1) k_attn_wave(const
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         o[rt][db] = mfma16(vf, ph[rt], o[rt][db]);
-        if constexpr (!FP8) o[rt][db] = mfma16(vf, pl[rt], o[rt][db]);
+        o[rt][db] = mfma16(vf, pl[rt], o[rt][db]);
       }
     }
   };
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 ? 2 : 1) k_attn_wave(const
     sum[rt] = 0.f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w)
-      sum[rt] += s_m[w][row] == -INFINITY ? 0.f : s_l[w][row] * exp2_raw(s_m[w][row] - top[rt]);
+      sum[rt] += s_l[w][row] == 0.f ? 0.f : s_l[w][row] * exp2_raw(s_m[w][row] - top[rt]);
     const float f = m[rt] == -INFINITY ? 0.f : exp2_raw(m[rt] - top[rt]);
 #pragma unroll
     for (int db = 0; db < DB; ++db) o[rt][db] *= f;
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 ? 2 : 1) k_attn_wave(const
     // o[rt][db][i]: element db 16 + 4 g4 + i
     if (in_use > 1) {
       if (g4 == 0) L.part_ml[part + row] = make_float2(top[rt], sum[rt]);
-      if (sum[rt] > 0.f)
+      if (sum[rt] != 0.f)
 #pragma unroll
         for (int db = 0; db < DB; ++db)
           *reinterpret_cast<f32x4*>(L.part_o + (part + row) * D + db * 16 + 4 * g4) = o[rt][db];
@@ -423,12 +424,12 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 ? 2 : 1) k_attn_wave(const
     }
     const int qi = SEL ? 0 : row / G, qh = g * G + (SEL ? row : row - qi * G);
     const int64_t orow = ((int64_t)tok0 + qi) * a.n_heads + qh;
-    const float inv = sum[rt] > 0.f ? 1.f / sum[rt] : 0.f;
+    const float inv = sum[rt] != 0.f ? 1.f / sum[rt] : 0.f;
 #pragma unroll
     for (int db = 0; db < DB; ++db)
       *reinterpret_cast<uint2*>(a.out + orow * D + db * 16 + 4 * g4) =
           make_uint2(pk_bf16(o[rt][db][0] * inv, o[rt][db][1] * inv), pk_bf16(o[rt][db][2] * inv, o[rt][db][3] * inv));
-    if (a.lse != nullptr && g4 == 0) a.lse[orow] = sum[rt] > 0.f ? (top[rt] + __log2f(sum[rt])) * kLn2 : -INFINITY;
+    if (a.lse != nullptr && g4 == 0) a.lse[orow] = sum[rt] != 0.f ? (top[rt] + __log2f(sum[rt])) * kLn2 : -INFINITY;
   }
 }
 

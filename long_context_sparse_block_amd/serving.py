@@ -101,12 +101,21 @@ def _rows(t, dtypes, name, dev, shape=None):
     return t.data_ptr(), (st if T > 1 else 0), (sh if H > 1 else 0)
 
 
-def _call(name, fn, dev, stream, *args):
-    """fn(*args, stream handle) on GPU `dev`."""
+def _on(stream, f, *args):
+    """f(*args) with `stream` as the current one: what f allocates is then
+    `stream`'s own memory, which no work of another stream may still be using."""
+    if not isinstance(stream, torch.cuda.Stream):
+        raise ValueError(f"stream: {stream!r}, expected a torch.cuda.Stream")
+    with torch.cuda.stream(stream):
+        return f(*args)
+
+
+def _call(name, fn, dev, *args):
+    """fn(*args, current stream's handle) on GPU `dev`."""
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            return _call(name, fn, dev, stream, *args)
-    st = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+            return _call(name, fn, dev, *args)
+    st = fn(*args, _raw_stream(dev))
     if st != 0:
         _check(st, name)
 
@@ -117,6 +126,8 @@ def misa_plan_pages(cached_lens, new_lens, free_pages, block_table, page_keys: i
     block_table [n_seq, max_pages] (int32, in place) from free_pages (int32) and
     returns the PagePlan.  n_tokens: length of the slot map (at least the sum of
     new_lens; entries behind the last token get slot -1)."""
+    if stream is not None:
+        return _on(stream, misa_plan_pages, cached_lens, new_lens, free_pages, block_table, page_keys, n_tokens, plan)
     dev = _dev(cached_lens, "cached_lens")
     n = cached_lens.shape[0]
     i32 = torch.int32
@@ -133,7 +144,7 @@ def misa_plan_pages(cached_lens, new_lens, free_pages, block_table, page_keys: i
                 _dense(plan.positions, i32, (n_tokens,), "positions", dev), n_tokens,
                 _dense(plan.n_taken, i32, (1,), "n_taken", dev))
     n_free, width = free_pages.shape[0], block_table.shape[-1]
-    _call("misa_plan_pages", load().misa_plan_pages, dev, stream, n, _dense(cached_lens, i32, (n,), "cached_lens", dev),
+    _call("misa_plan_pages", load().misa_plan_pages, dev, n, _dense(cached_lens, i32, (n,), "cached_lens", dev),
           _dense(new_lens, i32, (n,), "new_lens", dev), page_keys, _dense(free_pages, i32, (n_free,), "free_pages", dev),
           n_free, _dense(block_table, i32, (n, width), "block_table", dev), width, *outs)
     return plan
@@ -194,6 +205,8 @@ def misa_rope(x, positions, inv_freq, layout: str = "half", rot_start: int = 0, 
     rotary part is elements rot_start .. rot_start + 2 len(inv_freq) - 1 of a
     head.  backward: the gradient with respect to x of x -> misa_rope(x, ...),
     given the gradient of its output.  out may be x (in place)."""
+    if stream is not None:
+        return _on(stream, misa_rope, x, positions, inv_freq, layout, rot_start, mscale, backward, out)
     dev = _dev(x, "x")
     xp, xst, xsh = _rows(x, _DTYPES, "x", dev)
     T, H, D = x.shape
@@ -202,7 +215,7 @@ def misa_rope(x, positions, inv_freq, layout: str = "half", rot_start: int = 0, 
     op, ost, osh = _rows(out, (x.dtype,), "out", dev, x.shape)
     spec = _rope_spec(positions, inv_freq, layout, rot_start, mscale, backward, T, dev)
     if T > 0:
-        _call("misa_rope", load().misa_rope, dev, stream, spec, xp, _DTYPES[x.dtype], T, H, D, xst, xsh, op, ost, osh)
+        _call("misa_rope", load().misa_rope, dev, spec, xp, _DTYPES[x.dtype], T, H, D, xst, xsh, op, ost, osh)
     return out
 
 
@@ -234,6 +247,9 @@ def misa_write_pages(k, slots, k_pages, k_scale_pages=None, v=None, v_pages=None
     head dimension out, as misa_indexer_paged takes them.  Given positions and
     inv_freq, k is rotated first (misa_rope).  Slots outside the pool are
     skipped."""
+    if stream is not None:
+        return _on(stream, misa_write_pages, k, slots, k_pages, k_scale_pages, v, v_pages, v_scale_pages, positions,
+                   inv_freq, layout, rot_start, mscale)
     dev = _dev(k, "k")
     kp, kst, ksh = _rows(k, _BF16, "k", dev)
     T, H, D = k.shape
@@ -256,7 +272,7 @@ def misa_write_pages(k, slots, k_pages, k_scale_pages=None, v=None, v_pages=None
     if inv_freq is not None:
         spec = _rope_spec(positions, inv_freq, layout, rot_start, mscale, False, T, dev)
     if T > 0:
-        _call("misa_write_pages", load().misa_write_pages, dev, stream, T, H, D, kp, kst, ksh, vp, vst or 0, vsh or 0, sp,
+        _call("misa_write_pages", load().misa_write_pages, dev, T, H, D, kp, kst, ksh, vp, vst or 0, vsh or 0, sp,
               spec, kpool, vpool, kd, ks, vs, n_pages, page_keys)
 
 
@@ -270,6 +286,9 @@ def misa_attention_selected_workspace_bytes(shape: AttnShape, pages: KvPages, to
 
 def _attention(name, q, k_pages, v_pages, block_table, q_start, kv_lens, idx, k_scale, v_scale, scale, max_new, out, lse,
                want_lse, ws, stream):
+    if stream is not None:
+        return _on(stream, _attention, name, q, k_pages, v_pages, block_table, q_start, kv_lens, idx, k_scale, v_scale,
+                   scale, max_new, out, lse, want_lse, ws, None)
     dev = _dev(q, "q")
     qp, qst, qsh = _rows(q, _BF16, "q", dev)
     T, H, D = q.shape
@@ -313,14 +332,12 @@ def _attention(name, q, k_pages, v_pages, block_table, q_start, kv_lens, idx, k_
                 else lib.misa_attention_selected_workspace_bytes(shape, pages, topk))
         if need:
             ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-            if stream is not None:   # its memory may be handed on once `stream` has passed this call
-                ws.record_stream(stream)
     elif ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"ws must be a dense tensor on cuda:{dev}")
     if ws is None:
-        _call(name, fn, dev, stream, *args, None, 0)
+        _call(name, fn, dev, *args, None, 0)
     else:
-        _call(name, fn, dev, stream, *args, ws.data_ptr(), ws.numel() * ws.element_size())
+        _call(name, fn, dev, *args, ws.data_ptr(), ws.numel() * ws.element_size())
     return out, lse
 
 
