@@ -270,9 +270,9 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
       float p[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) p[e] = exp2_raw(__builtin_fmaf(s[kb][e], sc, -mu));
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      float sum[4] = {p[0], p[1], p[2], p[3]};
 #pragma unroll
-      for (int e = 0; e < 16; ++e) sum[e & 3] += p[e];
+      for (int e = 4; e < 16; ++e) sum[e & 3] += p[e];
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if constexpr (FP8) {
 #pragma unroll

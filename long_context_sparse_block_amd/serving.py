@@ -134,7 +134,7 @@ def misa_plan_pages(cached_lens, new_lens, free_pages, block_table, page_keys: i
     if plan is None:
         slots = torch.empty(n_tokens, dtype=torch.int64, device=cached_lens.device)
         rest = torch.empty(2 * n + 2 + n_tokens, dtype=i32, device=cached_lens.device)
-        q_start, kv_lens, positions, n_taken = rest.split((n + 1, n, n_tokens, 1))
+        q_start, kv_lens, positions, n_taken = torch.unsafe_split_with_sizes(rest, (n + 1, n, n_tokens, 1))
         plan = PagePlan(q_start, kv_lens, slots, positions, n_taken)
         at = rest.data_ptr()
         outs = (at, at + 4 * (n + 1), slots.data_ptr(), at + 4 * (2 * n + 1), n_tokens, at + 4 * (2 * n + 1 + n_tokens))
