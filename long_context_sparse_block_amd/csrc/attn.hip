@@ -6,6 +6,7 @@
 // sequence's new tokens.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "attn_device.h"
 
@@ -17,9 +18,10 @@ hipError_t launch_attn_wave(const AttnArgs& a, const AttnLaunch& L, int D, bool 
 namespace {
 
 // The joins of a call's launches in one: workgroups below n_tile join
-// attn_tile's units (BM rows each), the others attn_wave's (16 RT rows), 16
-// rows a workgroup and 4 a wave, whose loads are all under way together (a row
-// a wave took four times as long: 46k rows of two to seven splits in 19 us).
+// attn_tile's units (BM rows each), the others attn_wave's (16 RT rows).  D / 4
+// lanes take a row, 16 bytes of every split each, and go through the splits four
+// or eight at a time with a running maximum: each lane forms the row's weights
+// by itself, so lanes exchange nothing.
 struct JoinSide {
   AttnLaunch L;
   int rows;   // of a unit's part of the workspace
@@ -28,14 +30,13 @@ struct JoinSide {
 template <int D, bool SEL>
 __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a, const JoinSide tile, const JoinSide wave,
                                                    uint32_t n_tile) {
-  constexpr int LR = D / 4, kGroups = kWave / LR, R = 4;   // lanes of a row, rows' splits read side by side, rows
+  constexpr int LR = D / 4, RW = 256 / LR;   // lanes of a row, rows of a workgroup
   const bool is_tile = blockIdx.x < n_tile;
   const JoinSide& S = is_tile ? tile : wave;
   const uint32_t i = is_tile ? blockIdx.x : blockIdx.x - n_tile;
-  const int lane = threadIdx.x & 63;
   const int G = a.n_heads / a.n_kv_heads;
-  const uint32_t per = (uint32_t)S.rows / 16;   // workgroups of a unit and kv head
-  const int rr0 = (int)(i % per) * 16 + (int)(threadIdx.x >> 6) * R;
+  const uint32_t per = (uint32_t)S.rows / RW;   // workgroups of a unit and kv head
+  const int rr = (int)(i % per) * RW + (int)threadIdx.x / LR, piece = (int)threadIdx.x % LR;
   const int g = (int)(i / per % (uint32_t)a.n_kv_heads), unit = (int)(i / per / (uint32_t)a.n_kv_heads);
   int r0, nrows, tok0, n = S.L.n_splits;
   if (SEL) {
@@ -51,61 +52,47 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a, const JoinS
     nrows = u.z;
     n = u.w;
   }
-  if (n <= 1 || r0 + rr0 >= nrows) return;   // written by the unit itself, or no row
-  const int64_t pr = (((int64_t)unit * a.n_kv_heads + g) * S.L.n_splits) * S.rows + rr0;
-  // lane s: split s's weight of each row
-  float2 ml[R];
+  const int r = r0 + rr;
+  if (n <= 1 || r >= nrows) return;   // written by the unit itself, or no row
+  const int64_t pr = (((int64_t)unit * a.n_kv_heads + g) * S.L.n_splits) * S.rows + rr;
+  const float2* const ml = S.L.part_ml + pr;
+  const float* const po = S.L.part_o + pr * D + piece * 4;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  float top = -INFINITY, sum = 0.f;
+  auto some = [&](int s0, auto count) __attribute__((always_inline)) {
+    constexpr int U = decltype(count)::value;
+    float2 x[U];
+    f32x4 v[U];
 #pragma unroll
-  for (int k = 0; k < R; ++k)
-    ml[k] = lane < n && r0 + rr0 + k < nrows ? S.L.part_ml[pr + (int64_t)lane * S.rows + k] : make_float2(-INFINITY, 0.f);
-  float w[R], top[R], sum[R];
+    for (int k = 0; k < U; ++k) x[k] = ml[(int64_t)min(s0 + k, n - 1) * S.rows];
 #pragma unroll
-  for (int k = 0; k < R; ++k) {
-    top[k] = ml[k].y != 0.f ? ml[k].x : -INFINITY;
+    for (int k = 0; k < U; ++k) v[k] = *reinterpret_cast<const f32x4*>(po + (int64_t)min(s0 + k, n - 1) * S.rows * D);
+    float most = top;
 #pragma unroll
-    for (int x = 32; x >= 1; x >>= 1) top[k] = fmaxf(top[k], __shfl_xor(top[k], x));
-    w[k] = ml[k].y != 0.f ? exp2_raw(ml[k].x - top[k]) : 0.f;
-    sum[k] = w[k] * ml[k].y;
+    for (int k = 0; k < U; ++k) most = fmaxf(most, x[k].y != 0.f ? x[k].x : -INFINITY);
+    const float keep = top == -INFINITY ? 0.f : exp2_raw(top - most);   // (nothing to keep before the first)
+    top = most;
+    o *= keep;
+    sum *= keep;
 #pragma unroll
-    for (int x = 32; x >= 1; x >>= 1) sum[k] += __shfl_xor(sum[k], x);
-  }
-  // D / 4 lanes read a split's row, 16 bytes each, the wave's groups of such
-  // lanes the splits in turn.  Fixed order.
-  f32x4 o[R] = {};
-#pragma unroll 2
-  for (int s0 = 0; s0 < n; s0 += kGroups) {
-    const int s = min(s0 + lane / LR, n - 1);
-    f32x4 v[R];
+    for (int k = 0; k < U; ++k) {
+      // an empty split wrote no output: whatever is there is not used
+      const float w = s0 + k < n && x[k].y != 0.f ? exp2_raw(x[k].x - most) : 0.f;
+      sum = w == 0.f ? sum : __builtin_fmaf(w, x[k].y, sum);
 #pragma unroll
-    for (int k = 0; k < R; ++k)
-      v[k] = *reinterpret_cast<const f32x4*>(S.L.part_o + (pr + (int64_t)s * S.rows + k) * D + (lane % LR) * 4);
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const float all = __shfl(w[k], s);   // (by every lane: the lane asked has to be there)
-      const float ws = s0 + lane / LR < n ? all : 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)   // an empty split wrote no output: whatever is there is not used
-        o[k][e] = ws == 0.f ? o[k][e] : __builtin_fmaf(ws, v[k][e], o[k][e]);
+      for (int e = 0; e < 4; ++e) o[e] = w == 0.f ? o[e] : __builtin_fmaf(w, v[k][e], o[e]);
     }
-  }
-#pragma unroll
-  for (int x = LR; x < kWave; x <<= 1)
-#pragma unroll
-    for (int k = 0; k < R; ++k)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[k][e] += __shfl_xor(o[k][e], x);
-#pragma unroll
-  for (int k = 0; k < R; ++k) {
-    const int r = r0 + rr0 + k;
-    if (r >= nrows) return;
-    const int qi = SEL ? 0 : r / G, qh = g * G + (SEL ? r : r - qi * G);
-    const int64_t out_row = ((int64_t)tok0 + qi) * a.n_heads + qh;
-    const float inv = sum[k] != 0.f ? 1.f / sum[k] : 0.f;
-    if (lane < LR)
-      *reinterpret_cast<uint2*>(a.out + out_row * D + lane * 4) =
-          make_uint2(pk_bf16(o[k][0] * inv, o[k][1] * inv), pk_bf16(o[k][2] * inv, o[k][3] * inv));
-    if (a.lse != nullptr && lane == 0) a.lse[out_row] = sum[k] != 0.f ? (top[k] + __log2f(sum[k])) * kLn2 : -INFINITY;
-  }
+  };
+  if (n <= 4)
+    some(0, std::integral_constant<int, 4>{});
+  else
+    for (int s0 = 0; s0 < n; s0 += 8) some(s0, std::integral_constant<int, 8>{});
+  const int qi = SEL ? 0 : r / G, qh = g * G + (SEL ? r : r - qi * G);
+  const int64_t out_row = ((int64_t)tok0 + qi) * a.n_heads + qh;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  *reinterpret_cast<uint2*>(a.out + out_row * D + piece * 4) =
+      make_uint2(pk_bf16(o[0] * inv, o[1] * inv), pk_bf16(o[2] * inv, o[3] * inv));
+  if (a.lse != nullptr && piece == 0) a.lse[out_row] = sum != 0.f ? (top + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
 struct AttnPlan {
@@ -240,8 +227,9 @@ hipError_t launch_attention(const misa_attn_shape& s, const misa_kv_pages& pg, c
   hipError_t e = hipSuccess;
   if (p.NW > 0) e = launch_attn_tile(a, T, s.head_dim, fp8, p.NW, st);
   if (e == hipSuccess && p.RT > 0) e = launch_attn_wave(a, W, s.head_dim, fp8, p.RT, st);
-  const int64_t n_tile = p.NW > 0 && p.tile_splits > 1 ? (int64_t)p.tile_units * s.n_kv_heads * p.NW * 2 : 0;
-  const int64_t n_wave = p.RT > 0 && p.wave_splits > 1 ? (int64_t)p.wave_units * s.n_kv_heads * p.RT : 0;
+  const int lanes = s.head_dim / 4;   // of a row
+  const int64_t n_tile = p.NW > 0 && p.tile_splits > 1 ? (int64_t)p.tile_units * s.n_kv_heads * p.NW * 32 * lanes / 256 : 0;
+  const int64_t n_wave = p.RT > 0 && p.wave_splits > 1 ? (int64_t)p.wave_units * s.n_kv_heads * p.RT * 16 * lanes / 256 : 0;
   if (e != hipSuccess || n_tile + n_wave == 0) return e;
   const JoinSide jt{T, 32 * p.NW}, jw{W, 16 * p.RT};
   const dim3 grid((unsigned)(n_tile + n_wave));
