@@ -165,26 +165,79 @@ struct AttnLaunch {
   int4* unit_info;
 };
 
-// Sums over the sequences of a dense launch, for one kv head
+// What a dense launch's lengths are, for one kv head, and the split made of them
 struct DenseScan {
   float steps;   // key tiles of all units together
   int units;
   int longest;   // key tiles of one unit, at most
+  int per;       // key tiles of a split (0: not scanned)
 };
 
-// Key tiles of a split.  Lengths differ within a batch, and a unit's share of
-// the splits should follow its own: all splits are equally long, two to each
-// workgroup that the GPU holds.  No splits where the units are one full round
-// of nearly equal length (they would only add rounds), or so many that they
-// balance by themselves.
-__device__ __forceinline__ int split_tiles(const DenseScan& w, const AttnLaunch& L, int kv_heads, int n, int least) {
-  if (w.units == 0) return (n + L.n_splits - 1) / L.n_splits;   // selected tokens, or no scan: even shares
+// Key tiles of a split.  Lengths differ within a batch, and a unit's share of the
+// splits should follow its own, so all splits are about equally long.
+//
+// attn_wave, bound by the card's reading: two splits to each workgroup that the
+// GPU holds.  No splits where the units are one full round of nearly equal
+// length (they would only add rounds), or so many that they balance by
+// themselves.
+__device__ __forceinline__ int wave_per(const DenseScan& w, const AttnLaunch& L, int kv_heads) {
   const float fair = w.steps * (float)kv_heads / (float)L.slots;
   const float units = (float)w.units * (float)kv_heads;
-  int p = max(least, (int)ceilf(fair * 0.5f));
+  int p = max(16, (int)ceilf(fair * 0.5f));
   if (((float)w.longest <= 1.25f * fair && units <= 1.05f * (float)L.slots) || units >= 6.f * (float)L.slots)
     p = max(p, w.longest);
-  return max(p, (n + L.n_splits - 1) / L.n_splits);
+  return p;
+}
+
+// attn_tile, bound by each CU's own arithmetic: what counts is the CU with the
+// most tiles.  Some ways of cutting the longest unit are weighed, in tiles of a
+// CU: splits of p tiles make g workgroups, of which a CU gets ceil(g / 256), and
+// works at less than its full rate where fewer of them are resident than it
+// holds; a start costs about 2.5 us (1.6 tiles at head_dim 128, 4 at 64), and a
+// split's part is written, read and joined, about a hundredth of a tile of every
+// CU's time.  g is exact where the units are about equally long (one chunk, a
+// batch of equal ones); else the remainders count as half a split a unit, and
+// the CUs even out but for half a split.
+constexpr int kCuts = 9;
+template <int D>
+__device__ __forceinline__ int tile_per(const DenseScan& w, const AttnLaunch& L, int kv_heads) {
+  constexpr int cut[kCuts] = {1, 2, 3, 4, 5, 6, 8, 14, 32};
+  constexpr float start = D == 64 ? 4.f : 1.6f, cus = 256.f, held = D == 64 ? 3.f : 2.f;
+  constexpr float one = D == 64 ? 1 / 0.45f : 1 / 0.7f, two = D == 64 ? 2 / 0.8f : 2.f;   // tiles' time beside 1, 2
+  const int least = max(8, (w.longest + L.n_splits - 1) / L.n_splits);
+  const float heads = (float)kv_heads, longest = (float)w.longest, units = (float)w.units * heads;
+  const float fair = w.steps * heads / cus;
+  const bool alike = w.steps > 0.9f * (float)w.units * longest;
+  float best = longest, lowest = INFINITY;
+#pragma unroll
+  for (int j = 0; j < kCuts; ++j) {
+    const float per = fminf(longest, fmaxf((float)least, ceilf(longest * (1.f / cut[j]) - 1e-3f)));
+    const float inv = 1.f / fmaxf(per, 1.f);
+    float g, cost;
+    if (alike) {
+      g = units * ceilf(longest * inv - 1e-3f);
+      const float m = ceilf(g * (1.f / cus)), full = held * floorf(m * (1.f / held) + 1e-3f), rest = m - full;
+      cost = (full + (rest < 0.5f ? 0.f : rest < 1.5f ? one : two)) * (per + start);
+    } else {
+      g = j == 0 ? units : w.steps * heads * inv + 0.5f * units;
+      cost = fmaxf(fair + g * (start / cus) + 0.5f * per, one * (per + start));
+    }
+    if (per < longest) cost += g * 0.01f + start;
+    if (cost < lowest) {
+      lowest = cost;
+      best = per;
+    }
+  }
+  return __builtin_amdgcn_readfirstlane((int)best);
+}
+
+// Key tiles of each of a unit's splits (the last may have fewer), n in all
+__device__ __forceinline__ int split_tiles(const DenseScan& w, const AttnLaunch& L, int n, int* in_use) {
+  int per = n;
+  if (L.n_splits > 1) per = max(w.per, (n + L.n_splits - 1) / L.n_splits);   // no scan: even shares
+  per = max(per, 1);
+  *in_use = max(1, (n + per - 1) / per);
+  return per;
 }
 
 // Up to this many sequences a workgroup sums them all; more share their splits evenly
@@ -195,7 +248,7 @@ constexpr int kScanSeqs = 4096;
 // such tile).  Else unit is the sequence (false: not attn_wave's).  Fills
 // `scan` over the sequences of the launch's kind where splits need it.
 // Uniform.
-template <bool TILES, int KEYS>
+template <bool TILES, int KEYS, int D>
 __device__ __forceinline__ bool find_unit(const AttnArgs& a, const AttnLaunch& L, int G, int BM, int unit, int lane,
                                           SeqSpan* span, int* b_out, int* r0_out, DenseScan* scan) {
   const bool sums = L.n_splits > 1 && a.n_seq <= kScanSeqs;
@@ -217,11 +270,9 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, const AttnLaunch& L
       const bool in = b0 + lane * 4 + i < a.n_seq && rows > 0 && (rows > L.rows_min) == TILES;
       c[i] = in ? (TILES ? (int)((rows + BM - 1) / BM) : 1) : 0;
       sum += c[i];
-      if (in) {
-        const int n = (sp.len + KEYS - 1) / KEYS;
-        steps += (float)c[i] * (float)n;
-        longest = max(longest, n);
-      }
+      const int n = in ? (sp.len + KEYS - 1) / KEYS : 0;
+      steps += (float)c[i] * (float)n;
+      longest = max(longest, n);
     }
     units += sum;
     int src = -1, i = 0, left = 0;
@@ -282,9 +333,10 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, const AttnLaunch& L
       longest = max(longest, __shfl_xor(longest, x));
       units += __shfl_xor(units, x);
     }
-    *scan = DenseScan{steps, units, longest};
+    *scan = DenseScan{steps, units, longest, 0};
+    scan->per = TILES ? tile_per<D>(*scan, L, a.n_kv_heads) : wave_per(*scan, L, a.n_kv_heads);
   } else {
-    *scan = DenseScan{0.f, 0, 0};
+    *scan = DenseScan{0.f, 0, 0, 0};
   }
   return true;
 }
@@ -292,17 +344,20 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, const AttnLaunch& L
 // Workgroup -> (unit, kv head, split).  Workgroup i runs on XCD i mod 8, and the
 // units of one (kv head, split) read the same keys: where there are a
 // multiple of 8 such pairs, each goes to one XCD, whose L2 then holds the keys
-// for all its units; else neighbours go round the XCDs.
+// for all its units; else neighbours go round the XCDs.  Where an XCD would get
+// some splits only, of which a dense unit uses the first ones, the pairs move on
+// an XCD every 2^turn units, so that all XCDs get as many splits in use (8 x 256
+// tokens over 2700 keys, 4 kv heads, three of four splits in use: 117 -> 98 us).
 struct Place {
   int unit, g, split;
 };
-__device__ __forceinline__ Place place_of(const AttnLaunch& L, int kv_heads, uint32_t i) {
+__device__ __forceinline__ Place place_of(const AttnLaunch& L, int kv_heads, uint32_t i, int turn) {
   const uint32_t n = (uint32_t)L.n_units, pairs = (uint32_t)(kv_heads * L.n_splits);
   uint32_t pair, unit;
   if (pairs % 8 == 0) {
     const uint32_t j = i / 8;
-    pair = i % 8 + 8 * (j / n);
     unit = j % n;
+    pair = 8 * (j / n) + ((i + (kv_heads % 8 == 0 ? 0 : unit >> turn)) & 7);
   } else {
     pair = i / n;
     unit = i % n;

@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
   const int h = lane >> 5, c32 = lane & 31;
   const int G = a.n_heads / a.n_kv_heads;
 
-  const Place at = place_of(L, a.n_kv_heads, blockIdx.x);
+  const Place at = place_of(L, a.n_kv_heads, blockIdx.x, SEL ? 31 : 3);
   const int split = at.split, g = at.g;
   int unit = at.unit;
   int b, r0, nrows, tok0;      // sequence, first row, its rows in all, its first token
@@ -53,8 +53,7 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
   int in_use = 1;              // its unit's splits in use
   auto range = [&](const DenseScan& w) __attribute__((always_inline)) {
     const int n = (kend + kBN - 1) / kBN;
-    const int per = max(1, L.n_splits == 1 ? n : split_tiles(w, L, a.n_kv_heads, n, 8));
-    in_use = max(1, (n + per - 1) / per);
+    const int per = split_tiles(w, L, n, &in_use);
     jt0 = split * per;
     jt1 = min(n, jt0 + per);
   };
@@ -65,7 +64,7 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
     r0 = (unit % sub) * BM;
     nrows = G;
     kend = a.topk;
-    range(DenseScan{0.f, 0, 0});
+    range(DenseScan{0.f, 0, 0, 0});
     // on their way while the sequence is looked up
     pick0 = pick(a, tok0, jt0 * kBN + lane);
     pick1 = pick(a, tok0, jt0 * kBN + kBN + lane);
@@ -80,7 +79,7 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
     SeqSpan sp;
     DenseScan scan;
     const bool tell = L.n_splits > 1 && split == 0 && g == 0 && tid == 0;   // the join's directions
-    if (!find_unit<true, kBN>(a, L, G, BM, unit, lane, &sp, &b, &r0, &scan)) {
+    if (!find_unit<true, kBN, D>(a, L, G, BM, unit, lane, &sp, &b, &r0, &scan)) {
       if (tell) L.unit_info[unit] = make_int4(0, 0, 0, 0);
       return;
     }

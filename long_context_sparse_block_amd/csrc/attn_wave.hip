@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 ? 2 : 1) k_attn_wave(const
   const int g4 = lane >> 4, c16 = lane & 15;
   const int G = a.n_heads / a.n_kv_heads;
 
-  const Place at = place_of(L, a.n_kv_heads, blockIdx.x);
+  const Place at = place_of(L, a.n_kv_heads, blockIdx.x, SEL ? 31 : 0);
   const int split = at.split, g = at.g, unit = at.unit;
   int b, tok0, nrows, kend, kfull;   // sequence, first token, rows; keys some row sees, keys every row sees
   int64_t pos0;
@@ -63,8 +63,7 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 ? 2 : 1) k_attn_wave(const
   int in_use = 1;                    // the unit's splits in use
   auto range = [&](const DenseScan& w) __attribute__((always_inline)) {
     const int n = (kend + kWT - 1) / kWT;
-    const int per = max(1, L.n_splits == 1 ? n : split_tiles(w, L, a.n_kv_heads, n, 4 * kWaves));
-    in_use = max(1, (n + per - 1) / per);
+    const int per = split_tiles(w, L, n, &in_use);
     jt0 = split * per + wave;
     jt1 = min(n, (split + 1) * per);
   };
@@ -75,7 +74,7 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 ? 2 : 1) k_attn_wave(const
     tok0 = unit;
     nrows = G;
     kend = a.topk;
-    range(DenseScan{0.f, 0, 0});
+    range(DenseScan{0.f, 0, 0, 0});
     // on their way while the sequence is looked up
     pick0 = pick(a, tok0, jt0 * kWT + k_mine);
     pick1 = pick(a, tok0, (jt0 + kWaves) * kWT + k_mine);
@@ -90,7 +89,7 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 ? 2 : 1) k_attn_wave(const
     SeqSpan sp;
     DenseScan scan;
     int none;
-    if (!find_unit<false, kWT>(a, L, G, 1, unit, lane, &sp, &b, &none, &scan)) {
+    if (!find_unit<false, kWT, D>(a, L, G, 1, unit, lane, &sp, &b, &none, &scan)) {
       if (L.n_splits > 1 && split == 0 && g == 0 && tid == 0) L.unit_info[unit] = make_int4(0, 0, 0, 0);
       return;
     }
