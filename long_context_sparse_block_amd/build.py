@@ -1,4 +1,5 @@
-"""Build libmisa.so (HIP kernels + C ABI) for gfx950, in-tree.
+"""Build libmisa.so (HIP kernels + C ABI) for gfx950, and the Python wrappers'
+argument checks (_tensor_args.so, host code against torch's headers), in-tree.
 
     python -m long_context_sparse_block_amd.build
 
@@ -12,12 +13,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmisa.so")
+TENSOR_ARGS = os.path.join(PKG, "_tensor_args.so")
 ARCH = "gfx950"
 
 
@@ -30,6 +33,16 @@ def hipcc() -> str:
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.hip")))
+
+
+def tensor_args_command(out: str) -> list[str]:
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *(f"-I{p}" for p in [*include_paths(), sysconfig.get_paths()["include"]]),
+            os.path.join(CSRC, "tensor_args.cpp"), "-o", out, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
 def build_library(verbose: bool = False, extra=()) -> str:
@@ -49,6 +62,10 @@ def build_library(verbose: bool = False, extra=()) -> str:
             print(" ".join(cmd), flush=True)
         procs.append((src, cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
         objs.append(obj)
+    cmd = tensor_args_command(TENSOR_ARGS + ".tmp")
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    procs.append((os.path.join(CSRC, "tensor_args.cpp"), cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, cmd, p in procs:
         out, _ = p.communicate()
@@ -60,7 +77,8 @@ def build_library(verbose: bool = False, extra=()) -> str:
             print(text)
     if failed:
         msg = "\n\n".join(f"== {s}\n{t}" for s, t in failed)
-        raise RuntimeError(f"hipcc failed:\n{msg}")
+        raise RuntimeError(f"compilation failed:\n{msg}")
+    os.replace(TENSOR_ARGS + ".tmp", TENSOR_ARGS)
     tmp = LIB + ".tmp"
     link = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:

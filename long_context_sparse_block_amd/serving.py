@@ -73,7 +73,7 @@ def _dev(t, name):
     return d
 
 
-def _dense(t, dtype, shape, name, dev):
+def _dense_py(t, dtype, shape, name, dev):
     """Pointer of a dense tensor of this type and shape on GPU `dev`."""
     if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         _need(t, dtype, shape, name)
@@ -81,7 +81,7 @@ def _dense(t, dtype, shape, name, dev):
     return t.data_ptr()
 
 
-def _rows(t, dtypes, name, dev, shape=None):
+def _rows_py(t, dtypes, name, dev, shape=None):
     """Pointer, token and head strides of a [tokens, heads, head_dim] tensor whose
     last dimension is dense."""
     if t is None:
@@ -99,6 +99,12 @@ def _rows(t, dtypes, name, dev, shape=None):
         raise ValueError(f"{name}: the last dimension must be dense")
     # the strides of dimensions of one element mean nothing
     return t.data_ptr(), (st if T > 1 else 0), (sh if H > 1 else 0)
+
+
+try:   # the same checks in C++ (csrc/tensor_args.cpp), a quarter of the time
+    from ._tensor_args import dense as _dense, rows as _rows
+except ImportError:   # not built yet
+    _dense, _rows = _dense_py, _rows_py
 
 
 def _on(stream, f, *args):

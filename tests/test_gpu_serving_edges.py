@@ -270,3 +270,29 @@ def test_two_graphs_share_a_workspace():
             assert torch.equal(outs[n], base[n][0]), (rep, n)
             ws.fill_(rep)
             assert torch.equal(run(*jobs[n])[0], base[n][0])
+
+
+# ---------------------------------------------------------------- argument checks
+
+def outcome(check, *args):
+    try:
+        return check(*args)
+    except ValueError as e:
+        return str(e)
+
+
+def test_built_argument_checks_equal_the_plain_ones():
+    from long_context_sparse_block_amd import serving
+    x = torch.zeros((5, 4, 8), device="cuda")
+    one = torch.zeros((1, 1, 8), device="cuda")
+    for t in (x, x.half(), x[:, ::2], x[..., ::2], x.transpose(0, 1), x[:0], x[0], one, one.expand(5, 1, 8), x[:, :, :1]):
+        for dtype in (torch.float32, torch.int32):
+            for shape in ((5, 4, 8), (5, 4), x.shape, t.shape, (5, 4, 9), ()):
+                args = (t, dtype, shape, "x", 0)
+                assert outcome(serving._dense, *args) == outcome(serving._dense_py, *args), args[1:]
+        for dtypes in ((torch.float32,), (torch.bfloat16, torch.float16), {torch.float32: 2}):
+            for shape in (None, x.shape, (5, 4, 9)):
+                args = (t, dtypes, "x", 0, shape)
+                assert outcome(serving._rows, *args) == outcome(serving._rows_py, *args), args[1:]
+    assert "cuda:1" in outcome(serving._dense, x, torch.float32, (5, 4, 8), "x", 1)
+    assert "cuda:1" in outcome(serving._rows, x, (torch.float32,), "x", 1)

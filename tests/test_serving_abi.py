@@ -164,3 +164,22 @@ def test_rope_frequencies():
                 dict(rotary_dim=8, factor=0.0), dict(rotary_dim=2, scaling="ntk", factor=2.0)):
         with pytest.raises(ValueError):
             misa.rope_inv_freq(device="cpu", **bad)
+
+
+def test_argument_checks_are_the_built_ones():
+    from long_context_sparse_block_amd import _tensor_args, serving
+    assert serving._dense is _tensor_args.dense and serving._rows is _tensor_args.rows
+    for check in (serving._dense, serving._dense_py):
+        with pytest.raises(ValueError, match="^x is required$"):
+            check(None, torch.float32, (3,), "x", 0)
+        with pytest.raises(ValueError, match="^x must be a GPU tensor$"):
+            check(torch.zeros(3), torch.float32, (3,), "x", 0)
+    for check in (serving._rows, serving._rows_py):
+        with pytest.raises(ValueError, match="^x is required$"):
+            check(None, (torch.float32,), "x", 0)
+        with pytest.raises(ValueError, match="^x must be a GPU tensor$"):
+            check(torch.zeros(3, 2, 4), (torch.float32,), "x", 0, None)
+    with pytest.raises(TypeError):
+        serving._dense(1)
+    with pytest.raises(ValueError):
+        serving._dense(7, torch.float32, (3,), "x", 0)
