@@ -12,7 +12,7 @@
 // the other (2048 tokens over 32K keys, 32 / 8 heads of 128: 1.07-1.15 ms by card, 930
 // to 1000 TFLOP/s where the library's product reaches 1327).  At head_dim 64 over
 // e4m3 pages the vector unit is the bound (70%: exponentials and scales; 9
-// sequences of 0..515 new tokens over up to 5003 keys, 20 / 4 heads: 98 us a call).
+// sequences of 0..515 new tokens over up to 5003 keys, 20 / 4 heads: 80-98 us a call).
 // 32 rows a wave: with 64, or with scores formed a tile ahead, the registers
 // leave one wave a SIMD, and both were slower (1.17 to 1.6 ms).  NW = 2 where a
 // unit has at most 64 rows: half the rows of 4 would be empty.

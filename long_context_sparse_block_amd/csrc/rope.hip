@@ -13,7 +13,7 @@
 // tokens x 64 heads of 128 in bf16 in 50.7 us (5.3 TB/s, a copy's rate); keys and
 // values of 4099 tokens x 8 heads of 128 into bf16 pages in 9.4 us (3.6 TB/s, held
 // by the way from slot and row to the page: one pass of rows to a thread); 8192
-// index keys into e4m3 pages in 5.7 us.
+// index keys into e4m3 pages in 6.2 us.
 #include <algorithm>
 
 #include "misa_common.h"
@@ -180,7 +180,9 @@ hipError_t launch_rope(const misa_rope_spec& spec, const void* x, int dtype, int
 // (interleaved) or in one other piece (half layout), or anywhere (odd offsets).
 // Rows that become codes are rotated in fp64: a value that lands on the other
 // side of an e4m3 border is an error of half a step, so the value that meets
-// the border should be the true one.
+// the border should be the true one.  Such a value is kept as fp32 x + dx; the
+// quotients by which it becomes a scale or a code are those of x, corrected by
+// their remainders, and so rounded to fp32 once.
 template <bool FP8>
 struct Turn {
   using T = double;
@@ -280,8 +282,12 @@ __global__ void __launch_bounds__(kThreads) k_write_pages(const WriteArgs a, con
     for (int it = 0; it < items; ++it) {
       if (it > 0) w = fetch(it);
       if (w.slot < 0 || w.slot >= a.n_slots) continue;   // uniform over a row's lanes
-      float x[8];
+      float x[8], dx[8] = {};
       unpack8(w.mine, x);
+      auto put = [&](int i, T z) __attribute__((always_inline)) {
+        x[i] = (float)z;
+        if constexpr (FP8) dx[i] = __builtin_fabsf(x[i]) < INFINITY ? (float)(z - (T)x[i]) : 0.f;
+      };
       if (turns && !w.is_v) {
         const T *c = s_c + w.t * r.half, *s = s_s + w.t * r.half;
         if constexpr (KIND == kHalf) {
@@ -290,15 +296,15 @@ __global__ void __launch_bounds__(kThreads) k_write_pages(const WriteArgs a, con
           unpack8(w.other, y);
 #pragma unroll
           for (int i = 0; i < 8; ++i)   // first: a c - b s; second: b c + a s
-            x[i] = (float)((T)x[i] * c[j0 + i] + (T)(second0 ? y[i] : -y[i]) * s[j0 + i]);
+            put(i, (T)x[i] * c[j0 + i] + (T)(second0 ? y[i] : -y[i]) * s[j0 + i]);
         } else if constexpr (KIND == kPairs) {
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
             const int q = q0 + i;
             if (q < 0 || q >= 2 * r.half) continue;
             const T a0 = x[i], b0 = x[i + 1], cj = c[q >> 1], sj = s[q >> 1];
-            x[i] = (float)(a0 * cj - b0 * sj);
-            x[i + 1] = (float)(b0 * cj + a0 * sj);
+            put(i, a0 * cj - b0 * sj);
+            put(i + 1, b0 * cj + a0 * sj);
           }
         } else {
 #pragma unroll
@@ -309,28 +315,47 @@ __global__ void __launch_bounds__(kThreads) k_write_pages(const WriteArgs a, con
             const int j = hl ? (second ? q - r.half : q) : q >> 1;
             const int other = hl ? (second ? q - r.half : q + r.half) : q ^ 1;
             const T mine = x[i], his = bf16_bits_to_f32(w.src[r.start + other]);
-            x[i] = (float)(mine * c[j] + (second ? his : -his) * s[j]);
+            put(i, mine * c[j] + (second ? his : -his) * s[j]);
           }
         }
       }
       const int64_t dst_row = w.slot * a.H + w.h;
       if constexpr (FP8) {
-        float amax = 0.f;
+        float sc;
+        if constexpr (KIND == kStill) {
+          float amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(x[i]));
-        for (int o = lpr >> 1; o >= 1; o >>= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o, lpr));
-        const float s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+          for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(x[i]));
+          for (int o = lpr >> 1; o >= 1; o >>= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o, lpr));
+          sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+        } else {
+          double amax = 0.;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) amax = __builtin_fmax(amax, __builtin_fabs((double)x[i] + (double)dx[i]));
+          for (int o = lpr >> 1; o >= 1; o >>= 1) amax = __builtin_fmax(amax, __shfl_xor(amax, o, lpr));
+          const float top = (float)amax, rest = (float)(amax - (double)top);
+          sc = __fdiv_rn(top, 448.f);
+          if (rest != 0.f && top < INFINITY) sc += (__builtin_fmaf(-sc, 448.f, top) + rest) * (1.f / 448.f);
+          if (!(amax > 0.)) sc = 1.f;
+        }
+        float q[8];
+        const float inv = KIND == kStill ? 0.f : __fdiv_rn(1.f, sc);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          q[i] = __fdiv_rn(x[i], sc);
+          if (KIND != kStill && dx[i] != 0.f && sc < INFINITY) q[i] += (__builtin_fmaf(-q[i], sc, x[i]) + dx[i]) * inv;
+        }
         uint32_t c[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           int u = 0;
-          u = __builtin_amdgcn_cvt_pk_fp8_f32(__fdiv_rn(x[4 * i], s), __fdiv_rn(x[4 * i + 1], s), u, false);
-          u = __builtin_amdgcn_cvt_pk_fp8_f32(__fdiv_rn(x[4 * i + 2], s), __fdiv_rn(x[4 * i + 3], s), u, true);
+          u = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i], q[4 * i + 1], u, false);
+          u = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i + 2], q[4 * i + 3], u, true);
           c[i] = (uint32_t)u;
         }
         uint8_t* pool = static_cast<uint8_t*>(w.is_v ? a.v_pages : a.k_pages);
         if (live) *reinterpret_cast<uint2*>(pool + dst_row * a.D + e0) = make_uint2(c[0], c[1]);
-        if (p == 0) (w.is_v ? a.v_scale : a.k_scale)[dst_row] = s;
+        if (p == 0) (w.is_v ? a.v_scale : a.k_scale)[dst_row] = sc;
       } else {
         uint16_t* pool = static_cast<uint16_t*>(w.is_v ? a.v_pages : a.k_pages);
         if (live)
