@@ -1,10 +1,12 @@
-// Checks of tensor arguments for the Python wrappers (module _tensor_args): the
-// pointer of a dense tensor, the pointer and strides of a [tokens, heads,
-// head_dim] one.  Looked up attribute by attribute from Python, each costs three
-// to four times as much, and a call of a few microseconds checks half a dozen.
+// Tensor arguments of the Python wrappers (module _tensor_args): the pointer of a
+// dense tensor, the pointer and strides of a [tokens, heads, head_dim] one, a page
+// pool's, a workspace.  Looked up attribute by attribute from Python, each costs
+// three to four times as much, and a call of a few microseconds checks half a
+// dozen.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/ops/empty.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/DynamicTypes.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -105,7 +107,62 @@ PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return got;
 }
 
+// pool(pages, heads, head_dim, name, dev) -> pointer, code type (misa_kdtype), pages, rows a page
+PyObject* pool(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 5 || !PyUnicode_Check(a[3])) {
+    PyErr_SetString(PyExc_TypeError, "pool(pages, heads, head_dim, name, dev)");
+    return nullptr;
+  }
+  const at::Tensor* t = gpu_tensor(a[0], a[3], a[4]);
+  if (t == nullptr) return nullptr;
+  const long long heads = PyLong_AsLongLong(a[1]), dim = PyLong_AsLongLong(a[2]);
+  if (PyErr_Occurred()) return nullptr;
+  const auto type = t->scalar_type();
+  const bool codes = type == at::kByte || type == at::kFloat8_e4m3fn;
+  if (!codes && type != at::kBFloat16) {
+    PyErr_Format(PyExc_ValueError, "%U: dtype %S (expected bfloat16 or float8_e4m3fn/uint8 codes)", a[3], dtype_of(*t));
+    return nullptr;
+  }
+  const int64_t nd = t->dim();
+  const bool fits = (nd == 4 && t->size(2) == heads && t->size(3) == dim) || (nd == 3 && heads == 1 && t->size(2) == dim);
+  if (!fits) {
+    PyObject* want = PyUnicode_FromFormat("(n_pages, page_keys, %lld, %lld)", heads, dim);
+    if (want != nullptr) refuse_shape(a[3], *t, want);
+    Py_XDECREF(want);
+    return nullptr;
+  }
+  if (!t->is_contiguous()) return refuse(a[3], " must be contiguous");
+  PyObject* got = PyTuple_New(4);
+  if (got == nullptr) return nullptr;
+  PyTuple_SET_ITEM(got, 0, PyLong_FromVoidPtr(t->data_ptr()));
+  PyTuple_SET_ITEM(got, 1, PyLong_FromLong(codes ? 1 : 0));
+  PyTuple_SET_ITEM(got, 2, PyLong_FromLongLong(t->size(0)));
+  PyTuple_SET_ITEM(got, 3, PyLong_FromLongLong(t->size(1)));
+  return got;
+}
+
+// scratch(bytes, like) -> uint8 tensor on like's device, pointer
+PyObject* scratch(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 2 || !THPVariable_Check(a[1])) {
+    PyErr_SetString(PyExc_TypeError, "scratch(bytes, like)");
+    return nullptr;
+  }
+  const long long bytes = PyLong_AsLongLong(a[0]);
+  if (PyErr_Occurred()) return nullptr;
+  try {
+    const at::Tensor t = at::empty({bytes}, at::TensorOptions().device(THPVariable_Unpack(a[1]).device()).dtype(at::kByte));
+    return Py_BuildValue("(NN)", THPVariable_Wrap(t), PyLong_FromVoidPtr(t.data_ptr()));
+  } catch (const std::exception& e) {   // out of memory
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
 PyMethodDef methods[] = {
+    {"pool", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(pool)), METH_FASTCALL,
+     "pool(pages, heads, head_dim, name, dev): pointer, code type, n_pages, page_keys of a page pool"},
+    {"scratch", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(scratch)), METH_FASTCALL,
+     "scratch(bytes, like): a workspace on like's device, and its pointer"},
     {"dense", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(dense)), METH_FASTCALL,
      "dense(tensor, dtype, shape, name, dev): pointer of a dense tensor of this type and shape on GPU dev"},
     {"rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rows)), METH_FASTCALL,

@@ -101,10 +101,34 @@ def _rows_py(t, dtypes, name, dev, shape=None):
     return t.data_ptr(), (st if T > 1 else 0), (sh if H > 1 else 0)
 
 
-try:   # the same checks in C++ (csrc/tensor_args.cpp), a quarter of the time
-    from ._tensor_args import dense as _dense, rows as _rows
+def _pool_py(pages, heads, head_dim, name, dev):
+    """Pointer, kdtype, n_pages, page_keys of a page pool [n_pages, page_keys, heads,
+    head_dim] (or [n_pages, page_keys, head_dim] of one head) on GPU `dev`."""
+    if pages is None:
+        raise ValueError(f"{name} is required")
+    if not pages.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if pages.get_device() != dev:
+        raise ValueError(f"{name} is on {pages.device}, expected cuda:{dev}")
+    if pages.dtype not in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn):
+        raise ValueError(f"{name}: dtype {pages.dtype} (expected bfloat16 or float8_e4m3fn/uint8 codes)")
+    shape = tuple(pages.shape)
+    if shape[2:] != (heads, head_dim) and not (heads == 1 and shape[2:] == (head_dim,)):
+        raise ValueError(f"{name}: shape {shape}, expected (n_pages, page_keys, {heads}, {head_dim})")
+    if not pages.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return pages.data_ptr(), _kdtype(pages), shape[0], shape[1]
+
+
+def _scratch_py(nbytes, like):
+    t = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    return t, t.data_ptr()
+
+
+try:   # the same in C++ (csrc/tensor_args.cpp): a quarter of the time
+    from ._tensor_args import dense as _dense, pool as _pool, rows as _rows, scratch as _scratch
 except ImportError:   # not built yet
-    _dense, _rows = _dense_py, _rows_py
+    _dense, _pool, _rows, _scratch = _dense_py, _pool_py, _rows_py, _scratch_py
 
 
 def _on(stream, f, *args):
@@ -225,19 +249,6 @@ def misa_rope(x, positions, inv_freq, layout: str = "half", rot_start: int = 0, 
     return out
 
 
-def _pool(pages, heads, head_dim, name, dev):
-    """Pointer, kdtype, n_pages, page_keys of a page pool [n_pages, page_keys, heads,
-    head_dim] (or [n_pages, page_keys, head_dim] of one head)."""
-    if pages is None:
-        raise ValueError(f"{name} is required")
-    kd = _kdtype(pages)
-    shape = pages.shape
-    want = (shape[0], shape[1], heads, head_dim)
-    if len(shape) == 3 and heads == 1:
-        want = (shape[0], shape[1], head_dim)
-    return _dense(pages, pages.dtype, want, name, dev), kd, shape[0], shape[1]
-
-
 def _pool_scale(scale, n_pages, page_keys, heads, name, dev):
     want = (n_pages, page_keys, heads)
     if scale is not None and heads == 1 and scale.dim() == 2:
@@ -336,13 +347,11 @@ def _attention(name, q, k_pages, v_pages, block_table, q_start, kv_lens, idx, k_
     if ws is None:
         need = (lib.misa_attention_paged_workspace_bytes(shape, pages) if idx is None
                 else lib.misa_attention_selected_workspace_bytes(shape, pages, topk))
-        if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif ws.get_device() != dev or not ws.is_contiguous():
-        raise ValueError(f"ws must be a dense tensor on cuda:{dev}")
-    if ws is None:
-        _call(name, fn, dev, *args, None, 0)
+        ws, at = _scratch(need, q) if need else (None, None)   # (ws stays until the call has been made)
+        _call(name, fn, dev, *args, at, need)
     else:
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be a dense tensor on cuda:{dev}")
         _call(name, fn, dev, *args, ws.data_ptr(), ws.numel() * ws.element_size())
     return out, lse
 

@@ -318,5 +318,13 @@ def test_built_argument_checks_equal_the_plain_ones():
             for shape in (None, x.shape, (5, 4, 9)):
                 args = (t, dtypes, "x", 0, shape)
                 assert outcome(serving._rows, *args) == outcome(serving._rows_py, *args), args[1:]
+    for t in (x, x.bfloat16(), x.byte()[None], x.bfloat16()[None], x.bfloat16()[None].transpose(1, 2),
+              x.to(torch.float8_e4m3fn)[None], x.bfloat16()[0], x.bfloat16()[0, 0]):
+        for heads, dim in ((4, 8), (1, 8), (5, 4), (4, 4)):
+            args = (t, heads, dim, "x", 0)
+            assert outcome(serving._pool, *args) == outcome(serving._pool_py, *args), (t.shape, args[1:])
+    ws, at = serving._scratch(1000, x)
+    assert ws.shape == (1000,) and ws.dtype == torch.uint8 and ws.device == x.device and at == ws.data_ptr()
+    assert "cuda:1" in outcome(serving._pool, x.bfloat16(), 1, 8, "x", 1)
     assert "cuda:1" in outcome(serving._dense, x, torch.float32, (5, 4, 8), "x", 1)
     assert "cuda:1" in outcome(serving._rows, x, (torch.float32,), "x", 1)
