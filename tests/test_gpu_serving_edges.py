@@ -272,6 +272,36 @@ def test_two_graphs_share_a_workspace():
             assert torch.equal(run(*jobs[n])[0], base[n][0])
 
 
+# ---------------------------------------------------------------- plans of many sequences
+
+@pytest.mark.parametrize("n,page,most,live", [(1024, 16, 3, 1.0), (1025, 16, 3, 1.0), (1537, 64, 400, 0.1), (5000, 8, 1, 0.05),
+                                              (65535, 32, 2, 0.5), (65535, 32, 0, 0.0)])
+@pytest.mark.parametrize("hold", [0, 50])
+def test_plan_of_many_sequences(n, page, most, live, hold):
+    """Runs of sequences without new tokens, tokens of a workgroup in many runs, and a free list that runs out."""
+    say("plan", n, page, most, live, hold)
+    g = torch.Generator().manual_seed(n + hold)
+    cached = torch.randint(0, 100, (n,), generator=g)
+    new = torch.randint(0, most + 1, (n,), generator=g) * (torch.rand((n,), generator=g) < live)
+    width = int((-(-(cached + new) // page)).max()) + 1
+    have = -(-cached // page)
+    ids = torch.randperm(int(have.sum()) + n + 10, generator=g).to(torch.int32)
+    table = torch.full((n, width), -7, dtype=torch.int32)
+    table[torch.arange(width)[None, :] < have[:, None]] = ids[:int(have.sum())]
+    need = int((-(-(cached + new) // page) - have).sum())
+    free = ids[int(have.sum()):][:max(0, need - hold)].contiguous()
+    T = int(new.sum()) + 30
+    want = ref.plan(cached.tolist(), new.tolist(), free.tolist(), table, page, T)
+    t = table.cuda()
+    i32 = torch.int32
+    got = misa.misa_plan_pages(cached.to(i32).cuda(), new.to(i32).cuda(), free.cuda(), t, page, T)
+    torch.cuda.synchronize()
+    assert t.tolist() == want["table"]
+    assert got.q_start.tolist() == want["q_start"] and got.kv_lens.tolist() == want["kv_lens"]
+    assert got.positions.tolist() == want["positions"] and got.slots.tolist() == want["slots"]
+    assert got.n_taken.tolist() == want["n_taken"]
+
+
 # ---------------------------------------------------------------- codes of rotated rows
 
 @pytest.mark.parametrize("layout,start", [("half", 0), ("half", 3), ("interleaved", 16)])
