@@ -77,11 +77,13 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a, const JoinS
     sum *= keep;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      // an empty split wrote no output: whatever is there is not used
-      const float w = s0 + k < n && x[k].y != 0.f ? exp2_raw(x[k].x - most) : 0.f;
-      sum = w == 0.f ? sum : __builtin_fmaf(w, x[k].y, sum);
+      // An empty split wrote no output: whatever is there is not used.  Any other
+      // takes part however little it weighs, so that its NaN shows.
+      const bool in = s0 + k < n && x[k].y != 0.f;
+      const float w = exp2_raw(x[k].x - most);
+      sum = in ? __builtin_fmaf(w, x[k].y, sum) : sum;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = w == 0.f ? o[e] : __builtin_fmaf(w, v[k][e], o[e]);
+      for (int e = 0; e < 4; ++e) o[e] = in ? __builtin_fmaf(w, v[k][e], o[e]) : o[e];
     }
   };
   if (n <= 4)
