@@ -125,7 +125,6 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
     const int j = jt * kBN + lane;
     return SEL ? pick(a, tok0, j) : min(j, kend - 1);
   };
-  auto clamp_tok = [&](int t) __attribute__((always_inline)) -> int { return SEL ? (t >= 0 && t < kfull ? t : 0) : t; };
   using Stage = Fp8Stage<D, NT>;
   // Lane k of every wave knows where key k's pool row starts (bytes); a load's
   // lanes fetch that from the lane of their row.  Which piece of the row a lane
@@ -316,9 +315,14 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
 
   if (jt0 < jt1) {
     const int last = jt1 - 1;
+    // An absent entry (a weight of 0) reads the tile's first listed token instead,
+    // whose value the row sees anyway; a tile without one is skipped.
     auto look = [&](int t, uint64_t& mask) __attribute__((always_inline)) -> int {
-      if (SEL) mask = __ballot(t >= 0 && t < kfull);
-      return clamp_tok(t);
+      if (!SEL) return t;
+      const bool in = t >= 0 && t < kfull;
+      mask = __ballot(in);
+      const int first = mask != 0 ? __builtin_amdgcn_readlane(t, (int)__builtin_ctzll(mask)) : 0;
+      return in ? t : first;
     };
     uint64_t m0 = ~0ull, m1 = ~0ull, m2 = ~0ull;   // of this tile and the next two
     const int t0 = look(SEL ? pick0 : token_at(jt0), m0);
@@ -339,7 +343,7 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
           ent_n = table_entry(a, b, tok_n);
           tok_nn = token_at(min(jt + 3, last));
         }
-        compute(ck, cv, s_ks0, s_vs0, jt, m0);
+        if (!SEL || m0 != 0) compute(ck, cv, s_ks0, s_vs0, jt, m0);
         m0 = m1;
         m1 = m2;
       };
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
         ent_n = table_entry(a, b, tok_n);
         tok_nn = token_at(min(jt + 4, last));
         issue(row, nullptr, nullptr, free);
-        compute(ck, cv, cks, cvs, jt, m0);
+        if (!SEL || m0 != 0) compute(ck, cv, cks, cvs, jt, m0);
         land(next, nk, nv, nks, nvs);
         m0 = m1;
         m1 = m2;

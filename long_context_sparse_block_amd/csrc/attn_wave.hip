@@ -135,7 +135,6 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 && (SEL || RT == 1 || D ==
     return SEL ? pick(a, tok0, j) : min(j, kend - 1);
   };
   auto seen = [&](int t) __attribute__((always_inline)) -> bool { return t >= 0 && t < kfull; };
-  auto clamp_tok = [&](int t) __attribute__((always_inline)) -> int { return SEL ? (seen(t) ? t : 0) : t; };
   // Lane k < 32 knows where key k's pool row starts (bytes); others fetch it there
   auto fetch = [&](int64_t off, int from) __attribute__((always_inline)) -> int64_t {
     const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)off, from), hi = (uint32_t)__shfl((int)(off >> 32), from);
@@ -299,9 +298,14 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 && (SEL || RT == 1 || D ==
 
   if (jt0 < jt1) {
     const int last = jt1 - 1;
+    // An absent entry (a weight of 0) reads the tile's first listed token instead,
+    // whose value the row sees anyway; a tile without one is skipped.
     auto look = [&](int t, uint32_t& mask) __attribute__((always_inline)) -> int {
-      if (SEL) mask = (uint32_t)__ballot(seen(t));
-      return clamp_tok(t);
+      if (!SEL) return t;
+      const bool in = seen(t);
+      mask = (uint32_t)__ballot(in);
+      const int first = mask != 0 ? __builtin_amdgcn_readlane(t, (int)__builtin_ctz(mask)) : 0;
+      return in ? t : first;
     };
     auto next = [&](int i) __attribute__((always_inline)) { return min(jt0 + i * kWaves, last); };
     uint32_t m0 = 0, m1 = 0, m2 = 0;   // of this tile and the next two
@@ -336,7 +340,7 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 && (SEL || RT == 1 || D ==
         ent_n = table_entry(a, b, tok_n);
         tok_nn = token_at(min(jt + 4 * kWaves, last));
         issue(row, nullptr, r);
-        compute(ka, jt, m0);
+        if (!SEL || m0 != 0) compute(ka, jt, m0);
         m0 = m1;
         m1 = m2;
         m2 = m3;
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 && (SEL || RT == 1 || D ==
           ent_n = table_entry(a, b, tok_n);
           tok_nn = token_at(min(jt + 3 * kWaves, last));
         }
-        compute(cur, jt, m0);
+        if (!SEL || m0 != 0) compute(cur, jt, m0);
         m0 = m1;
         m1 = m2;
       };

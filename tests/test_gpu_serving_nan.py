@@ -99,3 +99,44 @@ def test_nan_among_keys_far_below_the_maximum(new, which):
     out, lse = run(p, scale=1.0)
     assert bool(torch.isnan(out[:, :, 3]).all())
     assert bool(torch.isnan(lse).all()) == (which == 0)
+
+
+# ---------------------------------------------------------------- entries that are absent
+
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads,kv_heads,dim,topk", [(8, 2, 128, 77), (8, 2, 64, 1101), (40, 1, 128, 300), (70, 1, 64, 2048)])
+def test_a_token_that_no_list_names_reaches_no_row(heads, kv_heads, dim, topk, fp8, bad):
+    """Lists with holes, of lengths that end inside a tile, one with nothing in it, none with token 0 or a token of its
+    page: what that page holds, and which page the table names for it, changes nothing."""
+    say("unlisted", heads, kv_heads, dim, topk, fp8, bad)
+    def make():
+        p = ref.Paged(25, [2300, 60], [4, 1], heads, kv_heads, dim, 16, fp8)
+        idx = p.select(topk, 0.3)
+        idx[idx < 16] = -1
+        idx[2] = -1
+        idx[3, 64:] = -1      # whole tiles without an entry
+        idx[3, :5] = torch.tensor([-1, 100000, 17, -7, 2299])
+        at = int(p.table[0, 0])   # let that page be the pool's first
+        was = p.table.clone()
+        p.table[was == 0], p.table[was == at] = at, 0
+        for rows in (p.pages, p.vals) + ((p.scale, p.codes) if fp8 else ()):
+            for x in rows:
+                first = x[0].clone()
+                x[0], x[at] = x[at].clone(), first
+        return p, idx
+    p, idx = make()
+    want = run(p, idx)
+    ref.check_attention(p, *want, idx)
+    for which in (0, 1):
+        for b in (0, 1):
+            poison(p, which, b, range(16), head=None, value=float(bad))
+    for a, b in zip(run(p, idx), want):
+        assert torch.equal(a, b)
+    # the page was given back: another sequence's, or none
+    for entry in (-1, 10 ** 6, 0):
+        p.table[:, 0] = entry
+        p.pages[0][0].view(torch.uint8).fill_(0x7F)
+        p.pages[1][0].view(torch.uint8).fill_(0x7F)
+        for a, b in zip(run(p, idx), want):
+            assert torch.equal(a, b)
