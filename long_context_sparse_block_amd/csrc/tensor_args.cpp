@@ -6,9 +6,12 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <exception>
+
 #include <ATen/ops/empty.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/DynamicTypes.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 namespace {
@@ -99,12 +102,9 @@ PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (t->dim() != 3) return refuse(a[2], ": expected [tokens, heads, head_dim]");
   if (t->stride(2) != 1 && t->size(2) > 1) return refuse(a[2], ": the last dimension must be dense");
   // the strides of dimensions of one element mean nothing
-  PyObject* got = PyTuple_New(3);
-  if (got == nullptr) return nullptr;
-  PyTuple_SET_ITEM(got, 0, PyLong_FromVoidPtr(t->data_ptr()));
-  PyTuple_SET_ITEM(got, 1, PyLong_FromLongLong(t->size(0) > 1 ? t->stride(0) : 0));
-  PyTuple_SET_ITEM(got, 2, PyLong_FromLongLong(t->size(1) > 1 ? t->stride(1) : 0));
-  return got;
+  const long long st = t->size(0) > 1 ? t->stride(0) : 0, sh = t->size(1) > 1 ? t->stride(1) : 0;
+  void* const at = t->data_ptr();
+  return Py_BuildValue("(NLL)", PyLong_FromVoidPtr(at), st, sh);
 }
 
 // pool(pages, heads, head_dim, name, dev) -> pointer, code type (misa_kdtype), pages, rows a page
@@ -132,13 +132,9 @@ PyObject* pool(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return nullptr;
   }
   if (!t->is_contiguous()) return refuse(a[3], " must be contiguous");
-  PyObject* got = PyTuple_New(4);
-  if (got == nullptr) return nullptr;
-  PyTuple_SET_ITEM(got, 0, PyLong_FromVoidPtr(t->data_ptr()));
-  PyTuple_SET_ITEM(got, 1, PyLong_FromLong(codes ? 1 : 0));
-  PyTuple_SET_ITEM(got, 2, PyLong_FromLongLong(t->size(0)));
-  PyTuple_SET_ITEM(got, 3, PyLong_FromLongLong(t->size(1)));
-  return got;
+  const long long n_pages = t->size(0), page_keys = t->size(1);
+  void* const at = t->data_ptr();
+  return Py_BuildValue("(NiLL)", PyLong_FromVoidPtr(at), codes ? 1 : 0, n_pages, page_keys);
 }
 
 // scratch(bytes, like) -> uint8 tensor on like's device, pointer
@@ -149,23 +145,34 @@ PyObject* scratch(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const long long bytes = PyLong_AsLongLong(a[0]);
   if (PyErr_Occurred()) return nullptr;
+  const at::Tensor t = at::empty({bytes}, at::TensorOptions().device(THPVariable_Unpack(a[1]).device()).dtype(at::kByte));
+  void* const at = t.data_ptr();
+  return Py_BuildValue("(NN)", THPVariable_Wrap(t), PyLong_FromVoidPtr(at));
+}
+
+// Torch throws where a tensor has no pointer, sizes or strides of its own (under
+// vmap, while tracing), and where memory runs out: its Python errors, nothing
+// past this border.
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   try {
-    const at::Tensor t = at::empty({bytes}, at::TensorOptions().device(THPVariable_Unpack(a[1]).device()).dtype(at::kByte));
-    return Py_BuildValue("(NN)", THPVariable_Wrap(t), PyLong_FromVoidPtr(t.data_ptr()));
-  } catch (const std::exception& e) {   // out of memory
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return F(self, a, n);
+  } catch (...) {
+    torch::translate_exception_to_python(std::current_exception());
     return nullptr;
   }
 }
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyCFunction entry() { return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<F>)); }
 
 PyMethodDef methods[] = {
-    {"pool", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(pool)), METH_FASTCALL,
+    {"pool", entry<pool>(), METH_FASTCALL,
      "pool(pages, heads, head_dim, name, dev): pointer, code type, n_pages, page_keys of a page pool"},
-    {"scratch", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(scratch)), METH_FASTCALL,
+    {"scratch", entry<scratch>(), METH_FASTCALL,
      "scratch(bytes, like): a workspace on like's device, and its pointer"},
-    {"dense", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(dense)), METH_FASTCALL,
+    {"dense", entry<dense>(), METH_FASTCALL,
      "dense(tensor, dtype, shape, name, dev): pointer of a dense tensor of this type and shape on GPU dev"},
-    {"rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rows)), METH_FASTCALL,
+    {"rows", entry<rows>(), METH_FASTCALL,
      "rows(tensor, dtypes, name, dev, shape=None): pointer, token and head strides of a [tokens, heads, head_dim] tensor"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_args", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

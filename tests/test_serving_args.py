@@ -1,0 +1,50 @@
+"""Arguments of the paged serving calls that the built checks (_tensor_args) and the wrappers around them have to turn
+into Python errors, on the CPU.  Fake tensors stand for GPU ones: they have a device, sizes and strides and no memory."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+# Each call below meets a tensor whose sizes, strides or pointer torch refuses with a C++ exception.  Tried in a process
+# of its own: one that passes a C function's border ends it.
+CALLS = {
+    "dense": "serving._dense(x, torch.float32, (3, 2, 64), 'x', 0)",
+    "rows": "serving._rows(x, (torch.float32,), 'x', 0)",
+    "rows_shape": "serving._rows(x, (torch.float32,), 'x', 0, (3, 2, 64))",
+    "pool": "serving._pool(x.to(torch.bfloat16), 1, 64, 'x', 0)",
+    "scratch": "serving._scratch(-5, x)",
+}
+TENSORS = {
+    "vmap": "torch.func.vmap(call)(torch.empty((2, 3, 2, 64), device='cuda'))",
+    "sparse": "call(torch.sparse_coo_tensor(torch.zeros((3, 1), dtype=torch.int64, device='cuda'), "
+              "torch.zeros(1, device='cuda'), (3, 2, 64)))",
+    "symbolic": "call(torch.empty((sizes.create_unbacked_symint(), 2, 64), device='cuda'))",
+}
+PROGRAM = """
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+from torch.fx.experimental.symbolic_shapes import ShapeEnv
+from long_context_sparse_block_amd import serving
+sizes = ShapeEnv()
+mode = FakeTensorMode(shape_env=sizes, allow_non_fake_inputs=True)
+def call(x):
+    return {call}
+with mode:
+    try:
+        print("returned", {tensor})
+    except Exception as e:
+        print("raised", type(e).__name__, str(e)[:200])
+"""
+
+
+@pytest.mark.parametrize("tensor", TENSORS)
+@pytest.mark.parametrize("call", CALLS)
+def test_errors_of_torch_stay_errors(call, tensor):
+    r = subprocess.run([sys.executable, "-W", "ignore", "-c", PROGRAM.format(call=CALLS[call], tensor=TENSORS[tensor])],
+                       cwd=ROOT, capture_output=True, text=True, timeout=120)
+    print(r.stdout, r.stderr[-500:])
+    assert r.returncode == 0
+    assert r.stdout.startswith("raised")
