@@ -127,8 +127,13 @@ def _scratch_py(nbytes, like):
 
 try:   # the same in C++ (csrc/tensor_args.cpp): a quarter of the time
     from ._tensor_args import dense as _dense, pool as _pool, rows as _rows, scratch as _scratch
-except ImportError:   # not built yet
+except ModuleNotFoundError:   # not built yet
     _dense, _pool, _rows, _scratch = _dense_py, _pool_py, _rows_py, _scratch_py
+except ImportError as e:   # built against another torch, say: every call raises, importing and building again do not
+    def _dense(*args, why=str(e)):
+        raise RuntimeError(f"_tensor_args does not load ({why}): build it again with "
+                           "`python -m long_context_sparse_block_amd.build`")
+    _pool = _rows = _scratch = _dense
 
 
 def _on(stream, f, *args):

@@ -48,3 +48,32 @@ def test_errors_of_torch_stay_errors(call, tensor):
     print(r.stdout, r.stderr[-500:])
     assert r.returncode == 0
     assert r.stdout.startswith("raised")
+
+
+BROKEN = """
+import sys
+class Finder:
+    def find_spec(self, name, path=None, target=None):
+        if name.endswith("._tensor_args"):
+            raise {error}
+sys.meta_path.insert(0, Finder())
+import torch
+from long_context_sparse_block_amd import build, serving   # (building again stays possible)
+try:
+    serving._dense(None, torch.float32, (3,), "x", 0)
+except Exception as e:
+    print(type(e).__name__, serving._dense is serving._dense_py, e)
+"""
+
+
+def test_built_checks_that_do_not_load_are_an_error():
+    """A library that is there but fails to load (built against another torch, say) is not passed over; one that is not
+    built leaves the Python checks."""
+    def run(error):
+        r = subprocess.run([sys.executable, "-c", BROKEN.format(error=error)], cwd=ROOT, capture_output=True, text=True,
+                           timeout=120)
+        assert r.returncode == 0, r.stderr[-2000:]
+        return r.stdout
+    assert run("ModuleNotFoundError('none', name=name)").startswith("ValueError True x is required")
+    out = run("ImportError('undefined symbol: _Znwm')")
+    assert out.startswith("RuntimeError False") and "undefined symbol" in out and "build" in out
