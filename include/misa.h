@@ -579,7 +579,10 @@ typedef struct {
   int32_t head_dim;             /* 64 or 128 */
   int64_t n_tokens;             /* rows of q and out, 0..2^26 */
   int64_t q_stride_token, q_stride_head;   /* multiples of 8 */
-  int32_t max_new;              /* no sequence has more new tokens than this; 0: not known */
+  int32_t max_new;              /* no sequence has more new tokens than this (rows past it may stay unwritten); 0:
+                                   not known, and the call prepares for any mix: both kernels run, and there is
+                                   a workspace where decodes alone need none (64 decodes over 2..4K keys, 32 / 8
+                                   heads of 128: 166 us and 34 MB, with max_new = 1 155 us and none) */
   float scale;                  /* on q . k, usually 1/sqrt(head_dim) */
 } misa_attn_shape;
 

@@ -23,23 +23,18 @@ namespace {
 // or eight at a time with a running maximum: each lane forms the row's weights
 // by itself, so lanes exchange nothing.  (46k rows of two to four splits: 6 us;
 // splits side by side on lanes that then sum by shuffles took 16.)
-struct JoinSide {
-  AttnLaunch L;
-  int rows;   // of a unit's part of the workspace
-};
-
 template <int D, bool SEL>
-__global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a, const JoinSide tile, const JoinSide wave,
+__global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a, const AttnLaunch tile, const AttnLaunch wave,
                                                    uint32_t n_tile) {
   constexpr int LR = D / 4, RW = 256 / LR;   // lanes of a row, rows of a workgroup
   const bool is_tile = blockIdx.x < n_tile;
-  const JoinSide& S = is_tile ? tile : wave;
+  const AttnLaunch& S = is_tile ? tile : wave;
   const uint32_t i = is_tile ? blockIdx.x : blockIdx.x - n_tile;
   const int G = a.n_heads / a.n_kv_heads;
   const uint32_t per = (uint32_t)S.rows / RW;   // workgroups of a unit and kv head
   const int rr = (int)(i % per) * RW + (int)threadIdx.x / LR, piece = (int)threadIdx.x % LR;
   const int g = (int)(i / per % (uint32_t)a.n_kv_heads), unit = (int)(i / per / (uint32_t)a.n_kv_heads);
-  int r0, nrows, tok0, n = S.L.n_splits;
+  int r0, nrows, tok0, n = S.n_splits;
   if (SEL) {
     const int sub = is_tile ? (G + S.rows - 1) / S.rows : 1;
     tok0 = unit / sub;
@@ -47,7 +42,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a, const JoinS
     if (tok0 >= a.q_start[a.n_seq] || tok0 < a.q_start[0]) return;   // no sequence's token: nothing was written
     nrows = G;
   } else {
-    const int4 u = S.L.unit_info[unit];
+    const int4 u = S.unit_info[unit];
     tok0 = u.x;
     r0 = u.y;
     nrows = u.z;
@@ -55,9 +50,10 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a, const JoinS
   }
   const int r = r0 + rr;
   if (n <= 1 || r >= nrows) return;   // written by the unit itself, or no row
-  const int64_t pr = (((int64_t)unit * a.n_kv_heads + g) * S.L.n_splits) * S.rows + rr;
-  const float2* const ml = S.L.part_ml + pr;
-  const float* const po = S.L.part_o + pr * D + piece * 4;
+  const PartPlace part = part_place<SEL>(S, a.n_kv_heads, G, S.rows, g, unit, tok0, r0, nrows);
+  const int64_t pr = part.begin + rr;
+  const float2* const ml = S.part_ml + pr;
+  const float* const po = S.part_o + pr * D + piece * 4;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
   float top = -INFINITY, sum = 0.f;
   auto some = [&](int s0, auto count) __attribute__((always_inline)) {
@@ -65,9 +61,9 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a, const JoinS
     float2 x[U];
     f32x4 v[U];
 #pragma unroll
-    for (int k = 0; k < U; ++k) x[k] = ml[(int64_t)min(s0 + k, n - 1) * S.rows];
+    for (int k = 0; k < U; ++k) x[k] = ml[(int64_t)min(s0 + k, n - 1) * part.step];
 #pragma unroll
-    for (int k = 0; k < U; ++k) v[k] = *reinterpret_cast<const f32x4*>(po + (int64_t)min(s0 + k, n - 1) * S.rows * D);
+    for (int k = 0; k < U; ++k) v[k] = *reinterpret_cast<const f32x4*>(po + (int64_t)min(s0 + k, n - 1) * part.step * D);
     float most = top;
 #pragma unroll
     for (int k = 0; k < U; ++k) most = fmaxf(most, x[k].y != 0.f ? x[k].x : -INFINITY);
@@ -102,6 +98,7 @@ struct AttnPlan {
   int RT = 0, wave_units = 0, wave_splits = 1, wave_slots = 0;   // RT = 0: attn_wave does not run
   int NW = 0, tile_units = 0, tile_splits = 1, tile_slots = 0;   // NW = 0: attn_tile does not run
   int rows_min = 0;
+  int64_t wave_part = 0, tile_part = 0;   // rows of a kv head's part, a split
   size_t wave_o = 0, wave_ml = 0, wave_info = 0, tile_o = 0, tile_ml = 0, tile_info = 0, total = 0;
   int64_t groups = 0;   // workgroups of the larger launch
 };
@@ -180,8 +177,15 @@ AttnPlan make_plan(const misa_attn_shape& s, const misa_kv_pages& pg, int topk) 
   }
   p.groups = std::max(wave_units * p.wave_splits, tile_units * p.tile_splits) * KH;
   size_t off = 0;
+  // (see AttnLaunch)
+  p.wave_part = (int64_t)p.wave_units * 16 * p.RT;
+  p.tile_part = (int64_t)p.tile_units * 32 * p.NW;
+  if (topk == 0) {
+    p.wave_part = std::min<int64_t>(T * G, p.wave_part);
+    p.tile_part = std::min<int64_t>(T * G, p.tile_part);
+  }
   if (p.RT > 0 && p.wave_splits > 1) {
-    const size_t rows = (size_t)p.wave_units * KH * p.wave_splits * 16 * p.RT;
+    const size_t rows = (size_t)p.wave_part * KH * p.wave_splits;
     p.wave_o = off;
     off += align_up(rows * s.head_dim * sizeof(float));
     p.wave_ml = off;
@@ -190,7 +194,7 @@ AttnPlan make_plan(const misa_attn_shape& s, const misa_kv_pages& pg, int topk) 
     off += align_up((size_t)p.wave_units * sizeof(int4));
   }
   if (p.NW > 0 && p.tile_splits > 1) {
-    const size_t rows = (size_t)p.tile_units * KH * p.tile_splits * 32 * p.NW;
+    const size_t rows = (size_t)p.tile_part * KH * p.tile_splits;
     p.tile_o = off;
     off += align_up(rows * s.head_dim * sizeof(float));
     p.tile_ml = off;
@@ -223,10 +227,13 @@ hipError_t launch_attention(const misa_attn_shape& s, const misa_kv_pages& pg, c
                    s.n_tokens};
   const bool fp8 = pg.kdtype == MISA_K_FP8_E4M3;
   char* base = static_cast<char*>(ws);
-  const AttnLaunch T{p.tile_units, p.tile_splits, p.tile_slots, p.rows_min, reinterpret_cast<float*>(base + p.tile_o),
-                     reinterpret_cast<float2*>(base + p.tile_ml), reinterpret_cast<int4*>(base + p.tile_info)};
-  const AttnLaunch W{p.wave_units, p.wave_splits, p.wave_slots, p.rows_min, reinterpret_cast<float*>(base + p.wave_o),
-                     reinterpret_cast<float2*>(base + p.wave_ml), reinterpret_cast<int4*>(base + p.wave_info)};
+  const int64_t all = s.n_tokens * (s.n_heads / s.n_kv_heads);   // rows of a kv head
+  const AttnLaunch T{p.tile_units, p.tile_splits, p.tile_slots, p.rows_min, 32 * p.NW, p.tile_part == all, p.tile_part,
+                     reinterpret_cast<float*>(base + p.tile_o), reinterpret_cast<float2*>(base + p.tile_ml),
+                     reinterpret_cast<int4*>(base + p.tile_info)};
+  const AttnLaunch W{p.wave_units, p.wave_splits, p.wave_slots, p.rows_min, 16 * p.RT, p.wave_part == all, p.wave_part,
+                     reinterpret_cast<float*>(base + p.wave_o), reinterpret_cast<float2*>(base + p.wave_ml),
+                     reinterpret_cast<int4*>(base + p.wave_info)};
   hipError_t e = hipSuccess;
   if (p.NW > 0) e = launch_attn_tile(a, T, s.head_dim, fp8, p.NW, st);
   if (e == hipSuccess && p.RT > 0) e = launch_attn_wave(a, W, s.head_dim, fp8, p.RT, st);
@@ -234,16 +241,15 @@ hipError_t launch_attention(const misa_attn_shape& s, const misa_kv_pages& pg, c
   const int64_t n_tile = p.NW > 0 && p.tile_splits > 1 ? (int64_t)p.tile_units * s.n_kv_heads * p.NW * 32 * lanes / 256 : 0;
   const int64_t n_wave = p.RT > 0 && p.wave_splits > 1 ? (int64_t)p.wave_units * s.n_kv_heads * p.RT * 16 * lanes / 256 : 0;
   if (e != hipSuccess || n_tile + n_wave == 0) return e;
-  const JoinSide jt{T, 32 * p.NW}, jw{W, 16 * p.RT};
   const dim3 grid((unsigned)(n_tile + n_wave));
   const uint32_t nt = (uint32_t)n_tile;
   const bool sel = idx != nullptr;
   if (s.head_dim == 128) {
-    if (sel) hipLaunchKernelGGL((k_attn_join<128, true>), grid, dim3(256), 0, st, a, jt, jw, nt);
-    else hipLaunchKernelGGL((k_attn_join<128, false>), grid, dim3(256), 0, st, a, jt, jw, nt);
+    if (sel) hipLaunchKernelGGL((k_attn_join<128, true>), grid, dim3(256), 0, st, a, T, W, nt);
+    else hipLaunchKernelGGL((k_attn_join<128, false>), grid, dim3(256), 0, st, a, T, W, nt);
   } else {
-    if (sel) hipLaunchKernelGGL((k_attn_join<64, true>), grid, dim3(256), 0, st, a, jt, jw, nt);
-    else hipLaunchKernelGGL((k_attn_join<64, false>), grid, dim3(256), 0, st, a, jt, jw, nt);
+    if (sel) hipLaunchKernelGGL((k_attn_join<64, true>), grid, dim3(256), 0, st, a, T, W, nt);
+    else hipLaunchKernelGGL((k_attn_join<64, false>), grid, dim3(256), 0, st, a, T, W, nt);
   }
   return hipGetLastError();
 }

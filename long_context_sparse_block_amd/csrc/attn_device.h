@@ -159,11 +159,35 @@ struct AttnLaunch {
   int n_splits;     // key splits of a unit, at most
   int slots;        // workgroups that the GPU holds at a time
   int rows_min;     // dense: attn_tile takes sequences with more rows than this, attn_wave the others
-  float* part_o;    // n_splits > 1: unnormalised outputs [unit][kv head][split][row][D]
-  float2* part_ml;  // and (maximum, sum) of each
+  int rows;         // of a unit, at most
+  // n_splits > 1: unnormalised outputs [D], and (maximum, sum), of every row and
+  // split.  Dense: [kv head][part_rows x n_splits], where a unit has the places
+  // that its rows have in the batch (packed: row r of first token t is t G + r), or
+  // `rows` of its own, whichever takes less: padded units cost nothing, nor do
+  // rows that are the other kernel's.
+  int packed;
+  int64_t part_rows;
+  float* part_o;
+  float2* part_ml;
   // dense: where a unit's rows are, for the join: (first token, first row, rows in all, splits in use)
   int4* unit_info;
 };
+
+// Where a unit's part for kv head g begins, and what is between its splits (in
+// rows): the splits of a unit are side by side, as the join reads them.  Selected:
+// units have as many rows each and stand in their order (placed by the batch's
+// rows like the others, 64 tokens x 64 heads took 22.2 us instead of 21.8).
+struct PartPlace {
+  int64_t begin;
+  int step;
+};
+template <bool SEL>
+__device__ __forceinline__ PartPlace part_place(const AttnLaunch& L, int kv_heads, int G, int rows, int g, int unit,
+                                                int tok0, int r0, int nrows) {
+  if (SEL) return PartPlace{((int64_t)unit * kv_heads + g) * L.n_splits * rows, rows};
+  return PartPlace{(g * L.part_rows + (L.packed ? (int64_t)tok0 * G + r0 : (int64_t)unit * rows)) * L.n_splits,
+                   min(rows, nrows - r0)};
+}
 
 // What a dense launch's lengths are, for one kv head, and the split made of them
 struct DenseScan {

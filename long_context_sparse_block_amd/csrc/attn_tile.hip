@@ -405,7 +405,9 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
     if (a.lse != nullptr && h == 0) a.lse[qrow * a.n_heads + qh] = l != 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
     return;
   }
-  const int64_t pr = (((int64_t)unit * a.n_kv_heads + g) * L.n_splits + split) * BM + wave * 32 + c32;
+  if (!live) return;
+  const PartPlace part = part_place<SEL>(L, a.n_kv_heads, G, BM, g, unit, tok0, r0, nrows);
+  const int64_t pr = part.begin + split * part.step + wave * 32 + c32;
   if (h == 0) L.part_ml[pr] = make_float2(m, l);
   if (l != 0.f) {
 #pragma unroll

@@ -419,7 +419,8 @@ __global__ void __launch_bounds__(kWaves * kWave, FP8 && (SEL || RT == 1 || D ==
   __syncthreads();
   if (wave != 0) return;
   add(1);
-  const int64_t part = (((int64_t)unit * a.n_kv_heads + g) * L.n_splits + split) * ROWS;
+  const PartPlace place = part_place<SEL>(L, a.n_kv_heads, G, ROWS, g, unit, tok0, 0, nrows);
+  const int64_t part = place.begin + split * place.step;
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int row = rt * 16 + c16;

@@ -368,7 +368,7 @@ def misa_attention_paged(q, k_pages, v_pages, block_table, q_start, kv_lens, k_s
     head_dim], bf16 or e4m3 codes with scale pools).  q_start int32 [n_seq + 1]
     and kv_lens int32 [n_seq] as misa_plan_pages gives them; max_new: a bound on
     the new tokens of any sequence, when the caller knows one (1 for a decode
-    batch).  scale: on q . k, 1 / sqrt(head_dim) unless given.  Returns (out
+    batch; without it the call prepares for any mix, see misa_attn_shape).  scale: on q . k, 1 / sqrt(head_dim) unless given.  Returns (out
     [tokens, heads, head_dim] bf16, lse [tokens, heads] fp32 or None); rows from
     q_start[-1] on are left as they were."""
     return _attention("misa_attention_paged", q, k_pages, v_pages, block_table, q_start, kv_lens, None, k_scale_pages,

@@ -77,3 +77,25 @@ def test_built_checks_that_do_not_load_are_an_error():
     assert run("ModuleNotFoundError('none', name=name)").startswith("ValueError True x is required")
     out = run("ImportError('undefined symbol: _Znwm')")
     assert out.startswith("RuntimeError False") and "undefined symbol" in out and "build" in out
+
+
+def attention_bytes(n_seq, tokens, max_new, heads=32, kv_heads=8, dim=128, fp8=False, width=256, page=64):
+    import long_context_sparse_block_amd as misa
+    shape = misa.AttnShape(n_seq, heads, kv_heads, dim, tokens, heads * dim, dim, max_new, 1.0)
+    return misa.misa_attention_paged_workspace_bytes(
+        shape, misa.KvPages(None, None, None, None, None, width, n_seq * width, page, int(fp8)))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_workspace_follows_the_rows_that_exist(dim, fp8):
+    """Parts are kept for at most two workgroups to each that the GPU holds (768 or 512 of up to 128 rows, 1024 of 32),
+    whatever max_new says: 768 x 2 x 128 rows and 1024 x 2 x 32 of dim fp32 values and two more."""
+    most = (2 * (768 if dim == 64 else 512) * 128 + 2 * 1024 * 32) * (dim + 2) * 4 + (1 << 20)
+    for n in (1, 2, 9, 64, 256, 1024, 4096):
+        for new in (1, 2, 7):
+            for max_new in (0, new):
+                assert attention_bytes(n, n * new, max_new, dim=dim, fp8=fp8) <= most, (n, new, max_new)
+    # few decodes: no more than 96 splits of the rows there are
+    for n in (1, 2, 3, 9):
+        assert attention_bytes(n, n, 0, dim=dim, fp8=fp8) <= 96 * n * 32 * (dim + 2) * 4 + (1 << 16)
