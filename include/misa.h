@@ -492,7 +492,9 @@ size_t misa_prefill_workspace_bytes(const misa_shape* shape, misa_kdtype kdtype,
  * cached_lens, new_lens: int32 [n_seq].  free_pages: int32 [n_free], NULL when
  * n_free = 0.  block_table: int32 [n_seq][max_pages].  slots: int64 [n_tokens],
  * positions: int32 [n_tokens].  1 <= n_seq <= 65535, page_keys >= 1,
- * max_pages >= 1, n_tokens <= 2^26 (larger: MISA_ERR_UNSUPPORTED).
+ * max_pages >= 1, n_tokens <= 2^26 (larger: MISA_ERR_UNSUPPORTED).  Outputs
+ * overlap neither inputs nor each other (MISA_ERR_INVALID_ARG): the kv_lens that
+ * a call fills are the next step's cached_lens only once it has other outputs.
  */
 misa_status misa_plan_pages(int32_t n_seq, const int32_t* cached_lens, const int32_t* new_lens, int32_t page_keys,
                             const int32_t* free_pages, int32_t n_free, int32_t* block_table, int64_t max_pages,

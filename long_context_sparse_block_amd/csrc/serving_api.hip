@@ -39,6 +39,15 @@ bool strides_apart(int64_t n_tokens, int64_t n_heads, int64_t head_dim, int64_t 
   return true;
 }
 
+struct Span {
+  const void* at;
+  int64_t bytes;   // 0: nothing there
+};
+inline bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
+  return a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+
 misa_status check_pool(int64_t n_pages, int32_t page_keys) {
   if (n_pages < 1 || page_keys < 1) return MISA_ERR_INVALID_ARG;
   if (n_pages >= kMaxSlots || n_pages * page_keys >= kMaxSlots) return MISA_ERR_UNSUPPORTED;
@@ -97,6 +106,16 @@ misa_status misa_plan_pages(int32_t n_seq, const int32_t* cached_lens, const int
   if (n_free > 0 && free_pages == nullptr) return MISA_ERR_INVALID_ARG;
   if (n_tokens > 0 && (slots == nullptr || positions == nullptr)) return MISA_ERR_INVALID_ARG;
   if (n_seq > 65535 || n_tokens > kMaxTokens || max_pages >= kMaxSlots) return MISA_ERR_UNSUPPORTED;
+  // workgroups read the inputs while others write
+  const Span in[] = {{cached_lens, 4 * (int64_t)n_seq}, {new_lens, 4 * (int64_t)n_seq}, {free_pages, 4 * (int64_t)n_free}};
+  const Span out[] = {{block_table, 4 * n_seq * max_pages}, {q_start, 4 * ((int64_t)n_seq + 1)}, {kv_lens, 4 * (int64_t)n_seq},
+                      {slots, 8 * n_tokens}, {positions, 4 * n_tokens}, {n_taken, 4}};
+  for (const Span& o : out) {
+    for (const Span& i : in)
+      if (overlap(o, i)) return MISA_ERR_INVALID_ARG;
+    for (const Span& p : out)
+      if (&p != &o && overlap(o, p)) return MISA_ERR_INVALID_ARG;
+  }
   return from_hip(misa::launch_plan_pages(n_seq, cached_lens, new_lens, page_keys, free_pages, n_free, block_table,
                                           max_pages, q_start, kv_lens, slots, positions, n_tokens, n_taken,
                                           (hipStream_t)stream));

@@ -159,7 +159,8 @@ def misa_plan_pages(cached_lens, new_lens, free_pages, block_table, page_keys: i
                     plan: PagePlan | None = None, stream=None) -> PagePlan:
     """Pages for the new tokens of every sequence: writes the new entries of
     block_table [n_seq, max_pages] (int32, in place) from free_pages (int32) and
-    returns the PagePlan.  n_tokens: length of the slot map (at least the sum of
+    returns the PagePlan (plan: its tensors, made new unless given, and none of
+    them among this call's inputs).  n_tokens: length of the slot map (at least the sum of
     new_lens; entries behind the last token get slot -1)."""
     if stream is not None:
         return _on(stream, misa_plan_pages, cached_lens, new_lens, free_pages, block_table, page_keys, n_tokens, plan)

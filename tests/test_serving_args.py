@@ -99,3 +99,32 @@ def test_workspace_follows_the_rows_that_exist(dim, fp8):
     # few decodes: no more than 96 splits of the rows there are
     for n in (1, 2, 3, 9):
         assert attention_bytes(n, n, 0, dim=dim, fp8=fp8) <= 96 * n * 32 * (dim + 2) * 4 + (1 << 16)
+
+
+# name, bytes of each array of a misa_plan_pages call of 4 sequences, 8 free pages, 10 table columns and 16 tokens
+PLAN_ARRAYS = [("cached", 16), ("new", 16), ("free", 32), ("table", 160), ("qs", 20), ("kv", 16), ("slots", 128), ("pos", 64),
+               ("taken", 4)]
+PLAN_INPUTS = ("cached", "new", "free")
+
+
+def plan_status(**at):
+    """Status of a call whose arrays lie apart, but for those given (addresses, never read)."""
+    import ctypes
+
+    import long_context_sparse_block_amd as misa
+    where = {name: 0x100000 + 0x1000 * i for i, (name, _) in enumerate(PLAN_ARRAYS)}
+    where.update(at)
+    p = {name: ctypes.c_void_p(a) for name, a in where.items()}
+    return misa.load().misa_plan_pages(4, p["cached"], p["new"], 64, p["free"], 8, p["table"], 10, p["qs"], p["kv"], p["slots"],
+                                       p["pos"], 16, p["taken"], None)
+
+
+def test_plan_refuses_outputs_over_its_arrays():
+    """Workgroups read the lengths and the free list while others write: the next step's cached_lens may not be the
+    kv_lens that the same call fills."""
+    for i, (a, bytes_a) in enumerate(PLAN_ARRAYS):
+        for b, bytes_b in PLAN_ARRAYS[i + 1:]:
+            if a in PLAN_INPUTS and b in PLAN_INPUTS:
+                continue   # (two inputs may be one array)
+            for apart in (0, bytes_a - 4, 4 - bytes_b):   # the same array, the last four bytes of either
+                assert plan_status(**{a: 0x800000, b: 0x800000 + apart}) == -1, (a, b, apart)
