@@ -136,11 +136,14 @@ except ImportError as e:   # built against another torch, say: every call raises
     _pool = _rows = _scratch = _dense
 
 
-def _on(stream, f, *args):
-    """f(*args) with `stream` as the current one: what f allocates is then
-    `stream`'s own memory, which no work of another stream may still be using."""
+def _on(stream, t, name, f, *args):
+    """f(*args) with `stream`, of tensor t's GPU, as the current one: what f
+    allocates is then `stream`'s own memory, which no work of another stream may
+    still be using."""
     if not isinstance(stream, torch.cuda.Stream):
         raise ValueError(f"stream: {stream!r}, expected a torch.cuda.Stream")
+    if stream.device_index != _dev(t, name):
+        raise ValueError(f"stream is on cuda:{stream.device_index}, {name} on {t.device}")
     with torch.cuda.stream(stream):
         return f(*args)
 
@@ -163,7 +166,8 @@ def misa_plan_pages(cached_lens, new_lens, free_pages, block_table, page_keys: i
     them among this call's inputs).  n_tokens: length of the slot map (at least the sum of
     new_lens; entries behind the last token get slot -1)."""
     if stream is not None:
-        return _on(stream, misa_plan_pages, cached_lens, new_lens, free_pages, block_table, page_keys, n_tokens, plan)
+        return _on(stream, cached_lens, "cached_lens", misa_plan_pages, cached_lens, new_lens, free_pages, block_table,
+                   page_keys, n_tokens, plan)
     dev = _dev(cached_lens, "cached_lens")
     n = cached_lens.shape[0]
     i32 = torch.int32
@@ -242,7 +246,7 @@ def misa_rope(x, positions, inv_freq, layout: str = "half", rot_start: int = 0, 
     head.  backward: the gradient with respect to x of x -> misa_rope(x, ...),
     given the gradient of its output.  out may be x (in place)."""
     if stream is not None:
-        return _on(stream, misa_rope, x, positions, inv_freq, layout, rot_start, mscale, backward, out)
+        return _on(stream, x, "x", misa_rope, x, positions, inv_freq, layout, rot_start, mscale, backward, out)
     dev = _dev(x, "x")
     xp, xst, xsh = _rows(x, _DTYPES, "x", dev)
     T, H, D = x.shape
@@ -271,8 +275,8 @@ def misa_write_pages(k, slots, k_pages, k_scale_pages=None, v=None, v_pages=None
     inv_freq, k is rotated first (misa_rope).  Slots outside the pool are
     skipped."""
     if stream is not None:
-        return _on(stream, misa_write_pages, k, slots, k_pages, k_scale_pages, v, v_pages, v_scale_pages, positions,
-                   inv_freq, layout, rot_start, mscale)
+        return _on(stream, k, "k", misa_write_pages, k, slots, k_pages, k_scale_pages, v, v_pages, v_scale_pages,
+                   positions, inv_freq, layout, rot_start, mscale)
     dev = _dev(k, "k")
     kp, kst, ksh = _rows(k, _BF16, "k", dev)
     T, H, D = k.shape
@@ -310,8 +314,8 @@ def misa_attention_selected_workspace_bytes(shape: AttnShape, pages: KvPages, to
 def _attention(name, q, k_pages, v_pages, block_table, q_start, kv_lens, idx, k_scale, v_scale, scale, max_new, out, lse,
                want_lse, ws, stream):
     if stream is not None:
-        return _on(stream, _attention, name, q, k_pages, v_pages, block_table, q_start, kv_lens, idx, k_scale, v_scale,
-                   scale, max_new, out, lse, want_lse, ws, None)
+        return _on(stream, q, "q", _attention, name, q, k_pages, v_pages, block_table, q_start, kv_lens, idx, k_scale,
+                   v_scale, scale, max_new, out, lse, want_lse, ws, None)
     dev = _dev(q, "q")
     qp, qst, qsh = _rows(q, _BF16, "q", dev)
     T, H, D = q.shape
@@ -369,8 +373,9 @@ def misa_attention_paged(q, k_pages, v_pages, block_table, q_start, kv_lens, k_s
     head_dim], bf16 or e4m3 codes with scale pools).  q_start int32 [n_seq + 1]
     and kv_lens int32 [n_seq] as misa_plan_pages gives them; max_new: a bound on
     the new tokens of any sequence, when the caller knows one (1 for a decode
-    batch; without it the call prepares for any mix, see misa_attn_shape).  scale: on q . k, 1 / sqrt(head_dim) unless given.  Returns (out
-    [tokens, heads, head_dim] bf16, lse [tokens, heads] fp32 or None); rows from
+    batch; without it the call prepares for any mix, see misa_attn_shape).
+    scale: on q . k, 1 / sqrt(head_dim) unless given.  Returns (out [tokens,
+    heads, head_dim] bf16, lse [tokens, heads] fp32 or None); rows from
     q_start[-1] on are left as they were."""
     return _attention("misa_attention_paged", q, k_pages, v_pages, block_table, q_start, kv_lens, None, k_scale_pages,
                       v_scale_pages, scale, max_new, out, lse, want_lse, ws, stream)

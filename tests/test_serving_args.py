@@ -128,3 +128,27 @@ def test_plan_refuses_outputs_over_its_arrays():
                 continue   # (two inputs may be one array)
             for apart in (0, bytes_a - 4, 4 - bytes_b):   # the same array, the last four bytes of either
                 assert plan_status(**{a: 0x800000, b: 0x800000 + apart}) == -1, (a, b, apart)
+
+
+def test_a_stream_of_another_gpu_is_refused(monkeypatch):
+    """Work goes to the stream that the caller names, or nowhere."""
+    import torch
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    import long_context_sparse_block_amd as misa
+
+    class Stream:
+        device_index = 1
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    with FakeTensorMode():
+        x = torch.empty((3, 2, 64), dtype=torch.bfloat16, device="cuda")   # on GPU 0
+        n = torch.empty((3,), dtype=torch.int32, device="cuda")
+    at = dict(stream=Stream())
+    for call in (lambda: misa.misa_rope(x, n, None, **at), lambda: misa.misa_write_pages(x, n, x, **at),
+                 lambda: misa.misa_plan_pages(n, n, n, n, 16, 3, **at),
+                 lambda: misa.misa_attention_paged(x, x, x, n, n, n, **at),
+                 lambda: misa.misa_attention_selected(x, x, x, n, n, n, n, **at)):
+        with pytest.raises(ValueError, match="stream.*cuda:1.*cuda:0"):
+            call()
+    with pytest.raises(ValueError, match="stream"):
+        misa.misa_rope(x, n, None, stream=7)
