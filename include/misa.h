@@ -603,9 +603,15 @@ typedef struct {
  * through the formulas; in a value among a sequence's new tokens they may reach
  * its earlier new tokens too, never another sequence.
  * q: bf16.  out: bf16 [n_tokens][n_heads][head_dim] dense, lse: float
- * [n_tokens][n_heads] or NULL.  kv_lens[b] past max_pages * page_keys counts
- * as that.  ws: misa_attention_paged_workspace_bytes() bytes (16-byte
- * aligned; may be NULL when that is 0); nothing in it outlives the call.
+ * [n_tokens][n_heads] or NULL; neither overlaps an input.  Where kv_lens[b] is
+ * past max_pages * page_keys, positions are still those of the true length, as
+ * in the page plan, and the keys without a table entry are not read.
+ * ws: misa_attention_paged_workspace_bytes() bytes (16-byte aligned; may be NULL
+ * when that is 0); nothing in it outlives the call.
+ * Calls of more than 2^23 workgroups are MISA_ERR_UNSUPPORTED, and the workspace
+ * query gives 0.  With G = n_heads / n_kv_heads and for each kv head these are
+ * at most n_seq, and n_tokens * G / 64 + n_seq of chunks' rows (n_tokens * G /
+ * 128 where more than 64 rows of a kv head may be one sequence's).
  */
 misa_status misa_attention_paged(const misa_attn_shape* shape, const misa_kv_pages* pages, const uint16_t* q,
                                  const int32_t* q_start, const int32_t* kv_lens, uint16_t* out, float* lse, void* ws,
@@ -617,7 +623,8 @@ size_t misa_attention_paged_workspace_bytes(const misa_attn_shape* shape, const 
  * tokens idx[t][0..topk-1] of its sequence (an indexer call's idx viewed as
  * [n_tokens][topk]).  Entries that are negative or lie behind the token's own
  * position count as absent; an id listed twice counts twice.
- * idx: int32 [n_tokens][topk], 1 <= topk <= MISA_MAX_TOPK.
+ * idx: int32 [n_tokens][topk], 1 <= topk <= MISA_MAX_TOPK.  Workgroups (see
+ * above) for each kv head: n_tokens, times ceil(G / 128) where G > 64.
  */
 misa_status misa_attention_selected(const misa_attn_shape* shape, const misa_kv_pages* pages, const uint16_t* q,
                                     const int32_t* q_start, const int32_t* kv_lens, const int32_t* idx, int32_t topk,

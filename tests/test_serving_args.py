@@ -152,3 +152,23 @@ def test_a_stream_of_another_gpu_is_refused(monkeypatch):
             call()
     with pytest.raises(ValueError, match="stream"):
         misa.misa_rope(x, n, None, stream=7)
+
+
+def test_attention_grids_past_their_bound_are_refused():
+    """More than 2^23 workgroups: unsupported, and no workspace is asked for."""
+    import ctypes
+
+    import long_context_sparse_block_amd as misa
+    lib, at = misa.load(), ctypes.c_void_p(0x100000)   # (never read)
+    ref = ctypes.byref
+    pages = misa.KvPages(0x100000, 0x100000, None, None, 0x100000, 8, 20, 64, 0)
+    for n_seq, heads, kv, tokens, topk in ((2, 32, 8, (1 << 20) + 1, 64), (2, 1024, 1, (1 << 20) + 1, 2048),
+                                           (65535, 1024, 1024, 65535, 0), (1, 1024, 1, (1 << 20) + 64, 0)):
+        shape = misa.AttnShape(n_seq, heads, kv, 128, tokens, 0, 0, 0, 1.0)
+        if topk:
+            st = lib.misa_attention_selected(ref(shape), ref(pages), at, at, at, at, topk, at, None, at, 1 << 40, None)
+            need = misa.misa_attention_selected_workspace_bytes(shape, pages, topk)
+        else:
+            st = lib.misa_attention_paged(ref(shape), ref(pages), at, at, at, at, None, at, 1 << 40, None)
+            need = misa.misa_attention_paged_workspace_bytes(shape, pages)
+        assert st == -2 and need == 0, (n_seq, heads, kv, tokens, topk)
