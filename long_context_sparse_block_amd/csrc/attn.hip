@@ -165,8 +165,7 @@ AttnPlan make_plan(const misa_attn_shape& s, const misa_kv_pages& pg, int topk) 
   p.wave_units = (int)wave_units;
   p.tile_units = (int)tile_units;
   if (p.RT > 0) {
-    // resident workgroups a CU: what their LDS lets in (128 KB of bf16 tiles at head_dim 128)
-    p.wave_slots = 256 * (pg.kdtype == MISA_K_FP8_E4M3 ? 2 : 1) * (s.head_dim == 64 ? 2 : 1);
+    p.wave_slots = 256 * wave_groups(s.head_dim, pg.kdtype == MISA_K_FP8_E4M3, topk > 0, p.RT);
     p.wave_splits = choose_splits(wave_units * KH, p.wave_slots, (ctx + 127) / 128, 64, topk > 0);
   }
   if (p.NW > 0) {

@@ -153,6 +153,18 @@ __device__ __forceinline__ bf16x8 load_q(const uint16_t* p, uint32_t flip) {
   return as_bf16x8(make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip));
 }
 
+// Workgroups of attn_wave that a CU holds, and so waves of a SIMD: what the LDS
+// lets in over bf16 pages (128 KB of tiles at head_dim 128), the registers over
+// e4m3 pages.  With 32 rows of 128 two waves spill ten registers: over selected
+// tokens, bound by the vector unit, they are better all the same (1000 x 2048
+// picks, 64 / 2 heads: 196 us, alone 246), in decodes one is (64 of 8..16K keys:
+// 119 us, with two 133).
+constexpr int wave_groups(int D, bool fp8, bool sel, int RT) {
+  if (!fp8) return D == 64 ? 2 : 1;
+  if (D == 64) return RT == 1 ? 3 : 2;
+  return sel || RT == 1 ? 2 : 1;
+}
+
 // What a launch adds to the arguments
 struct AttnLaunch {
   int n_units;      // row tiles (attn_tile), or sequences / tokens (attn_wave)

@@ -37,12 +37,8 @@ constexpr int kWT = 32;      // keys of a wave's tile
 constexpr int kWaves = 4;
 }  // namespace
 
-// Waves of a SIMD, at least: e4m3 tiles take half the LDS, so that two fit.  With 32
-// rows of 128 that spills ten registers: over selected tokens, bound by the
-// vector unit, two waves are better all the same (1000 x 2048 picks, 64 / 2 heads:
-// 196 us, alone 246), in decodes one is (64 of 8..16K keys: 126 us against 133).
 template <int D, bool FP8, bool SEL, int RT>
-__global__ void __launch_bounds__(kWaves * kWave, FP8 && (SEL || RT == 1 || D == 64) ? 2 : 1) k_attn_wave(const AttnArgs a, const AttnLaunch L) {
+__global__ void __launch_bounds__(kWaves * kWave, wave_groups(D, FP8, SEL, RT)) k_attn_wave(const AttnArgs a, const AttnLaunch L) {
   constexpr int RB = D * 2, P = D / 8, RPI = kWave / P;    // bf16: bytes and 16-byte pieces of a row, rows of a load
   constexpr int PC = D / 16, RPC = kWave / PC;              // e4m3: pieces of a row, rows of a load
   constexpr int KS = D / 32, DB = D / 16;

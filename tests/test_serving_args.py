@@ -172,3 +172,16 @@ def test_attention_grids_past_their_bound_are_refused():
             st = lib.misa_attention_paged(ref(shape), ref(pages), at, at, at, at, None, at, 1 << 40, None)
             need = misa.misa_attention_paged_workspace_bytes(shape, pages)
         assert st == -2 and need == 0, (n_seq, heads, kv, tokens, topk)
+
+
+@pytest.mark.parametrize("dim,fp8,heads,groups", [(128, False, 32, 1), (64, False, 32, 2), (128, True, 32, 2), (128, True, 256, 1),
+                                                  (64, True, 32, 3), (64, True, 256, 2)])
+def test_decodes_split_for_the_workgroups_a_cu_holds(dim, fp8, heads, groups):
+    """Two splits to each workgroup that the GPU holds: 256 CUs of `groups` (e4m3 with 32 rows of 128: one)."""
+    rows, kv = heads // 8, 8
+    for n in (1, 3, 17, 32, 50, 64, 65, 100, 128, 200):
+        units = n * kv
+        splits = 1 if units >= 512 * groups else min(-(-512 * groups // units), 64, 128 // 4)
+        part = splits * units * rows * 4
+        want = 0 if splits == 1 else sum(-(-x // 256) * 256 for x in (part * dim, part * 2, 16 * n))
+        assert attention_bytes(n, n, 1, heads=heads, kv_heads=kv, dim=dim, fp8=fp8) == want, n
