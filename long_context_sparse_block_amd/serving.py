@@ -5,7 +5,8 @@ the indexer picked.
 
 As in _lib: argument marshalling only, raw device pointers and the current HIP
 stream (of the tensors' own device) go to the library, and there is no
-fallback.
+fallback.  misa_rope takes part in autograd; the other calls serve, and their
+outputs have no gradient.
 """
 from __future__ import annotations
 
@@ -238,16 +239,41 @@ def _rope_spec(positions, inv_freq, layout, rot_start, mscale, backward, n_token
                            _LAYOUTS[layout], 1 if backward else 0, mscale)
 
 
+class _Rope(torch.autograd.Function):
+    """misa_rope of an x that requires a gradient, which is the other rotation of
+    the output's."""
+
+    @staticmethod
+    def forward(ctx, x, positions, inv_freq, layout, rot_start, mscale, backward):
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.how = layout, rot_start, mscale
+        ctx.turned_back = backward
+        return misa_rope(x, positions, inv_freq, layout, rot_start, mscale, backward)
+
+    @staticmethod
+    def backward(ctx, g):
+        positions, inv_freq = ctx.saved_tensors
+        if g.stride(-1) != 1:   # (expanded, say)
+            g = g.contiguous()
+        return (misa_rope(g, positions, inv_freq, *ctx.how, not ctx.turned_back),) + (None,) * 6
+
+
 def misa_rope(x, positions, inv_freq, layout: str = "half", rot_start: int = 0, mscale: float = 1.0,
               backward: bool = False, out=None, stream=None):
     """Rotary positions of x [tokens, heads, head_dim] (bf16, fp16 or fp32; any
     token and head strides).  inv_freq, mscale: as rope_inv_freq gives them; the
     rotary part is elements rot_start .. rot_start + 2 len(inv_freq) - 1 of a
     head.  backward: the gradient with respect to x of x -> misa_rope(x, ...),
-    given the gradient of its output.  out may be x (in place)."""
+    given the gradient of its output.  out may be x (in place).
+    Where x requires a gradient the result carries it (positions and inv_freq are
+    read again then); a given out cannot."""
     if stream is not None:
         return _on(stream, x, "x", misa_rope, x, positions, inv_freq, layout, rot_start, mscale, backward, out)
     dev = _dev(x, "x")
+    if x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("out takes no gradient: x requires one")
+        return _Rope.apply(x, positions, inv_freq, layout, rot_start, mscale, backward)
     xp, xst, xsh = _rows(x, _DTYPES, "x", dev)
     T, H, D = x.shape
     if out is None:
