@@ -26,7 +26,9 @@ constexpr int kThreads = 256;
 constexpr int64_t kMaxGroups = 1 << 20;   // workgroups of a launch (it holds fewer than 2^32 threads)
 constexpr double kInv2Pi = 0.15915494309189533576888;
 
-// cos and sin of `turns` whole turns, times m
+// cos and sin of `turns` whole turns, times m.  The first rounds the reduced angle
+// to fp32 (2^-25 of a half turn, 2^-23.3 in the functions): under a hundredth of a
+// step of the 16-bit types it serves.
 __device__ __forceinline__ float2 turn_f32(double turns, double m) {
   const float r = (float)(2.0 * (turns - __builtin_rint(turns)));   // half turns in [-1, 1]
   float s, c;
@@ -91,7 +93,13 @@ __global__ void __launch_bounds__(kThreads) k_rope(const typename Elem<DT>::T* x
     const int nt = (int)min((int64_t)TT, n_tokens - t0);
     for (int i = threadIdx.x; i < nt * r.half; i += kThreads) {
       const int t = i / r.half, j = i - t * r.half;
-      s_cs[i] = turn_f32((double)r.positions[t0 + t] * (r.inv_freq[j] * kInv2Pi), r.mscale);
+      const double turns = (double)r.positions[t0 + t] * (r.inv_freq[j] * kInv2Pi);
+      if constexpr (DT == MISA_T_FP32) {
+        const double2 cs = turn_f64(turns, r.mscale);
+        s_cs[i] = make_float2((float)cs.x, (float)cs.y);
+      } else {
+        s_cs[i] = turn_f32(turns, r.mscale);
+      }
     }
     __syncthreads();
     const int total = nt * H * units;
