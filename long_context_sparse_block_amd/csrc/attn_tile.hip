@@ -13,6 +13,12 @@
 // to 1000 TFLOP/s where the library's product reaches 1327).  At head_dim 64 over
 // e4m3 pages the vector unit is the bound (70%: exponentials and scales; 9
 // sequences of 0..515 new tokens over up to 5003 keys, 20 / 4 heads: 80-98 us a call).
+// The weights enter the second product as one bf16 each (half a step, 2^-8, of a
+// weight; a row's error is then about sqrt 2 of its output's own rounding).  A
+// second part, what the rounding left, is another 16 matrix instructions a tile,
+// and not hidden even where loads bound the kernel: over selected tokens, 64 x 2048
+// picks of 64 / 1 heads of 128 26.4 -> 27.8 us, 1000 x 2048 146 -> 169, of 128 / 1
+// heads 172 -> 214.
 // 32 rows a wave: with 64, or with scores formed a tile ahead, the registers
 // leave one wave a SIMD, and both were slower (1.17 to 1.6 ms).  NW = 2 where a
 // unit has at most 64 rows: half the rows of 4 would be empty.
