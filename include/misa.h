@@ -463,8 +463,10 @@ size_t misa_prefill_workspace_bytes(const misa_shape* shape, misa_kdtype kdtype,
  * 0 .. q_start[n_seq]-1 of token-major tensors: sequence b's new tokens are
  * rows q_start[b] .. q_start[b+1]-1, in order, and are the last ones of its
  * kv_lens[b] tokens, so new token i of m sits at position kv_lens[b] - m + i.
- * Lengths live on the GPU and are read there; rows from q_start[n_seq] on
- * (a padded batch) are left as they were.
+ * Lengths live on the GPU and are read there.  Rows from q_start[n_seq] on (a
+ * padded batch) are left as they were: in out and lse of the attention calls,
+ * and in the pages, where their slot is -1.  misa_rope knows no sequences and
+ * turns every row by its position, a padded one (-1) too.
  * Strided inputs.  Where a stride is given it counts elements; the last
  * dimension is dense.
  * Slots.  Row r of page p of a pool with page_keys rows a page is slot
@@ -599,9 +601,12 @@ typedef struct {
  * One call takes decodes (one new token), chunks and both mixed.  Products
  * accumulate in fp32; softmax statistics are fp32; the softmax weights enter
  * the product with v as bf16 (in two parts where a kv head has few rows).
- * NaN and infinity in the keys and values that a row sees take their course
- * through the formulas; in a value among a sequence's new tokens they may reach
- * its earlier new tokens too, never another sequence.
+ * NaN in the keys and values that a row sees shows in its out (and, of keys, in
+ * lse).  A score of +infinity gives NaN in both, one of -infinity a weight of 0;
+ * an infinite value makes the elements it enters infinite or NaN (a weight, or
+ * its second part, may round to 0).  NaN and infinity in a value among a
+ * sequence's new tokens may reach its earlier new tokens too, never another
+ * sequence; what a row of selected tokens does not list never reaches it.
  * q: bf16.  out: bf16 [n_tokens][n_heads][head_dim] dense, lse: float
  * [n_tokens][n_heads] or NULL; neither overlaps an input.  Where kv_lens[b] is
  * past max_pages * page_keys, positions are still those of the true length, as

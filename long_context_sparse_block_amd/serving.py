@@ -201,7 +201,11 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str | None = 
                 which stretches the lowest frequency by factor and leaves the highest
       "yarn"    f_j where pair j turns more than beta_fast times within original_max
                 positions, f_j / factor where fewer than beta_slow, a linear ramp over j
-                between; mscale 0.1 ln(factor) + 1
+                between; mscale 0.1 ln(factor) + 1, on queries and keys alike.
+                A model that scales its attention's logits by the square of that
+                instead (its configuration then gives the same factor for all
+                dimensions) takes the frequencies with mscale 1, and
+                scale = mscale ** 2 / sqrt(head_dim) in the attention calls.
     """
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError(f"rotary_dim: {rotary_dim}, expected a positive even number")

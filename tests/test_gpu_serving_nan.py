@@ -140,3 +140,43 @@ def test_a_token_that_no_list_names_reaches_no_row(heads, kv_heads, dim, topk, f
         p.pages[1][0].view(torch.uint8).fill_(0x7F)
         for a, b in zip(run(p, idx), want):
             assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- infinities
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new", [1, 40])
+def test_an_infinite_value_shows_where_it_is_seen(new, fp8):
+    """Infinite or NaN (a weight's second part may be 0) in the elements it enters, nothing elsewhere."""
+    say("infinite value", new, fp8)
+    p = ref.Paged(26, [400, 90], [new, 1], 8, 2, 64, 16, fp8)
+    clean, clean_lse = run(p)
+    poison(p, 1, 0, [70], value=math.inf)
+    out, lse = run(p)
+    bad = ~torch.isfinite(out[:new, :4])
+    assert bool(bad.all()) if fp8 else bool(bad[..., 3].all()) and int(bad.sum()) == new * 4
+    assert torch.equal(out[:new, 4:], clean[:new, 4:]) and torch.equal(out[new:], clean[new:]) and torch.equal(lse, clean_lse)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_infinite_scores(new):
+    """A score of plus infinity gives NaN in out and lse; one of minus infinity is a weight of 0."""
+    say("infinite score", new)
+    p = ref.Paged(27, [400, 90], [new, 1], 8, 2, 64, 16)
+    p.q[:new, :4, 3] = 1.0
+    want = run(p)
+    poison(p, 0, 0, [70], value=math.inf)
+    out, lse = run(p)
+    assert bool(torch.isnan(out[:new, :4]).all()) and bool(torch.isnan(lse[:new, :4]).all())
+    assert torch.equal(out[:new, 4:], want[0][:new, 4:]) and torch.equal(out[new:], want[0][new:])
+    poison(p, 0, 0, [70], value=-math.inf)
+    idx = torch.arange(400, dtype=torch.int32).expand(p.tokens, 400).clone()
+    without = idx.clone()
+    without[:, 70] = -1
+    out, lse = run(p)
+    picked, picked_lse = run(p, idx)
+    want, want_lse, tol, ltol = ref.attention(p, without)
+    for o, l in ((out, lse), (picked, picked_lse)):
+        o, l = o.double().cpu()[:new, :4], l.double().cpu()[:new, :4]
+        assert bool(((o - want[:new, :4]).abs() <= tol[:new, :4]).all())
+        assert bool(((l - want_lse[:new, :4]).abs() <= ltol[:new, :4]).all())
