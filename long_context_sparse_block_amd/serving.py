@@ -170,6 +170,7 @@ def misa_plan_pages(cached_lens, new_lens, free_pages, block_table, page_keys: i
         return _on(stream, cached_lens, "cached_lens", misa_plan_pages, cached_lens, new_lens, free_pages, block_table,
                    page_keys, n_tokens, plan)
     dev = _dev(cached_lens, "cached_lens")
+    _dev(free_pages, "free_pages"), _dev(block_table, "block_table")
     n = cached_lens.shape[0]
     i32 = torch.int32
     if plan is None:

@@ -185,3 +185,26 @@ def test_decodes_split_for_the_workgroups_a_cu_holds(dim, fp8, heads, groups):
         part = splits * units * rows * 4
         want = 0 if splits == 1 else sum(-(-x // 256) * 256 for x in (part * dim, part * 2, 16 * n))
         assert attention_bytes(n, n, 1, heads=heads, kv_heads=kv, dim=dim, fp8=fp8) == want, n
+
+
+def test_missing_arguments_are_named():
+    import torch
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    import long_context_sparse_block_amd as misa
+    with FakeTensorMode():
+        n = torch.empty((3,), dtype=torch.int32, device="cuda")
+        table = torch.empty((3, 4), dtype=torch.int32, device="cuda")
+        x = torch.empty((3, 2, 64), dtype=torch.bfloat16, device="cuda")
+        pages = torch.empty((5, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
+        plan = [n, n, n, table]
+        for i, name in enumerate(("cached_lens", "new_lens", "free_pages", "block_table")):
+            with pytest.raises(ValueError, match=f"^{name} is required$"):
+                misa.misa_plan_pages(*plan[:i], None, *plan[i + 1:], 16, 3)
+        for i, name in enumerate(("q", "k_pages", "v_pages", "block_table")):
+            args = [x, pages, pages, table]
+            args[i] = None
+            with pytest.raises(ValueError, match=f"^{name} is required$"):
+                misa.misa_attention_paged(*args, n, n)
+        with pytest.raises(ValueError, match="^inv_freq is required$"):
+            misa.misa_rope(x, n, None)
