@@ -383,7 +383,8 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, const AttnLaunch& L
 // for all its units; else neighbours go round the XCDs.  Where an XCD would get
 // some splits only, of which a dense unit uses the first ones, the pairs move on
 // an XCD every 2^turn units, so that all XCDs get as many splits in use (8 x 256
-// tokens over 2700 keys, 4 kv heads, three of four splits in use: 117 -> 98 us).
+// tokens over 2700 keys, 20 / 4 heads of 128, three of four splits in use: 117 -> 98
+// us).
 struct Place {
   int unit, g, split;
 };

@@ -12,7 +12,9 @@
 // the other (2048 tokens over 32K keys, 32 / 8 heads of 128: 1.07-1.15 ms by card, 930
 // to 1000 TFLOP/s where the library's product reaches 1327).  At head_dim 64 over
 // e4m3 pages the vector unit is the bound (70%: exponentials and scales; 9
-// sequences of 0..515 new tokens over up to 5003 keys, 20 / 4 heads: 80-98 us a call).
+// sequences of 0..515 new tokens over up to 5003 keys, 20 / 4 heads: 78-98 us a call).
+// The 2048 tokens over e4m3 pages 1.14 ms, with heads of 64 0.63 ms (850 TFLOP/s),
+// e4m3 0.73 (732).
 // The weights enter the second product as one bf16 each (half a step, 2^-8, of a
 // weight; a row's error is then about sqrt 2 of its output's own rounding).  A
 // second part, what the rounding left, is another 16 matrix instructions a tile,

@@ -25,9 +25,10 @@
 // e4m3: 243 to 249 us), but few rows with a few heavy keys average a weight's
 // rounding out too little.
 //
-// Measured: 64 decodes over 8..16K keys, 32 / 8 heads of 128: bf16 577 us (3.2 GB, 5.5
-// TB/s), e4m3 363 us; one token over 32K keys 38 us; 1000 tokens x 2048 picks, 32 / 4
-// heads, e4m3: 249 us (2.1 GB of gathered rows; vector unit 50%, LDS 31%, MFMA 19%).
+// Measured: 64 decodes over 8..16K keys, 32 / 8 heads of 128: bf16 577-599 us by card
+// (3.2 GB, 5.4 TB/s), e4m3 346-363 us; one token over 32K keys 37 us; 1000 tokens x
+// 2048 picks, 32 / 4 heads, e4m3: 249-253 us (2.1 GB of gathered rows; vector unit
+// 51%, LDS 30%, MFMA 18%), bf16 490 us.
 #include "attn_device.h"
 
 namespace misa {

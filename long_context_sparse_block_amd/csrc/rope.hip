@@ -9,11 +9,15 @@
 // every head.
 //
 // Both kernels are bound by HBM: each value is read once and written once, 16
-// bytes a lane and access where the sizes are multiples of it.  Measured: 8192
-// tokens x 64 heads of 128 in bf16 in 50.7 us (5.3 TB/s, a copy's rate); keys and
-// values of 4099 tokens x 8 heads of 128 into bf16 pages in 9.4 us (3.6 TB/s, held
-// by the way from slot and row to the page: one pass of rows to a thread); 8192
-// index keys into e4m3 pages in 6.2 us.
+// bytes a lane and access where the sizes are multiples of it.  Measured, with
+// inputs that are not in the caches: 8192 tokens x 64 heads of 128 in bf16 in 50.4
+// us (5.3 TB/s, a copy's rate); keys and values of 4099 tokens x 8 heads of 128
+// into bf16 pages in 10.3 us (3.3 TB/s, held by the way from slot and row to the
+// page: one pass of rows to a thread); 8192 index keys into e4m3 pages in 6.1 us.
+// Off 16-byte pieces, one element a lane: 8192 x 32 heads of 80, 20 of them turned,
+// bf16 52 us (1.6 TB/s), fp32 66 us (2.5 TB/s).  8192 x 8 + 8 heads of 128 into
+// pages: bf16 16.3 us, e4m3 29.2 (fp64 angles and rotation), not turned 12.2 and
+// 17.1, at an odd offset (60 values from 3 on) 25.7 and 37.1.
 #include <algorithm>
 
 #include "misa_common.h"

@@ -271,7 +271,7 @@ def misa_rope(x, positions, inv_freq, layout: str = "half", rot_start: int = 0, 
     head.  backward: the gradient with respect to x of x -> misa_rope(x, ...),
     given the gradient of its output.  out may be x (in place).
     Where x requires a gradient the result carries it (positions and inv_freq are
-    read again then); a given out cannot."""
+    read again then, and have none themselves); a given out cannot."""
     if stream is not None:
         return _on(stream, x, "x", misa_rope, x, positions, inv_freq, layout, rot_start, mscale, backward, out)
     dev = _dev(x, "x")
