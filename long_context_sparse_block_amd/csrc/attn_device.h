@@ -155,7 +155,7 @@ __device__ __forceinline__ bf16x8 load_q(const uint16_t* p, uint32_t flip) {
 
 // Workgroups of attn_wave that a CU holds, and so waves of a SIMD: what the LDS
 // lets in over bf16 pages (128 KB of tiles at head_dim 128), the registers over
-// e4m3 pages.  With 32 rows of 128 two waves spill ten registers: over selected
+// e4m3 pages.  With 32 rows of 128 two waves spill some registers: over selected
 // tokens, bound by the vector unit, they are better all the same (1000 x 2048
 // picks, 64 / 2 heads: 196 us, alone 246), in decodes one is (64 of 8..16K keys:
 // 119 us, with two 133).
