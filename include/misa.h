@@ -637,6 +637,119 @@ misa_status misa_attention_selected(const misa_attn_shape* shape, const misa_kv_
 size_t misa_attention_selected_workspace_bytes(const misa_attn_shape* shape, const misa_kv_pages* pages, int32_t topk);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Trees of drafted tokens.  A step that verifies drafts takes a sequence's new
+ * tokens as a tree instead of a chain: a new token is a child of another one or
+ * of the sequence's last cached token, and sees the cached prefix, its
+ * ancestors and itself.  The new tokens' keys and values are written to the
+ * places behind the prefix in the tokens' order (misa_plan_pages' slots, and
+ * misa_write_pages with this plan's positions); once a path of the tree is
+ * accepted, misa_keep_path moves its rows to where the prefix goes on.  A
+ * sequence with one new token is a tree of one, and one whose every token is the
+ * child of the token before it sees what misa_attention_paged's rows see.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * parents[t], of new token i of its sequence (row t = q_start[b] + i): the
+ * index of its parent among the sequence's new tokens, in 0 .. i-1; -1, or any
+ * other value, makes it a child of the last cached token.  Writes
+ *   mask[t][..]   ancestor bits: bit j of the row is set where new token j is an
+ *                 ancestor of token i or i itself (bit j % 32 of word j / 32).
+ *                 Ancestors from 32 * words on have no bit.
+ *   positions[t]  kv_lens[b] - m + depth, m the sequence's new tokens, depth the
+ *                 number of the token's ancestors among them: its place in the
+ *                 text that it is drafted for, which misa_rope turns it by
+ * Rows that are no sequence's (in front of q_start[0], from q_start[n_seq] on)
+ * get an empty mask and position -1.
+ * parents: int32 [n_tokens]; q_start, kv_lens as misa_plan_pages writes them.
+ * mask: uint32 [n_tokens][words], positions: int32 [n_tokens]; they overlap
+ * nothing else.  1 <= words <= 1024, 1 <= n_seq <= 65535, n_tokens <= 2^26.
+ */
+misa_status misa_plan_tree(int32_t n_seq, const int32_t* parents, const int32_t* q_start, const int32_t* kv_lens,
+                           int64_t n_tokens, int32_t words, uint32_t* mask, int32_t* positions, void* stream);
+
+/*
+ * misa_attention_paged over trees: new token i of a sequence of m sees its
+ * kv_lens[b] - m cached tokens, and new token j where bit j of its mask row is
+ * set and j < m (any bits: the mask need not come from misa_plan_tree).  The
+ * mask is read for the rows of sequences only.  A row that sees nothing gives
+ * out = 0, lse = -inf.  All else is as in misa_attention_paged, workspace and
+ * limits too; NaN and infinity in a value among a sequence's new tokens may reach
+ * others of its new tokens, never another sequence.
+ * mask: uint32 [n_tokens][words], 1 <= words <= 1024 (MISA_ERR_UNSUPPORTED past it).
+ */
+misa_status misa_attention_tree(const misa_attn_shape* shape, const misa_kv_pages* pages, const uint16_t* q,
+                                const int32_t* q_start, const int32_t* kv_lens, const uint32_t* mask, int32_t words,
+                                uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+size_t misa_attention_tree_workspace_bytes(const misa_attn_shape* shape, const misa_kv_pages* pages);
+
+/*
+ * The accepted path's rows to their places behind the cached prefix.  path[b][..]
+ * names new tokens of sequence b in rising order (a path from a root down, as
+ * parents come before their children); it ends at the first entry that does not
+ * rise, is negative or is not below the sequence's count of new tokens.  With c
+ * entries and first = kv_lens[b] - m, row first + path[b][i] of the keys (the
+ * values, their scales) becomes row first + i, for i < c, and kept_lens[b] =
+ * first + c: the next step's cached_lens.  Rows from kept_lens[b] on are left
+ * as they are, to be written over.
+ * Every layer's pages take a call of their own, the index keys' too (n_heads = 1,
+ * v_pages = NULL).  Rows whose table entry is missing (past max_pages, or not in
+ * [0, n_pages)) are not moved.  Sequences share no page that holds new tokens.
+ * path: int32 [n_seq][max_path], max_path <= 2^20.  kept_lens: int32 [n_seq],
+ * overlapping nothing else.  Pools as misa_write_pages takes them.
+ */
+misa_status misa_keep_path(int32_t n_seq, const int32_t* path, int32_t max_path, const int32_t* q_start,
+                           const int32_t* kv_lens, const int32_t* block_table, int64_t max_pages, int32_t n_heads,
+                           int32_t head_dim, void* k_pages, void* v_pages, misa_kdtype kdtype, float* k_scale_pages,
+                           float* v_scale_pages, int64_t n_pages, int32_t page_keys, int32_t* kept_lens, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Products with e4m3 weights that have a scale for each block of 128 x 128, and
+ * activations with one for each 1 x 128: the projections around the indexer and
+ * the attention (queries, index queries and keys, outputs).
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * e4m3 codes of x [rows][cols] and the scales of its blocks of block_rows (1 or
+ * 128) x 128; the last block of a row of blocks, and the last row of blocks, may be
+ * smaller:
+ *   scale = fp32(amax / 448), at least 2^-126; 1 for a block of zeros
+ *   codes = e4m3fn round-to-nearest-even of fp32(x / scale)
+ * the rule of misa_quantize_q, which this call equals bit for bit for heads of 128
+ * (block_rows = 1) but where a row's values all lie below 448 * 2^-126.  NaN becomes the NaN code and leaves its block's scale
+ * alone; a block with an infinity has scale infinity, its infinities NaN codes,
+ * the rest 0.
+ * x: bf16, fp16 or fp32, row stride x_stride (elements), 16-byte aligned rows.
+ * codes: [rows][cols] dense, 16-byte aligned.  scale: float
+ * [ceil(rows / block_rows)][ceil(cols / 128)].  cols: a multiple of 16, up to 2^20;
+ * rows * ceil(cols / 128) <= 2^27 (else MISA_ERR_UNSUPPORTED).
+ */
+misa_status misa_quantize_blocks(const void* x, misa_dtype dtype, int64_t rows, int64_t cols, int64_t x_stride,
+                                 int32_t block_rows, uint8_t* codes, float* scale, void* stream);
+
+/*
+ *   out[i][j] = sum_b x_scale[i][b] w_scale[j / 128][b] sum_{128 b <= c < 128 (b + 1)} x[i][c] w[j][c]
+ * x: e4m3 codes [m][k], w: e4m3 codes [n][k] (a linear layer's weight), row strides
+ * in bytes and multiples of 16, rows 16-byte aligned.  x_scale: float
+ * [m][ceil(k / 128)], w_scale: float [ceil(n / 128)][ceil(k / 128)], dense.  out:
+ * bf16 [m][n], row stride out_stride >= n (elements), overlapping no input.
+ * A block's sum is formed by the matrix units (about 2^-14 of sum |x w| of the
+ * block off), scaled and added up in fp32; out is rounded once.  The order of the sums is
+ * fixed: the same call gives the same bits.  NaN codes and scales show in the
+ * rows and columns that they are in.
+ * k: a multiple of 16, up to 2^20 (else MISA_ERR_UNSUPPORTED).
+ * ws: misa_matmul_q8_workspace_bytes() bytes (16-byte aligned; may be NULL when
+ * that is 0); nothing in it outlives the call.
+ */
+misa_status misa_matmul_q8(int64_t m, int64_t n, int64_t k, const uint8_t* x, int64_t x_stride, const float* x_scale,
+                           const uint8_t* w, int64_t w_stride, const float* w_scale, uint16_t* out, int64_t out_stride,
+                           void* ws, size_t ws_bytes, void* stream);
+size_t misa_matmul_q8_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
+/*
  * Profiling.  The stages of misa_indexer (and of the calls that run parts of
  * it: misa_sparse_head_topk[_q8], misa_indexer_cached, misa_indexer_q8,
  * misa_indexer_noalloc, misa_prefill_chunked) whose kernels a caller can time

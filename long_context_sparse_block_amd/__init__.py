@@ -16,7 +16,8 @@ from ._lib import (  # noqa: F401
     misa_profile_stage, STAGES, misa_indexer_paged, misa_indexer_paged_workspace_bytes,
 )
 from .serving import (  # noqa: F401
-    AttnShape, KvPages, PagePlan, RopeSpec, misa_attention_paged, misa_attention_paged_workspace_bytes,
-    misa_attention_selected, misa_attention_selected_workspace_bytes, misa_plan_pages, misa_rope, misa_write_pages,
-    rope_inv_freq,
+    AttnShape, KvPages, PagePlan, RopeSpec, TreePlan, misa_attention_paged, misa_attention_paged_workspace_bytes,
+    misa_attention_selected, misa_attention_selected_workspace_bytes, misa_attention_tree,
+    misa_attention_tree_workspace_bytes, misa_keep_path, misa_matmul_q8, misa_matmul_q8_workspace_bytes, misa_plan_pages,
+    misa_plan_tree, misa_quantize_blocks, misa_rope, misa_write_pages, rope_inv_freq,
 )

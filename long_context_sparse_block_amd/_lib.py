@@ -37,7 +37,9 @@ EXPORTED = ("misa_status_str", "misa_pool_keys", "misa_route_heads", "misa_spars
             "misa_profile_stage", "misa_indexer_paged", "misa_indexer_paged_workspace_bytes",
             "misa_plan_pages", "misa_rope", "misa_write_pages", "misa_attention_paged",
             "misa_attention_paged_workspace_bytes", "misa_attention_selected",
-            "misa_attention_selected_workspace_bytes")
+            "misa_attention_selected_workspace_bytes", "misa_plan_tree", "misa_attention_tree",
+            "misa_attention_tree_workspace_bytes", "misa_keep_path", "misa_quantize_blocks", "misa_matmul_q8",
+            "misa_matmul_q8_workspace_bytes")
 STAGES = dict(pool=1, route=2, score_sample=3, sample_threshold=4, score_candidates=5, region_select=6,
               rescore=7, rerank=8, final_topk=9, score_logits=10, logits_topk=11)
 MISA_ERR_SCRATCH = -5
@@ -99,6 +101,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "misa_write_pages": [i64, i32, i32, P, i64, i64, P, i64, i64, P, P, P, P, ctypes.c_int, P, P, i64, i32, P],
         "misa_attention_paged": [P, P, P, P, P, P, P, P, sz, P],
         "misa_attention_selected": [P, P, P, P, P, P, i32, P, P, P, sz, P],
+        "misa_plan_tree": [i32, P, P, P, i64, i32, P, P, P],
+        "misa_attention_tree": [P, P, P, P, P, P, i32, P, P, P, sz, P],
+        "misa_keep_path": [i32, P, i32, P, P, P, i64, i32, i32, P, P, ctypes.c_int, P, P, i64, i32, P, P],
+        "misa_quantize_blocks": [P, ctypes.c_int, i64, i64, i64, i32, P, P, P],
+        "misa_matmul_q8": [i64, i64, i64, P, i64, P, P, i64, P, P, i64, P, sz, P],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -122,6 +129,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.misa_indexer_paged_workspace_bytes.restype = sz
     lib.misa_attention_paged_workspace_bytes.argtypes = [P, P]
     lib.misa_attention_paged_workspace_bytes.restype = sz
+    lib.misa_attention_tree_workspace_bytes.argtypes = [P, P]
+    lib.misa_attention_tree_workspace_bytes.restype = sz
+    lib.misa_matmul_q8_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.misa_matmul_q8_workspace_bytes.restype = sz
     lib.misa_attention_selected_workspace_bytes.argtypes = [P, P, i32]
     lib.misa_attention_selected_workspace_bytes.restype = sz
     _lib = lib

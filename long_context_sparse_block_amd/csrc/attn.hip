@@ -217,13 +217,13 @@ size_t attn_workspace_bytes(const misa_attn_shape& s, const misa_kv_pages& pg, i
 
 hipError_t launch_attention(const misa_attn_shape& s, const misa_kv_pages& pg, const uint16_t* q,
                             const int32_t* q_start, const int32_t* kv_lens, const int32_t* idx, int topk,
-                            uint16_t* out, float* lse, void* ws, hipStream_t st) {
+                            const uint32_t* tree, int tree_words, uint16_t* out, float* lse, void* ws, hipStream_t st) {
   const AttnPlan p = make_plan(s, pg, topk);
   const bool pow2 = (pg.page_keys & (pg.page_keys - 1)) == 0;
   const AttnArgs a{q, s.q_stride_token, s.q_stride_head, pg.k, pg.v, pg.k_scale, pg.v_scale, pg.block_table,
                    pg.max_pages, (int)pg.n_pages, pg.page_keys, pow2 ? __builtin_ctz((unsigned)pg.page_keys) : -1, q_start,
                    kv_lens, idx, topk, out, lse, s.scale * 1.4426950408889634f, s.n_seq, s.n_heads, s.n_kv_heads,
-                   s.n_tokens};
+                   s.n_tokens, tree, tree_words};
   const bool fp8 = pg.kdtype == MISA_K_FP8_E4M3;
   char* base = static_cast<char*>(ws);
   const int64_t all = s.n_tokens * (s.n_heads / s.n_kv_heads);   // rows of a kv head

@@ -12,6 +12,10 @@
 // are already laid out as the second operand of O^T = V^T P^T, up to an order
 // of the keys that V's reads follow.
 //
+// Of a tree of drafted tokens a row sees the cached prefix and, of the sequence's
+// new tokens, those whose bits its token's ancestor bits have; a tile of keys
+// then takes its bits from the row's words (tree_bits).
+//
 // LDS tiles hold bf16 rows in 16-byte pieces, piece c of row r at position
 // c ^ swizzle(r): K rows are then read 16 at a time, and V four rows at a time
 // by gfx950's transposing read, without more lanes per bank than the read's
@@ -29,6 +33,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 // The outputs are rescaled only when a row's maximum has grown by more than this
 // (log2) since the last time: weights stay below 2^8, well inside bf16 and fp32.
 constexpr float kGrow = 8.f;
+
+// What a launch attends over
+enum AttnMode { kCausal = 0, kSelected = 1, kTree = 2 };
+inline AttnMode mode_of(const AttnArgs& a) { return a.idx != nullptr ? kSelected : a.tree != nullptr ? kTree : kCausal; }
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -145,6 +153,25 @@ __device__ __forceinline__ int pick(const AttnArgs& a, int64_t t, int j) {
   const int v = a.idx[t * a.topk + min(j, a.topk - 1)];
   return j < a.topk ? v : -1;
 }
+
+// 32 N ancestor bits of a token from bit `first` on (any, also negative): tokens
+// before the first drafted one are the prefix, which every row sees; bits
+// behind the words are 0.
+template <int N>
+__device__ __forceinline__ void tree_bits(const AttnArgs& a, int64_t token, int first, uint32_t (&bits)[N]) {
+  const uint32_t* const row = a.tree + token * a.tree_words;
+  const int w0 = first >> 5;   // (rounded down)
+  uint32_t w[N + 1];
+#pragma unroll
+  for (int i = 0; i <= N; ++i) {
+    const uint32_t x = row[min(max(w0 + i, 0), a.tree_words - 1)];
+    w[i] = w0 + i < 0 ? ~0u : w0 + i < a.tree_words ? x : 0u;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) bits[i] = __builtin_amdgcn_alignbit(w[i + 1], w[i], (uint32_t)first & 31);
+}
+// the first n of 32 bits
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
 
 // -scale is folded into the sign of q, so that a maximum of scores is a maximum
 // of scaled scores

@@ -42,8 +42,9 @@ struct Fp8Stage {
 };
 }  // namespace
 
-template <int D, bool FP8, bool SEL, int NW>
+template <int D, bool FP8, AttnMode MODE, int NW>
 __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const AttnArgs a, const AttnLaunch L) {
+  constexpr bool SEL = MODE == kSelected, TREE = MODE == kTree;
   constexpr int NT = NW * kWave, BM = NW * 32;
   constexpr int RB = D * 2;            // bytes of a bf16 row
   constexpr int P = D / 8;             // its 16-byte pieces
@@ -103,7 +104,8 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
     tok0 = sp.t0;
     nrows = sp.m * G;
     pos0 = sp.pos0;
-    const int last = (min(r0 + BM, nrows) - 1) / G, first = r0 / G;
+    // (a tree's rows see up to the last new token, and all of them the prefix alone)
+    const int last = TREE ? sp.m - 1 : (min(r0 + BM, nrows) - 1) / G, first = TREE ? -1 : r0 / G;
     kend = (int)max((int64_t)0, min((int64_t)sp.len, pos0 + last + 1));
     kfull = (int)max((int64_t)0, min((int64_t)sp.len, pos0 + first + 1));
     range(scan);
@@ -253,6 +255,18 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             if (!((mw[kb] >> (8 * (e >> 2) + (e & 3))) & 1)) s[kb][e] = -INFINITY;
+      }
+    } else if (TREE) {
+      if ((jt + 1) * kBN > kfull) {
+        uint32_t mw[2];
+        tree_bits<2>(a, qrow, (int)(jt * kBN - pos0), mw);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          mw[kb] = (mw[kb] & low_bits(kend - jt * kBN - kb * 32)) >> (4 * h);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (!((mw[kb] >> (8 * (e >> 2) + (e & 3))) & 1)) s[kb][e] = -INFINITY;
+        }
       }
     } else if ((jt + 1) * kBN > kfull) {
       const int lim = vis - jt * kBN - 4 * h;   // the row sees the tile's keys below this
@@ -427,22 +441,26 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
   }
 }
 
-template <int D, bool FP8, bool SEL>
+template <int D, bool FP8, AttnMode MODE>
 static hipError_t launch_nw(const AttnArgs& a, const AttnLaunch& L, int NW, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)L.n_units * L.n_splits * a.n_kv_heads));
-  if (NW == 2) hipLaunchKernelGGL((k_attn_tile<D, FP8, SEL, 2>), grid, dim3(128), 0, st, a, L);
-  else hipLaunchKernelGGL((k_attn_tile<D, FP8, SEL, 4>), grid, dim3(256), 0, st, a, L);
+  if (NW == 2) hipLaunchKernelGGL((k_attn_tile<D, FP8, MODE, 2>), grid, dim3(128), 0, st, a, L);
+  else hipLaunchKernelGGL((k_attn_tile<D, FP8, MODE, 4>), grid, dim3(256), 0, st, a, L);
   return hipGetLastError();
 }
 
-hipError_t launch_attn_tile(const AttnArgs& a, const AttnLaunch& L, int D, bool fp8, int NW, hipStream_t st) {
-  const bool sel = a.idx != nullptr;
-  if (D == 128) {
-    if (fp8) return sel ? launch_nw<128, true, true>(a, L, NW, st) : launch_nw<128, true, false>(a, L, NW, st);
-    return sel ? launch_nw<128, false, true>(a, L, NW, st) : launch_nw<128, false, false>(a, L, NW, st);
+template <int D, bool FP8>
+static hipError_t launch_mode(const AttnArgs& a, const AttnLaunch& L, int NW, hipStream_t st) {
+  switch (mode_of(a)) {
+    case kSelected: return launch_nw<D, FP8, kSelected>(a, L, NW, st);
+    case kTree: return launch_nw<D, FP8, kTree>(a, L, NW, st);
+    default: return launch_nw<D, FP8, kCausal>(a, L, NW, st);
   }
-  if (fp8) return sel ? launch_nw<64, true, true>(a, L, NW, st) : launch_nw<64, true, false>(a, L, NW, st);
-  return sel ? launch_nw<64, false, true>(a, L, NW, st) : launch_nw<64, false, false>(a, L, NW, st);
+}
+
+hipError_t launch_attn_tile(const AttnArgs& a, const AttnLaunch& L, int D, bool fp8, int NW, hipStream_t st) {
+  if (D == 128) return fp8 ? launch_mode<128, true>(a, L, NW, st) : launch_mode<128, false>(a, L, NW, st);
+  return fp8 ? launch_mode<64, true>(a, L, NW, st) : launch_mode<64, false>(a, L, NW, st);
 }
 
 }  // namespace misa

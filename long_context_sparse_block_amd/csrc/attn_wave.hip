@@ -38,8 +38,9 @@ constexpr int kWT = 32;      // keys of a wave's tile
 constexpr int kWaves = 4;
 }  // namespace
 
-template <int D, bool FP8, bool SEL, int RT>
-__global__ void __launch_bounds__(kWaves * kWave, wave_groups(D, FP8, SEL, RT)) k_attn_wave(const AttnArgs a, const AttnLaunch L) {
+template <int D, bool FP8, AttnMode MODE, int RT>
+__global__ void __launch_bounds__(kWaves * kWave, wave_groups(D, FP8, MODE == kSelected, RT)) k_attn_wave(const AttnArgs a, const AttnLaunch L) {
+  constexpr bool SEL = MODE == kSelected, TREE = MODE == kTree;
   constexpr int RB = D * 2, P = D / 8, RPI = kWave / P;    // bf16: bytes and 16-byte pieces of a row, rows of a load
   constexpr int PC = D / 16, RPC = kWave / PC;              // e4m3: pieces of a row, rows of a load
   constexpr int KS = D / 32, DB = D / 16;
@@ -102,13 +103,14 @@ __global__ void __launch_bounds__(kWaves * kWave, wave_groups(D, FP8, SEL, RT)) 
     nrows = sp.m * G;
     pos0 = sp.pos0;
     kend = (int)max((int64_t)0, min((int64_t)sp.len, pos0 + sp.m));
-    kfull = (int)max((int64_t)0, min((int64_t)sp.len, pos0 + 1));
+    kfull = (int)max((int64_t)0, min((int64_t)sp.len, pos0 + (TREE ? 0 : 1)));   // (a tree's rows all see the prefix)
     range(scan);
     if (L.n_splits > 1 && split == 0 && g == 0 && tid == 0) L.unit_info[unit] = make_int4(tok0, 0, nrows, in_use);
     if (split >= in_use) return;
   }
 
   int vis[RT];
+  int64_t qtok[RT];   // TREE: the row's token
   bf16x8 qf[RT][KS];
   const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
   const float sc = fmaxf(fabsf(a.scale_log2), 1e-30f);
@@ -116,6 +118,7 @@ __global__ void __launch_bounds__(kWaves * kWave, wave_groups(D, FP8, SEL, RT)) 
   for (int rt = 0; rt < RT; ++rt) {
     const int rc = min(rt * 16 + c16, nrows - 1);
     const int qi = SEL ? 0 : rc / G, qh = g * G + (SEL ? rc : rc - qi * G);
+    qtok[rt] = (int64_t)tok0 + qi;
     vis[rt] = SEL ? 0 : (int)max((int64_t)-1, min((int64_t)kend, pos0 + qi + 1));
     // e4m3: step ks of a product takes values 64 (ks / 2) + 16 g4 + 8 (ks % 2) .. +7 of the row, as K's codes come
     const uint16_t* src = a.q + ((int64_t)tok0 + qi) * a.q_st + qh * a.q_sh + g4 * (FP8 ? 16 : 8);
@@ -239,10 +242,15 @@ __global__ void __launch_bounds__(kWaves * kWave, wave_groups(D, FP8, SEL, RT)) 
       }
       if (!whole) {
         const int lim = vis[rt] - jt * kWT;
+        uint32_t bits[1] = {mask};
+        if (TREE) {
+          tree_bits<1>(a, qtok[rt], (int)(jt * kWT - pos0), bits);
+          bits[0] &= low_bits(kend - jt * kWT);
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int key = (e >> 2) * 16 + 4 * g4 + (e & 3);
-          p[e] = (SEL ? (mask >> key) & 1 : key < lim) ? p[e] : -INFINITY;
+          p[e] = (SEL || TREE ? (bits[0] >> key) & 1 : key < lim) ? p[e] : -INFINITY;
         }
       }
       float top = p[0];
@@ -442,22 +450,26 @@ __global__ void __launch_bounds__(kWaves * kWave, wave_groups(D, FP8, SEL, RT)) 
   }
 }
 
-template <int D, bool FP8, bool SEL>
+template <int D, bool FP8, AttnMode MODE>
 static hipError_t launch_rt(const AttnArgs& a, const AttnLaunch& L, int RT, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)L.n_units * L.n_splits * a.n_kv_heads));
-  if (RT == 1) hipLaunchKernelGGL((k_attn_wave<D, FP8, SEL, 1>), grid, dim3(256), 0, st, a, L);
-  else hipLaunchKernelGGL((k_attn_wave<D, FP8, SEL, 2>), grid, dim3(256), 0, st, a, L);
+  if (RT == 1) hipLaunchKernelGGL((k_attn_wave<D, FP8, MODE, 1>), grid, dim3(256), 0, st, a, L);
+  else hipLaunchKernelGGL((k_attn_wave<D, FP8, MODE, 2>), grid, dim3(256), 0, st, a, L);
   return hipGetLastError();
 }
 
-hipError_t launch_attn_wave(const AttnArgs& a, const AttnLaunch& L, int D, bool fp8, int RT, hipStream_t st) {
-  const bool sel = a.idx != nullptr;
-  if (D == 128) {
-    if (fp8) return sel ? launch_rt<128, true, true>(a, L, RT, st) : launch_rt<128, true, false>(a, L, RT, st);
-    return sel ? launch_rt<128, false, true>(a, L, RT, st) : launch_rt<128, false, false>(a, L, RT, st);
+template <int D, bool FP8>
+static hipError_t launch_mode(const AttnArgs& a, const AttnLaunch& L, int RT, hipStream_t st) {
+  switch (mode_of(a)) {
+    case kSelected: return launch_rt<D, FP8, kSelected>(a, L, RT, st);
+    case kTree: return launch_rt<D, FP8, kTree>(a, L, RT, st);
+    default: return launch_rt<D, FP8, kCausal>(a, L, RT, st);
   }
-  if (fp8) return sel ? launch_rt<64, true, true>(a, L, RT, st) : launch_rt<64, true, false>(a, L, RT, st);
-  return sel ? launch_rt<64, false, true>(a, L, RT, st) : launch_rt<64, false, false>(a, L, RT, st);
+}
+
+hipError_t launch_attn_wave(const AttnArgs& a, const AttnLaunch& L, int D, bool fp8, int RT, hipStream_t st) {
+  if (D == 128) return fp8 ? launch_mode<128, true>(a, L, RT, st) : launch_mode<128, false>(a, L, RT, st);
+  return fp8 ? launch_mode<64, true>(a, L, RT, st) : launch_mode<64, false>(a, L, RT, st);
 }
 
 }  // namespace misa

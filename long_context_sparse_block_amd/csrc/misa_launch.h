@@ -195,12 +195,49 @@ struct AttnArgs {
   float scale_log2;
   int n_seq, n_heads, n_kv_heads;
   int64_t n_tokens;
+  const uint32_t* tree;   // nullable: the drafted tokens' ancestor bits [n_tokens][tree_words]
+  int tree_words;
 };
-// topk = 0: over every visible key.  attn_fits: the launch's grid is in range.
+// topk = 0: over every visible key, or, with ancestor bits (tree != nullptr), those
+// of a drafted token.  attn_fits: the launch's grid is in range.
 bool attn_fits(const misa_attn_shape& s, const misa_kv_pages& pg, int topk);
 size_t attn_workspace_bytes(const misa_attn_shape& s, const misa_kv_pages& pg, int topk);
 hipError_t launch_attention(const misa_attn_shape& s, const misa_kv_pages& pg, const uint16_t* q,
                             const int32_t* q_start, const int32_t* kv_lens, const int32_t* idx, int topk,
-                            uint16_t* out, float* lse, void* ws, hipStream_t st);
+                            const uint32_t* tree, int tree_words, uint16_t* out, float* lse, void* ws, hipStream_t st);
+
+// ---------------------------------------------------------------------------
+// Drafted trees: their plan, and the move of the kept path's rows (misa.h).
+// ---------------------------------------------------------------------------
+hipError_t launch_plan_tree(int n_seq, const int32_t* parents, const int32_t* q_start, const int32_t* kv_lens,
+                            int64_t n_tokens, int words, uint32_t* mask, int32_t* positions, hipStream_t st);
+struct KeepArgs {
+  const int32_t *path, *q_start, *kv_lens, *table;
+  int max_path;
+  int64_t max_pages, n_pages;
+  int page_keys;
+  char *k, *v;                 // v nullable
+  int row_bytes;               // of all heads of a token
+  float *k_scale, *v_scale;    // nullable (bf16 pages)
+  int n_heads;
+  int32_t* kept_lens;
+};
+hipError_t launch_keep_path(int n_seq, const KeepArgs& a, hipStream_t st);
+
+// ---------------------------------------------------------------------------
+// e4m3 products with a scale for each block of 128 (misa.h).
+// ---------------------------------------------------------------------------
+hipError_t launch_quantize_blocks(const void* x, int dtype, int64_t rows, int64_t cols, int64_t x_st, int block_rows,
+                                  uint8_t* codes, float* scale, hipStream_t st);
+struct MatmulArgs {
+  const uint8_t *x, *w;
+  const float *xs, *ws;
+  uint16_t* out;
+  int64_t x_st, w_st, o_st;
+  int64_t m, n, k;
+};
+bool matmul_q8_fits(int64_t m, int64_t n, int64_t k);
+size_t matmul_q8_workspace_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_matmul_q8(const MatmulArgs& a, void* work, hipStream_t st);
 
 }  // namespace misa

@@ -1,6 +1,6 @@
 // extern "C" entry points of the paged serving step (page planning, rotary
-// positions, page writes, attention): argument checks on the host, then
-// asynchronous launches on the caller's stream.
+// positions, page writes, attention, drafted trees) and of e4m3 products:
+// argument checks on the host, then asynchronous launches on the caller's stream.
 #include <stdint.h>
 
 #include "misa.h"
@@ -81,14 +81,27 @@ misa_status check_attn_pointers(const misa_kv_pages* p, const void* q, const voi
 }
 
 misa_status attention(const misa_attn_shape* s, const misa_kv_pages* p, const uint16_t* q, const int32_t* q_start,
-                      const int32_t* kv_lens, const int32_t* idx, int32_t topk, uint16_t* out, float* lse, void* ws,
-                      size_t ws_bytes, void* stream) {
+                      const int32_t* kv_lens, const int32_t* idx, int32_t topk, const uint32_t* mask, int32_t words,
+                      uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
   MISA_TRY(check_attn_pointers(p, q, q_start, kv_lens, out));
   if (!misa::attn_fits(*s, *p, topk)) return MISA_ERR_UNSUPPORTED;
   const size_t need = misa::attn_workspace_bytes(*s, *p, topk);
   if (need > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < need)) return MISA_ERR_WORKSPACE;
   if (s->n_tokens == 0) return MISA_OK;
-  return from_hip(misa::launch_attention(*s, *p, q, q_start, kv_lens, idx, topk, out, lse, ws, (hipStream_t)stream));
+  return from_hip(misa::launch_attention(*s, *p, q, q_start, kv_lens, idx, topk, mask, words, out, lse, ws,
+                                         (hipStream_t)stream));
+}
+
+constexpr int32_t kMaxTreeWords = 1024;
+constexpr int64_t kMaxCols = (int64_t)1 << 20;
+constexpr int64_t kMaxBlocks = (int64_t)1 << 27;    // quantised in one call
+constexpr int64_t kMaxStride = (int64_t)1 << 40;
+
+misa_status check_matmul(int64_t m, int64_t n, int64_t k) {
+  if (m < 0 || n < 1 || k < 1) return MISA_ERR_INVALID_ARG;
+  if (k % 16 != 0 || k > kMaxCols || n > kMaxTokens || m > kMaxTokens) return MISA_ERR_UNSUPPORTED;
+  if (!misa::matmul_q8_fits(m, n, k)) return MISA_ERR_UNSUPPORTED;
+  return MISA_OK;
 }
 
 }  // namespace
@@ -177,7 +190,7 @@ misa_status misa_attention_paged(const misa_attn_shape* shape, const misa_kv_pag
                                  const int32_t* q_start, const int32_t* kv_lens, uint16_t* out, float* lse, void* ws,
                                  size_t ws_bytes, void* stream) {
   MISA_TRY(check_attn(shape, pages));
-  return attention(shape, pages, q, q_start, kv_lens, nullptr, 0, out, lse, ws, ws_bytes, stream);
+  return attention(shape, pages, q, q_start, kv_lens, nullptr, 0, nullptr, 0, out, lse, ws, ws_bytes, stream);
 }
 
 size_t misa_attention_selected_workspace_bytes(const misa_attn_shape* shape, const misa_kv_pages* pages,
@@ -191,7 +204,114 @@ misa_status misa_attention_selected(const misa_attn_shape* shape, const misa_kv_
                                     uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
   MISA_TRY(check_attn(shape, pages));
   if (idx == nullptr || topk < 1 || topk > MISA_MAX_TOPK) return MISA_ERR_INVALID_ARG;
-  return attention(shape, pages, q, q_start, kv_lens, idx, topk, out, lse, ws, ws_bytes, stream);
+  return attention(shape, pages, q, q_start, kv_lens, idx, topk, nullptr, 0, out, lse, ws, ws_bytes, stream);
+}
+
+misa_status misa_plan_tree(int32_t n_seq, const int32_t* parents, const int32_t* q_start, const int32_t* kv_lens,
+                           int64_t n_tokens, int32_t words, uint32_t* mask, int32_t* positions, void* stream) {
+  if (n_seq < 1 || n_tokens < 0 || words < 1) return MISA_ERR_INVALID_ARG;
+  if (q_start == nullptr || kv_lens == nullptr) return MISA_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (parents == nullptr || mask == nullptr || positions == nullptr)) return MISA_ERR_INVALID_ARG;
+  if (n_seq > 65535 || n_tokens > kMaxTokens || words > kMaxTreeWords) return MISA_ERR_UNSUPPORTED;
+  const Span in[] = {{parents, 4 * n_tokens}, {q_start, 4 * ((int64_t)n_seq + 1)}, {kv_lens, 4 * (int64_t)n_seq}};
+  const Span out[] = {{mask, 4 * n_tokens * words}, {positions, 4 * n_tokens}};
+  for (const Span& o : out)
+    for (const Span& i : in)
+      if (overlap(o, i)) return MISA_ERR_INVALID_ARG;
+  if (overlap(out[0], out[1])) return MISA_ERR_INVALID_ARG;
+  if (n_tokens == 0) return MISA_OK;
+  return from_hip(misa::launch_plan_tree(n_seq, parents, q_start, kv_lens, n_tokens, words, mask, positions,
+                                         (hipStream_t)stream));
+}
+
+size_t misa_attention_tree_workspace_bytes(const misa_attn_shape* shape, const misa_kv_pages* pages) {
+  return misa_attention_paged_workspace_bytes(shape, pages);
+}
+
+misa_status misa_attention_tree(const misa_attn_shape* shape, const misa_kv_pages* pages, const uint16_t* q,
+                                const int32_t* q_start, const int32_t* kv_lens, const uint32_t* mask, int32_t words,
+                                uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  MISA_TRY(check_attn(shape, pages));
+  if (mask == nullptr || words < 1) return MISA_ERR_INVALID_ARG;
+  if (words > kMaxTreeWords) return MISA_ERR_UNSUPPORTED;
+  return attention(shape, pages, q, q_start, kv_lens, nullptr, 0, mask, words, out, lse, ws, ws_bytes, stream);
+}
+
+misa_status misa_keep_path(int32_t n_seq, const int32_t* path, int32_t max_path, const int32_t* q_start,
+                           const int32_t* kv_lens, const int32_t* block_table, int64_t max_pages, int32_t n_heads,
+                           int32_t head_dim, void* k_pages, void* v_pages, misa_kdtype kdtype, float* k_scale_pages,
+                           float* v_scale_pages, int64_t n_pages, int32_t page_keys, int32_t* kept_lens, void* stream) {
+  if (n_seq < 1 || max_path < 1 || max_pages < 1 || n_heads < 1 || head_dim < 1) return MISA_ERR_INVALID_ARG;
+  if (kdtype != MISA_K_BF16 && kdtype != MISA_K_FP8_E4M3) return MISA_ERR_INVALID_ARG;
+  if (path == nullptr || q_start == nullptr || kv_lens == nullptr || block_table == nullptr || kept_lens == nullptr)
+    return MISA_ERR_INVALID_ARG;
+  if (k_pages == nullptr || !aligned16(k_pages) || !aligned16(v_pages)) return MISA_ERR_INVALID_ARG;
+  const bool fp8 = kdtype == MISA_K_FP8_E4M3;
+  if (fp8 && (k_scale_pages == nullptr || (v_pages != nullptr && v_scale_pages == nullptr))) return MISA_ERR_INVALID_ARG;
+  MISA_TRY(check_pool(n_pages, page_keys));
+  if (n_seq > 65535 || max_path > (1 << 20) || max_pages >= kMaxSlots) return MISA_ERR_UNSUPPORTED;
+  if (head_dim % 8 != 0 || head_dim > 512 || (int64_t)n_heads * head_dim > (1 << 20)) return MISA_ERR_UNSUPPORTED;
+  const int64_t row = (int64_t)n_heads * head_dim * (fp8 ? 1 : 2), slots = n_pages * page_keys;
+  const Span lens{kept_lens, 4 * (int64_t)n_seq};
+  const Span others[] = {{path, 4 * (int64_t)n_seq * max_path}, {q_start, 4 * ((int64_t)n_seq + 1)},
+                         {kv_lens, 4 * (int64_t)n_seq}, {block_table, 4 * n_seq * max_pages}, {k_pages, slots * row},
+                         {v_pages, v_pages != nullptr ? slots * row : 0}, {k_scale_pages, fp8 ? 4 * slots * n_heads : 0},
+                         {v_scale_pages, fp8 && v_pages != nullptr ? 4 * slots * n_heads : 0}};
+  for (const Span& o : others)   // workgroups read the lengths while others write theirs
+    if (overlap(lens, o)) return MISA_ERR_INVALID_ARG;
+  for (int i = 4; i < 8; ++i)    // the pools are apart, from each other and from what says where rows go
+    for (int j = 0; j < i; ++j)
+      if (overlap(others[i], others[j])) return MISA_ERR_INVALID_ARG;
+  const misa::KeepArgs a{path, q_start, kv_lens, block_table, max_path, max_pages, n_pages, page_keys,
+                         static_cast<char*>(k_pages), static_cast<char*>(v_pages), (int)row,
+                         fp8 ? k_scale_pages : nullptr, fp8 ? v_scale_pages : nullptr, n_heads, kept_lens};
+  return from_hip(misa::launch_keep_path(n_seq, a, (hipStream_t)stream));
+}
+
+misa_status misa_quantize_blocks(const void* x, misa_dtype dtype, int64_t rows, int64_t cols, int64_t x_stride,
+                                 int32_t block_rows, uint8_t* codes, float* scale, void* stream) {
+  if (rows < 0 || cols < 1 || x_stride < 0) return MISA_ERR_INVALID_ARG;
+  if (dtype != MISA_T_BF16 && dtype != MISA_T_FP16 && dtype != MISA_T_FP32) return MISA_ERR_INVALID_ARG;
+  if (block_rows != 1 && block_rows != 128) return MISA_ERR_INVALID_ARG;
+  if (x == nullptr || !aligned16(x) || codes == nullptr || !aligned16(codes) || scale == nullptr)
+    return MISA_ERR_INVALID_ARG;
+  if (x_stride % (dtype == MISA_T_FP32 ? 4 : 8) != 0) return MISA_ERR_INVALID_ARG;
+  if (cols % 16 != 0 || cols > kMaxCols || rows > kMaxTokens || rows * ((cols + 127) / 128) > kMaxBlocks)
+    return MISA_ERR_UNSUPPORTED;
+  if (rows == 0) return MISA_OK;
+  const int64_t size = dtype == MISA_T_FP32 ? 4 : 2;
+  const Span in{x, ((rows - 1) * x_stride + cols) * size};
+  const Span out[] = {{codes, rows * cols}, {scale, 4 * ((rows + block_rows - 1) / block_rows) * ((cols + 127) / 128)}};
+  if (overlap(in, out[0]) || overlap(in, out[1]) || overlap(out[0], out[1])) return MISA_ERR_INVALID_ARG;
+  return from_hip(misa::launch_quantize_blocks(x, dtype, rows, cols, x_stride, block_rows, codes, scale, (hipStream_t)stream));
+}
+
+size_t misa_matmul_q8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  if (check_matmul(m, n, k) != MISA_OK) return 0;
+  return misa::matmul_q8_workspace_bytes(m, n, k);
+}
+
+misa_status misa_matmul_q8(int64_t m, int64_t n, int64_t k, const uint8_t* x, int64_t x_stride, const float* x_scale,
+                           const uint8_t* w, int64_t w_stride, const float* w_scale, uint16_t* out, int64_t out_stride,
+                           void* ws, size_t ws_bytes, void* stream) {
+  MISA_TRY(check_matmul(m, n, k));
+  if (x == nullptr || !aligned16(x) || w == nullptr || !aligned16(w) || x_scale == nullptr || w_scale == nullptr ||
+      out == nullptr)
+    return MISA_ERR_INVALID_ARG;
+  if (x_stride < 0 || w_stride < 0 || x_stride % 16 != 0 || w_stride % 16 != 0) return MISA_ERR_INVALID_ARG;
+  if (m > 1 && out_stride < n) return MISA_ERR_INVALID_ARG;
+  if (x_stride > kMaxStride || w_stride > kMaxStride || out_stride > kMaxStride) return MISA_ERR_UNSUPPORTED;
+  const size_t need = misa::matmul_q8_workspace_bytes(m, n, k);
+  if (need > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < need)) return MISA_ERR_WORKSPACE;
+  if (m == 0) return MISA_OK;
+  const Span y{out, 2 * ((m - 1) * out_stride + n)};
+  const int64_t across = (k + 127) / 128;
+  const Span in[] = {{x, (m - 1) * x_stride + k}, {w, (n - 1) * w_stride + k}, {x_scale, 4 * m * across},
+                     {w_scale, 4 * ((n + 127) / 128) * across}};
+  for (const Span& i : in)
+    if (overlap(y, i)) return MISA_ERR_INVALID_ARG;
+  return from_hip(misa::launch_matmul_q8(misa::MatmulArgs{x, w, x_scale, w_scale, out, x_stride, w_stride, out_stride, m, n, k},
+                                         ws, (hipStream_t)stream));
 }
 
 }  // extern "C"

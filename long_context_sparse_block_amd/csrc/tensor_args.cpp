@@ -1,6 +1,6 @@
 // Tensor arguments of the Python wrappers (module _tensor_args): the pointer of a
-// dense tensor, the pointer and strides of a [tokens, heads, head_dim] one, a page
-// pool's, a workspace.  Looked up attribute by attribute from Python, each costs
+// dense tensor, the pointer and strides of a [tokens, heads, head_dim] or [rows,
+// columns] one, a page pool's, a workspace.  Looked up attribute by attribute from Python, each costs
 // three to four times as much, and a call of a few microseconds checks half a
 // dozen.
 #define PY_SSIZE_T_CLEAN
@@ -107,6 +107,38 @@ PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return Py_BuildValue("(NLL)", PyLong_FromVoidPtr(at), st, sh);
 }
 
+// matrix(tensor, dtypes, name, dev, shape or None) -> pointer, row stride
+PyObject* matrix(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if ((n != 4 && n != 5) || !PyUnicode_Check(a[2])) {
+    PyErr_SetString(PyExc_TypeError, "matrix(tensor, dtypes, name, dev, shape=None)");
+    return nullptr;
+  }
+  const at::Tensor* t = gpu_tensor(a[0], a[2], a[3]);
+  if (t == nullptr) return nullptr;
+  const int known = PySequence_Contains(a[1], dtype_of(*t));
+  if (known < 0) return nullptr;
+  if (known == 0) {
+    PyObject* want = PySequence_Tuple(a[1]);
+    if (want == nullptr) return nullptr;
+    PyErr_Format(PyExc_ValueError, "%U: dtype %S, expected one of %R", a[2], dtype_of(*t), want);
+    Py_DECREF(want);
+    return nullptr;
+  }
+  const bool fixed = n == 5 && a[4] != Py_None;
+  if (t->dim() != 2 || (fixed && !same_shape(*t, a[4]))) {
+    if (PyErr_Occurred()) return nullptr;
+    PyObject* want = fixed ? (Py_INCREF(a[4]), a[4]) : PyUnicode_FromString("[rows, columns]");
+    if (want != nullptr) refuse_shape(a[2], *t, want);
+    Py_XDECREF(want);
+    return nullptr;
+  }
+  if (t->stride(1) != 1 && t->size(1) > 1) return refuse(a[2], ": the last dimension must be dense");
+  // the stride of a dimension of one element means nothing
+  const long long st = t->size(0) > 1 ? t->stride(0) : 0;
+  void* const at = t->data_ptr();
+  return Py_BuildValue("(NL)", PyLong_FromVoidPtr(at), st);
+}
+
 // pool(pages, heads, head_dim, name, dev) -> pointer, code type (misa_kdtype), pages, rows a page
 PyObject* pool(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 5 || !PyUnicode_Check(a[3])) {
@@ -170,6 +202,8 @@ PyMethodDef methods[] = {
      "pool(pages, heads, head_dim, name, dev): pointer, code type, n_pages, page_keys of a page pool"},
     {"scratch", entry<scratch>(), METH_FASTCALL,
      "scratch(bytes, like): a workspace on like's device, and its pointer"},
+    {"matrix", entry<matrix>(), METH_FASTCALL,
+     "matrix(tensor, dtypes, name, dev, shape=None): pointer and row stride of a [rows, columns] tensor"},
     {"dense", entry<dense>(), METH_FASTCALL,
      "dense(tensor, dtype, shape, name, dev): pointer of a dense tensor of this type and shape on GPU dev"},
     {"rows", entry<rows>(), METH_FASTCALL,

@@ -1,0 +1,169 @@
+// Trees of drafted tokens: which of a sequence's new tokens descends from which
+// (misa_plan_tree), and the move of an accepted path's rows to where the cached
+// prefix goes on (misa_keep_path).  What attention makes of the tree is in
+// attn_tile.hip and attn_wave.hip.
+//
+// Both move a few KB: what bounds them is the launch and a chain of dependent
+// loads (lengths, then parents or path and table, then the rows).
+#include "misa_common.h"
+#include "misa_launch.h"
+
+namespace misa {
+
+namespace {
+constexpr int kPlanThreads = 256;
+constexpr int kLdsNodes = 2048;   // a tree's parents that a workgroup keeps in LDS
+constexpr int kPad = 4096;        // words of padded rows that a workgroup clears
+}  // namespace
+
+// A workgroup takes a sequence, a thread a word of a token's bits: it walks from
+// the token to the root and collects the ancestors that lie in its word.  Parents
+// come before their children, so a thread is done once it is below its word; that
+// of word 0 walks to the root and counts the depth.
+__global__ void __launch_bounds__(kPlanThreads) k_plan_tree(int n_seq, const int32_t* parents, const int32_t* q_start,
+                                                            const int32_t* kv_lens, int64_t n_tokens, int words,
+                                                            uint32_t* mask, int32_t* positions) {
+  __shared__ int s_up[kLdsNodes];
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x >= n_seq) {   // rows of no sequence
+    const int64_t lo = min(max((int64_t)q_start[0], (int64_t)0), n_tokens);
+    const int64_t hi = min(max((int64_t)q_start[n_seq], lo), n_tokens);
+    const int64_t i0 = (int64_t)(blockIdx.x - n_seq) * kPad, all = n_tokens * words;
+    for (int64_t i = i0 + tid; i < min(i0 + kPad, all); i += kPlanThreads) {
+      const int64_t t = i / words;
+      if (t >= lo && t < hi) continue;
+      mask[i] = 0;
+      if (i - t * words == 0) positions[t] = -1;
+    }
+    return;
+  }
+  const int64_t s = q_start[blockIdx.x], e = q_start[blockIdx.x + 1];
+  const int64_t t0 = min(max(s, (int64_t)0), n_tokens);
+  const int m = (int)max((int64_t)0, min(e, n_tokens) - t0);
+  const int64_t pos0 = (int64_t)max(kv_lens[blockIdx.x], 0) - (e - s);
+  const int32_t* const up = parents + t0;
+  // an entry that does not name a token before its own makes that a root
+  auto parent = [&](int i) __attribute__((always_inline)) {
+    const int p = up[i];
+    return p < i ? max(p, -1) : -1;
+  };
+  const int in_lds = min(m, kLdsNodes);
+  for (int i = tid; i < in_lds; i += kPlanThreads) s_up[i] = parent(i);
+  __syncthreads();
+  const int64_t all = (int64_t)m * words;
+  for (int64_t at = tid; at < all; at += kPlanThreads) {
+    const int i = (int)(at / words), w = (int)(at - (int64_t)i * words);
+    uint32_t bits = 0;
+    int depth = 0;
+    for (int j = i; j >= 32 * w; ++depth) {   // (j falls with every step)
+      if ((j >> 5) == w) bits |= 1u << (j & 31);
+      j = j < kLdsNodes ? s_up[j] : parent(j);
+    }
+    mask[t0 * words + at] = bits;
+    if (w == 0) positions[t0 + i] = (int32_t)(pos0 + depth - 1);
+  }
+}
+
+hipError_t launch_plan_tree(int n_seq, const int32_t* parents, const int32_t* q_start, const int32_t* kv_lens,
+                            int64_t n_tokens, int words, uint32_t* mask, int32_t* positions, hipStream_t st) {
+  const int64_t pad = (n_tokens * words + kPad - 1) / kPad;
+  hipLaunchKernelGGL(k_plan_tree, dim3((unsigned)(n_seq + pad)), dim3(kPlanThreads), 0, st, n_seq, parents, q_start,
+                     kv_lens, n_tokens, words, mask, positions);
+  return hipGetLastError();
+}
+
+// A workgroup takes a sequence (and, of wide rows, some of their pieces), a thread
+// a piece of every row: 16 (or 8) bytes of the keys or values, or one scale.  Row i
+// of the kept ones comes from place path[i] >= i, and path rises, so a thread that
+// goes through the rows in order, reading a few and then writing them, reads
+// every row before anything is written there: no other thread touches its pieces.
+template <typename Piece>
+__global__ void __launch_bounds__(256) k_keep_path(const KeepArgs a) {
+  constexpr int U = 8;   // rows under way
+  const int lane = threadIdx.x & 63, b = blockIdx.x;
+  const int64_t s = a.q_start[b], e = a.q_start[b + 1];
+  const int m = (int)min(max(e - s, (int64_t)0), (int64_t)0x7fffffff);
+  const int64_t first = (int64_t)max(a.kv_lens[b], 0) - m;
+  const int pieces = a.row_bytes / (int)sizeof(Piece);
+  const int kv = a.v != nullptr ? 2 : 1;
+  // this thread's piece of the K rows, the V rows, their scales
+  const int item = blockIdx.y * blockDim.x + threadIdx.x;
+  const bool is_row = item < kv * pieces;
+  const int sc = item - kv * pieces;
+  const bool is_scale = !is_row && a.k_scale != nullptr && sc < kv * a.n_heads;
+  char* const base = item < pieces ? a.k : a.v;
+  const int64_t col = (int64_t)(item < pieces ? item : item - pieces) * (int)sizeof(Piece);
+  float* const sbase = sc < a.n_heads ? a.k_scale : a.v_scale;
+  const int scol = sc < a.n_heads ? sc : sc - a.n_heads;
+  auto slot = [&](int64_t t) __attribute__((always_inline)) -> int64_t {
+    const int64_t p = t / a.page_keys;
+    if (t < 0 || p >= a.max_pages) return -1;
+    const int64_t entry = a.table[b * a.max_pages + p];
+    return entry < 0 || entry >= a.n_pages ? -1 : entry * a.page_keys + (t - p * a.page_keys);
+  };
+  int kept = 0;
+  for (int i0 = 0; i0 < a.max_path; i0 += 64) {
+    const int i = i0 + lane;
+    const int32_t* const path = a.path + (int64_t)b * a.max_path;
+    const int node = path[min(i, a.max_path - 1)];
+    const int before = i > 0 ? path[min(i, a.max_path - 1) - 1] : -1;
+    const bool ok = i < a.max_path && node > before && node >= 0 && node < m;
+    const uint64_t gone = ~__ballot(ok);
+    const int n = gone == 0 ? 64 : (int)__builtin_ctzll(gone);   // kept ones of these 64
+    kept += n;
+    // a row that stays, or has no place in the pages, moves nothing
+    int64_t src = -1, dst = -1;
+    if (lane < n && node != i) {
+      src = slot(first + node);
+      dst = slot(first + i);
+    }
+    uint64_t moves = __ballot(src >= 0 && dst >= 0);
+    while (moves != 0) {
+      int64_t from[U], to[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int l = moves != 0 ? (int)__builtin_ctzll(moves) : -1;
+        moves &= moves - 1;
+        const int at = max(l, 0);
+        const int64_t f = ((int64_t)__builtin_amdgcn_readlane((int)(src >> 32), at) << 32) | (uint32_t)__builtin_amdgcn_readlane((int)src, at);
+        const int64_t d = ((int64_t)__builtin_amdgcn_readlane((int)(dst >> 32), at) << 32) | (uint32_t)__builtin_amdgcn_readlane((int)dst, at);
+        from[u] = l < 0 ? -1 : f;
+        to[u] = d;
+      }
+      if (is_row) {
+        Piece x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (from[u] >= 0) x[u] = *reinterpret_cast<const Piece*>(base + from[u] * a.row_bytes + col);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (from[u] >= 0) *reinterpret_cast<Piece*>(base + to[u] * a.row_bytes + col) = x[u];
+      } else if (is_scale) {
+        float x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (from[u] >= 0) x[u] = sbase[from[u] * a.n_heads + scol];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (from[u] >= 0) sbase[to[u] * a.n_heads + scol] = x[u];
+      }
+    }
+    if (n < 64) break;
+  }
+  if (blockIdx.y == 0 && threadIdx.x == 0) a.kept_lens[b] = (int32_t)max((int64_t)0, first + kept);
+}
+
+template <typename Piece>
+static hipError_t launch_keep(int n_seq, const KeepArgs& a, hipStream_t st) {
+  const int items = (a.v != nullptr ? 2 : 1) * (a.row_bytes / (int)sizeof(Piece) + (a.k_scale != nullptr ? a.n_heads : 0));
+  const int threads = items <= 64 ? 64 : items <= 128 ? 128 : 256;
+  hipLaunchKernelGGL(k_keep_path<Piece>, dim3((unsigned)n_seq, (unsigned)((items + threads - 1) / threads)), dim3(threads), 0,
+                     st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_keep_path(int n_seq, const KeepArgs& a, hipStream_t st) {
+  return a.row_bytes % 16 == 0 ? launch_keep<uint4>(n_seq, a, st) : launch_keep<uint2>(n_seq, a, st);
+}
+
+}  // namespace misa

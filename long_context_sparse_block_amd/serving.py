@@ -1,7 +1,8 @@
 """The paged serving step around the indexer (C ABI in include/misa.h): page
 planning from request lengths, rotary positions, the write of new keys and
-values into their pages, and attention over the pages or over the tokens that
-the indexer picked.
+values into their pages, attention over the pages, over the tokens that the
+indexer picked or of trees of drafted tokens, those trees' plan and the move of
+an accepted path's rows, and e4m3 projections with a scale for each block of 128.
 
 As in _lib: argument marshalling only, raw device pointers and the current HIP
 stream (of the tensors' own device) go to the library, and there is no
@@ -22,6 +23,7 @@ from ._lib import MISA_K_FP8_E4M3, _check, _kdtype, _need, load
 MISA_T_BF16, MISA_T_FP16, MISA_T_FP32 = 0, 1, 2
 _DTYPES = {torch.bfloat16: MISA_T_BF16, torch.float16: MISA_T_FP16, torch.float32: MISA_T_FP32}
 _BF16 = (torch.bfloat16,)
+_CODES = (torch.uint8, torch.float8_e4m3fn)
 _LAYOUTS = {"half": 0, "interleaved": 1}
 
 
@@ -50,6 +52,12 @@ class PagePlan(NamedTuple):
     slots: torch.Tensor       # int64 [n_tokens]
     positions: torch.Tensor   # int32 [n_tokens]
     n_taken: torch.Tensor     # int32 [1]
+
+
+class TreePlan(NamedTuple):
+    """What misa_plan_tree writes (misa.h)."""
+    mask: torch.Tensor        # int32 [n_tokens, words]: ancestor bits
+    positions: torch.Tensor   # int32 [n_tokens]
 
 
 # The C structures as bytes (native layout: the ctypes classes above); packing
@@ -102,6 +110,21 @@ def _rows_py(t, dtypes, name, dev, shape=None):
     return t.data_ptr(), (st if T > 1 else 0), (sh if H > 1 else 0)
 
 
+def _matrix_py(t, dtypes, name, dev, shape=None):
+    """Pointer and row stride of a [rows, columns] tensor whose last dimension is dense."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}" if t.is_cuda else f"{name} must be a GPU tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {tuple(dtypes)}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {'[rows, columns]' if shape is None else tuple(shape)}")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else 0)
+
+
 def _pool_py(pages, heads, head_dim, name, dev):
     """Pointer, kdtype, n_pages, page_keys of a page pool [n_pages, page_keys, heads,
     head_dim] (or [n_pages, page_keys, head_dim] of one head) on GPU `dev`."""
@@ -127,14 +150,14 @@ def _scratch_py(nbytes, like):
 
 
 try:   # the same in C++ (csrc/tensor_args.cpp): a quarter of the time
-    from ._tensor_args import dense as _dense, pool as _pool, rows as _rows, scratch as _scratch
+    from ._tensor_args import dense as _dense, matrix as _matrix, pool as _pool, rows as _rows, scratch as _scratch
 except ModuleNotFoundError:   # not built yet
-    _dense, _pool, _rows, _scratch = _dense_py, _pool_py, _rows_py, _scratch_py
+    _dense, _matrix, _pool, _rows, _scratch = _dense_py, _matrix_py, _pool_py, _rows_py, _scratch_py
 except ImportError as e:   # built against another torch, say: every call raises, importing and building again do not
     def _dense(*args, why=str(e)):
         raise RuntimeError(f"_tensor_args does not load ({why}): build it again with "
                            "`python -m long_context_sparse_block_amd.build`")
-    _pool = _rows = _scratch = _dense
+    _matrix = _pool = _rows = _scratch = _dense
 
 
 def _on(stream, t, name, f, *args):
@@ -344,6 +367,7 @@ def misa_attention_selected_workspace_bytes(shape: AttnShape, pages: KvPages, to
 
 def _attention(name, q, k_pages, v_pages, block_table, q_start, kv_lens, idx, k_scale, v_scale, scale, max_new, out, lse,
                want_lse, ws, stream):
+    """idx: the selected tokens, or a tree's mask, by the call's name."""
     if stream is not None:
         return _on(stream, q, "q", _attention, name, q, k_pages, v_pages, block_table, q_start, kv_lens, idx, k_scale,
                    v_scale, scale, max_new, out, lse, want_lse, ws, None)
@@ -375,6 +399,11 @@ def _attention(name, q, k_pages, v_pages, block_table, q_start, kv_lens, idx, k_
             idx = idx.view(T, topk)
         args += [_dense(idx, i32, (T, topk), "idx", dev), topk]
         fn = lib.misa_attention_selected
+    elif name == "misa_attention_tree":
+        _dev(idx, "mask")
+        words = idx.shape[-1]
+        args += [_dense(idx, i32, (T, words), "mask", dev), words]
+        fn = lib.misa_attention_tree
     else:
         fn = lib.misa_attention_paged
     if out is None:
@@ -386,8 +415,8 @@ def _attention(name, q, k_pages, v_pages, block_table, q_start, kv_lens, idx, k_
     if T == 0:
         return out, lse
     if ws is None:
-        need = (lib.misa_attention_paged_workspace_bytes(shape, pages) if idx is None
-                else lib.misa_attention_selected_workspace_bytes(shape, pages, topk))
+        need = (lib.misa_attention_selected_workspace_bytes(shape, pages, topk) if name == "misa_attention_selected"
+                else lib.misa_attention_paged_workspace_bytes(shape, pages))   # (a tree's is the same)
         ws, at = _scratch(need, q) if need else (None, None)   # (ws stays until the call has been made)
         _call(name, fn, dev, *args, at, need)
     else:
@@ -420,3 +449,138 @@ def misa_attention_selected(q, k_pages, v_pages, block_table, q_start, kv_lens, 
     sequence; negative entries and ones behind the token's position are absent."""
     return _attention("misa_attention_selected", q, k_pages, v_pages, block_table, q_start, kv_lens, idx, k_scale_pages,
                       v_scale_pages, scale, max_new, out, lse, want_lse, ws, stream)
+
+
+def misa_plan_tree(parents, q_start, kv_lens, words: int, plan: TreePlan | None = None, stream=None) -> TreePlan:
+    """The trees of drafted tokens that a step verifies: parents int32 [tokens] names
+    each new token's parent among its sequence's new tokens (the last cached token:
+    -1), q_start and kv_lens as misa_plan_pages gives them.  Returns the TreePlan:
+    ancestor bits for misa_attention_tree, words * 32 of them at least as many as a
+    sequence has new tokens, and the positions that misa_rope and misa_write_pages
+    turn the tokens by (their slots are misa_plan_pages').  plan: its tensors, made
+    new unless given, and none of them among this call's inputs."""
+    if stream is not None:
+        return _on(stream, parents, "parents", misa_plan_tree, parents, q_start, kv_lens, words, plan)
+    dev = _dev(parents, "parents")
+    _dev(kv_lens, "kv_lens")
+    T, n = parents.shape[0], kv_lens.shape[0]
+    i32 = torch.int32
+    if plan is None:
+        plan = TreePlan(torch.empty((T, words), dtype=i32, device=parents.device),
+                        torch.empty(T, dtype=i32, device=parents.device))
+    args = (n, _dense(parents, i32, (T,), "parents", dev), _dense(q_start, i32, (n + 1,), "q_start", dev),
+            _dense(kv_lens, i32, (n,), "kv_lens", dev), T, words, _dense(plan.mask, i32, (T, words), "mask", dev),
+            _dense(plan.positions, i32, (T,), "positions", dev))
+    if T > 0:
+        _call("misa_plan_tree", load().misa_plan_tree, dev, *args)
+    return plan
+
+
+def misa_attention_tree(q, k_pages, v_pages, block_table, q_start, kv_lens, mask, k_scale_pages=None,
+                        v_scale_pages=None, scale=None, max_new: int = 0, out=None, lse=None, want_lse=False, ws=None,
+                        stream=None):
+    """misa_attention_paged of trees of drafted tokens: a sequence's new token i sees
+    its cached tokens and those new tokens j whose bit j its mask row has
+    (int32 [tokens, words], as misa_plan_tree gives it or any other)."""
+    return _attention("misa_attention_tree", q, k_pages, v_pages, block_table, q_start, kv_lens, mask, k_scale_pages,
+                      v_scale_pages, scale, max_new, out, lse, want_lse, ws, stream)
+
+
+def misa_attention_tree_workspace_bytes(shape: AttnShape, pages: KvPages) -> int:
+    return int(load().misa_attention_tree_workspace_bytes(ctypes.byref(shape), ctypes.byref(pages)))
+
+
+def misa_keep_path(path, q_start, kv_lens, block_table, k_pages, k_scale_pages=None, v_pages=None, v_scale_pages=None,
+                   kept_lens=None, stream=None):
+    """Moves an accepted path's keys (and values) to the places behind the cached
+    prefix, in the pages: path int32 [n_seq, most] names each sequence's kept new
+    tokens in rising order, ended by -1 (or the row's end).  Returns kept_lens int32
+    [n_seq], the sequences' lengths now, the next step's cached_lens (made new unless
+    given; not kv_lens itself).  One call for each layer's pages, and for the index
+    keys'."""
+    if stream is not None:
+        return _on(stream, path, "path", misa_keep_path, path, q_start, kv_lens, block_table, k_pages, k_scale_pages,
+                   v_pages, v_scale_pages, kept_lens)
+    dev = _dev(path, "path")
+    _dev(block_table, "block_table"), _dev(k_pages, "k_pages")
+    H, D = (k_pages.shape[2] if k_pages.dim() == 4 else 1), k_pages.shape[-1]
+    kpool, kd, n_pages, page_keys = _pool(k_pages, H, D, "k_pages", dev)
+    vpool = ks = vs = None
+    if v_pages is not None:
+        vpool, *like = _pool(v_pages, H, D, "v_pages", dev)
+        if like != [kd, n_pages, page_keys]:
+            raise ValueError("v_pages must match k_pages")
+    if kd == MISA_K_FP8_E4M3:
+        ks = _pool_scale(k_scale_pages, n_pages, page_keys, H, "k_scale_pages", dev)
+        if v_pages is not None:
+            vs = _pool_scale(v_scale_pages, n_pages, page_keys, H, "v_scale_pages", dev)
+    n, most, width = path.shape[0], path.shape[-1], block_table.shape[-1]
+    i32 = torch.int32
+    if kept_lens is None:
+        kept_lens = torch.empty(n, dtype=i32, device=path.device)
+    _call("misa_keep_path", load().misa_keep_path, dev, n, _dense(path, i32, (n, most), "path", dev), most,
+          _dense(q_start, i32, (n + 1,), "q_start", dev), _dense(kv_lens, i32, (n,), "kv_lens", dev),
+          _dense(block_table, i32, (n, width), "block_table", dev), width, H, D, kpool, vpool, kd, ks, vs, n_pages,
+          page_keys, _dense(kept_lens, i32, (n,), "kept_lens", dev))
+    return kept_lens
+
+
+def misa_quantize_blocks(x, block_rows: int = 1, codes=None, scale=None, stream=None):
+    """e4m3 codes (uint8) of x [rows, columns] (bf16, fp16 or fp32; any row stride that
+    keeps rows 16-byte aligned; columns a multiple of 16) and the fp32 scales of its
+    blocks of block_rows x 128, [ceil(rows / block_rows), ceil(columns / 128)]:
+    block_rows = 1 for activations, 128 for weights."""
+    if stream is not None:
+        return _on(stream, x, "x", misa_quantize_blocks, x, block_rows, codes, scale)
+    dev = _dev(x, "x")
+    at, st = _matrix(x, _DTYPES, "x", dev)
+    R, K = x.shape
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows: {block_rows}, expected 1 or 128")
+    blocks = (-(-R // block_rows), -(-K // 128))
+    if codes is None:
+        codes = torch.empty((R, K), dtype=torch.uint8, device=x.device)
+    if scale is None:
+        scale = torch.empty(blocks, dtype=torch.float32, device=x.device)
+    args = (at, _DTYPES[x.dtype], R, K, st, block_rows, _dense(codes, codes.dtype if codes.dtype in _CODES else torch.uint8,
+                                                               (R, K), "codes", dev),
+            _dense(scale, torch.float32, blocks, "scale", dev))
+    if R > 0:
+        _call("misa_quantize_blocks", load().misa_quantize_blocks, dev, *args)
+    return codes, scale
+
+
+def misa_matmul_q8_workspace_bytes(m: int, n: int, k: int) -> int:
+    return int(load().misa_matmul_q8_workspace_bytes(m, n, k))
+
+
+def misa_matmul_q8(x, x_scale, w, w_scale, out=None, ws=None, stream=None):
+    """x w^T in bf16 of e4m3 codes x [m, k] with a scale for each 1 x 128 block and w [n, k] with one for each
+    128 x 128 (misa_quantize_blocks; uint8 or float8_e4m3fn, rows 16-byte aligned, k a
+    multiple of 16).  out: bf16 [m, n], its last dimension dense."""
+    if stream is not None:
+        return _on(stream, x, "x", misa_matmul_q8, x, x_scale, w, w_scale, out, ws)
+    dev = _dev(x, "x")
+    xp, xst = _matrix(x, _CODES, "x", dev)
+    wp, wst = _matrix(w, _CODES, "w", dev)
+    (M, K), N = x.shape, w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError(f"w: shape {tuple(w.shape)}, expected ({N}, {K})")
+    across = (K + 127) // 128
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    op, ost = _matrix(out, _BF16, "out", dev, (M, N))
+    args = (M, N, K, xp, xst, _dense(x_scale, torch.float32, (M, across), "x_scale", dev), wp, wst,
+            _dense(w_scale, torch.float32, ((N + 127) // 128, across), "w_scale", dev), op, ost)
+    if M == 0:
+        return out
+    lib = load()
+    if ws is None:
+        need = lib.misa_matmul_q8_workspace_bytes(M, N, K)
+        ws, at = _scratch(need, x) if need else (None, None)   # (ws stays until the call has been made)
+    else:
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be a dense tensor on cuda:{dev}")
+        at, need = ws.data_ptr(), ws.numel() * ws.element_size()
+    _call("misa_matmul_q8", lib.misa_matmul_q8, dev, *args, at, need)
+    return out
