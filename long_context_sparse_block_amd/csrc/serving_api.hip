@@ -95,7 +95,7 @@ misa_status attention(const misa_attn_shape* s, const misa_kv_pages* p, const ui
 constexpr int32_t kMaxTreeWords = 1024;
 constexpr int64_t kMaxCols = (int64_t)1 << 20;
 constexpr int64_t kMaxBlocks = (int64_t)1 << 27;    // quantised in one call
-constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxStride = (int64_t)1 << 22;   // of rows of codes: a tile of 256 stays within 32 bits
 
 misa_status check_matmul(int64_t m, int64_t n, int64_t k) {
   if (m < 0 || n < 1 || k < 1) return MISA_ERR_INVALID_ARG;
@@ -300,7 +300,7 @@ misa_status misa_matmul_q8(int64_t m, int64_t n, int64_t k, const uint8_t* x, in
     return MISA_ERR_INVALID_ARG;
   if (x_stride < 0 || w_stride < 0 || x_stride % 16 != 0 || w_stride % 16 != 0) return MISA_ERR_INVALID_ARG;
   if (m > 1 && out_stride < n) return MISA_ERR_INVALID_ARG;
-  if (x_stride > kMaxStride || w_stride > kMaxStride || out_stride > kMaxStride) return MISA_ERR_UNSUPPORTED;
+  if (x_stride > kMaxStride || w_stride > kMaxStride || out_stride > ((int64_t)1 << 40)) return MISA_ERR_UNSUPPORTED;
   const size_t need = misa::matmul_q8_workspace_bytes(m, n, k);
   if (need > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < need)) return MISA_ERR_WORKSPACE;
   if (m == 0) return MISA_OK;
