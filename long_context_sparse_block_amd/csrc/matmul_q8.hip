@@ -12,8 +12,13 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
 __device__ __forceinline__ f32x4 mfma128(i32x8 a, i32x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma64(i32x8 a, i32x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
 }
 // 16 bytes a lane from a buffer into LDS (dst: the wave's 1 KB, lane order)
 typedef __attribute__((address_space(3))) void* lds_void;
@@ -21,24 +26,34 @@ __device__ __forceinline__ void stage16(__amdgpu_buffer_rsrc_t r, unsigned char*
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void)dst, 16, off, block * 128, 0, 0);
 }
 
+constexpr int kValu = 0x2, kMfma = 0x8, kDsRead = 0x100;   // instruction classes of sched_group_barrier
+
 // What a launch adds to the arguments
 struct Plan {
   int tiles_n, tiles_m;   // output tiles
   int splits, per;        // parts of the blocks, and blocks of a part
-  float* part;            // splits > 1: the parts' sums [split][m][n]
+  float* part;            // splits > 1: the parts' sums [split][m][ld]
+  int64_t ld;             // n, rounded up to 4
 };
 }  // namespace
 
-// A workgroup of WN x WM waves takes (16 FN WN) rows of w by (16 FM WM) rows of x, a
-// wave 16 FN by 16 FM of them.  A block's codes are staged in LDS for all waves, the
+// A workgroup of WN x WM waves takes (32 FN WN) rows of w by (32 FM WM) rows of x, a
+// wave 32 FN by 32 FM of them.  A block's codes are staged in LDS for all waves, the
 // next block's while this one is multiplied; row r's piece c of 16 bytes lies at c ^ (r
-// & 7), so eight rows' reads of a piece meet no bank twice.
+// / 2 & 7): a read of a piece takes 16 rows at a time, and two rows fill all banks.
+//
+// A block of a 32 x 32 tile is two matrix instructions of 64 cycles, between which
+// the tile before is scaled and added: 16 vector instructions, where such an
+// instruction leaves room for 12 beside it.  (Of 16 x 16 x 128 every second cycle of
+// the vector unit is the matrix unit's own, 4 fit beside one, and its tile needs 4.)
+// The last row of a block's tiles is multiplied behind the barrier, while the
+// next block's first operands are read.
 template <int WN, int WM, int FN, int FM>
-__global__ void __launch_bounds__(WN * WM * kWave, WN * WM == 8 ? 2 : 2) k_matmul_tile(const MatmulArgs a, const Plan pl) {
-  constexpr int NW = WN * WM, BN = 16 * FN * WN, BM = 16 * FM * WM;
+__global__ void __launch_bounds__(WN * WM * kWave, 2) k_matmul_tile(const MatmulArgs a, const Plan pl) {
+  constexpr int NW = WN * WM, BN = 32 * FN * WN, BM = 32 * FM * WM;
   constexpr int LN = BN / 8 / NW, LM = BM / 8 / NW;   // loads of a wave: 8 rows each
   __shared__ __attribute__((aligned(16))) unsigned char s_w0[BN * 128], s_w1[BN * 128], s_x0[BM * 128], s_x1[BM * 128];
-  const int lane = threadIdx.x & 63, g4 = lane >> 4, c16 = lane & 15;
+  const int lane = threadIdx.x & 63, h = lane >> 5, c32 = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave % WN, wm = wave / WN;
 
@@ -55,123 +70,314 @@ __global__ void __launch_bounds__(WN * WM * kWave, WN * WM == 8 ? 2 : 2) k_matmu
   const int kend = min((int)a.k, b1 * 128);
 
   const int rows_n = (int)min((int64_t)BN, a.n - n0), rows_m = (int)min((int64_t)BM, a.m - m0);
-  const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(a.w + n0 * a.w_st, (uint32_t)((rows_n - 1) * a.w_st + a.k));
-  const __amdgpu_buffer_rsrc_t rx = uniform_rsrc(a.x + m0 * a.x_st, (uint32_t)((rows_m - 1) * a.x_st + a.k));
-  // rows past the last repeat it; their results are not written
-  uint32_t ow[LN], ox[LM];
-  const int piece = (lane & 7) ^ (lane >> 3);   // (loads begin at multiples of 8 rows)
+  // Eight rows' buffer, as far as there are rows: what lies behind reads as 0
+  auto eight = [&](const uint8_t* base, int64_t st, int row, int rows) __attribute__((always_inline)) {
+    const int in = min(8, rows - row);
+    return uniform_rsrc(base + (in > 0 ? row * st : 0), in > 0 ? (uint32_t)((in - 1) * st + a.k) : 0u);
+  };
+  __amdgpu_buffer_rsrc_t rw[LN], rx[LM];
 #pragma unroll
-  for (int u = 0; u < LN; ++u) ow[u] = (uint32_t)min((u * NW + wave) * 8 + (lane >> 3), rows_n - 1) * (uint32_t)a.w_st + piece * 16;
+  for (int u = 0; u < LN; ++u) rw[u] = eight(a.w + n0 * a.w_st, a.w_st, (u * NW + wave) * 8, rows_n);
 #pragma unroll
-  for (int u = 0; u < LM; ++u) ox[u] = (uint32_t)min((u * NW + wave) * 8 + (lane >> 3), rows_m - 1) * (uint32_t)a.x_st + piece * 16;
-  const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(a.xs + m0 * across, (uint32_t)(rows_m * across) * 4u);
-  uint32_t os[FM];
+  for (int u = 0; u < LM; ++u) rx[u] = eight(a.x + m0 * a.x_st, a.x_st, (u * NW + wave) * 8, rows_m);
+  const int piece = (lane & 7) ^ (lane >> 4) ^ ((wave & 1) << 2);   // (a load's 8 rows begin at 8 (u NW + wave))
+  const uint32_t ow = (uint32_t)(lane >> 3) * (uint32_t)a.w_st + piece * 16;
+  const uint32_t ox = (uint32_t)(lane >> 3) * (uint32_t)a.x_st + piece * 16;
+  // scales: 32 rows of x each, as far as there are rows; the row of blocks of w that the wave is in
+  __amdgpu_buffer_rsrc_t rs[FM];
 #pragma unroll
-  for (int j = 0; j < FM; ++j) os[j] = (uint32_t)(min((wm * FM + j) * 16 + c16, rows_m - 1) * across) * 4u;
-  const __amdgpu_buffer_rsrc_t rt = uniform_rsrc(a.ws + min(n0 + wn * FN * 16, a.n - 1) / 128 * across, (uint32_t)across * 4u);
+  for (int j = 0; j < FM; ++j) {
+    const int row = (wm * FM + j) * 32, in = max(0, min(32, rows_m - row));
+    rs[j] = uniform_rsrc(a.xs + (in > 0 ? (m0 + row) * across : 0), (uint32_t)(in * across) * 4u);
+  }
+  const __amdgpu_buffer_rsrc_t rt = uniform_rsrc(a.ws + min(n0 + wn * FN * 32, a.n - 1) / 128 * across, (uint32_t)across * 4u);
+  const uint32_t os = (uint32_t)(c32 * across) * 4u;
 
-  float s_next[FM], ws_next;
   auto issue = [&](int b, unsigned char* dw, unsigned char* dx) __attribute__((always_inline)) {
-    // from kend on there are no codes: past the buffer's end, which reads as 0
+    // from kend on there are no codes: past the buffer's end too
     const uint32_t gone = b * 128 + piece * 16 >= kend ? 0x80000000u : 0u;
 #pragma unroll
-    for (int u = 0; u < LN; ++u) stage16(rw, dw + (u * NW + wave) * 1024, ow[u] | gone, b);
+    for (int u = 0; u < LN; ++u) stage16(rw[u], dw + (u * NW + wave) * 1024, ow | gone, b);
 #pragma unroll
-    for (int u = 0; u < LM; ++u) stage16(rx, dx + (u * NW + wave) * 1024, ox[u] | gone, b);
+    for (int u = 0; u < LM; ++u) stage16(rx[u], dx + (u * NW + wave) * 1024, ox | gone, b);
   };
+  float xs_next[FM], ws_next;
   auto scales = [&](int b) __attribute__((always_inline)) {
     const uint32_t gone = b < b1 ? 0u : 0x80000000u;   // (0, so that nothing is added)
 #pragma unroll
-    for (int j = 0; j < FM; ++j) s_next[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, os[j] | gone, b * 4, 0));
+    for (int j = 0; j < FM; ++j) xs_next[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs[j], os | gone, b * 4, 0));
     ws_next = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rt, gone, b * 4, 0));
   };
 
-  f32x4 sum[FN][FM];
+  f32x16 sum[FN][FM], p;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) p[e] = 0.f;
 #pragma unroll
   for (int i = 0; i < FN; ++i)
 #pragma unroll
-    for (int j = 0; j < FM; ++j) sum[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // pieces g4 and g4 + 4 of row c16
-  const int lo = c16 * 128 + ((g4 ^ (c16 & 7)) << 4);
-  auto frag = [&](const unsigned char* s) __attribute__((always_inline)) {
-    const i32x4 x = *reinterpret_cast<const i32x4*>(s + lo), y = *reinterpret_cast<const i32x4*>(s + (lo ^ 64));
-    return i32x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+    for (int j = 0; j < FM; ++j) sum[i][j] = p;
+  float s_old, s[FM];   // of the tile before the block's first, of the block
+#pragma unroll
+  for (int j = 0; j < FM; ++j) s[j] = 0.f;
+  // A lane's codes of row c32: pieces h, 2 + h, 4 + h, 6 + h
+  struct Frag {
+    i32x8 k[2];
   };
-  auto step = [&](int b, const unsigned char* cw, const unsigned char* cx, unsigned char* nw, unsigned char* nx) __attribute__((always_inline)) {
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();   // block b is in LDS, and nobody reads the other buffer any more
-    float s[FM];
+  const int at = c32 * 128 + ((h ^ ((c32 >> 1) & 7)) << 4), at_w = at + wn * FN * 4096, at_x = at + wm * FM * 4096;
+  auto frag = [&](const unsigned char* from, int lane_at) __attribute__((always_inline)) {
+    i32x4 x[4];
+    // (the addresses are formed here each time: kept, those of four buffers take 16 registers)
+    asm volatile("" : "+v"(lane_at));
 #pragma unroll
-    for (int j = 0; j < FM; ++j) s[j] = s_next[j] * ws_next;
-    issue(b + 1, nw, nx);
+    for (int q = 0; q < 4; ++q) x[q] = *reinterpret_cast<const i32x4*>(from + (lane_at ^ (q << 5)));
+    return Frag{{i32x8{x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]},
+                 i32x8{x[2][0], x[2][1], x[2][2], x[2][3], x[3][0], x[3][1], x[3][2], x[3][3]}}};
+  };
+  Frag fx[FM], fw;
+  auto step = [&](int b, unsigned char* cw, unsigned char* cx, const unsigned char* nw, const unsigned char* nx) __attribute__((always_inline)) {
+    s_old = s[FM - 1];
+#pragma unroll
+    for (int j = 0; j < FM; ++j) s[j] = xs_next[j] * ws_next;
     scales(b + 1);
-    i32x8 fx[FM];
 #pragma unroll
-    for (int j = 0; j < FM; ++j) fx[j] = frag(cx + (wm * FM + j) * 2048);
-    // A row of products while the row before it is scaled and added
-    i32x8 fw = frag(cw + wn * FN * 2048);
-    f32x4 p[2][FM];
-#pragma unroll
-    for (int i = 0; i <= FN; ++i) {
-      i32x8 next = fw;
-      if (i + 1 < FN) next = frag(cw + (wn * FN + i + 1) * 2048);
+    for (int i = 0; i < FN; ++i) {
+      if (i == FN - 1) {
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();   // block b + 1 is in LDS, and nobody reads block b there any more
+        issue(b + 2, cw, cx);
+      }
+      const Frag next = i + 1 < FN ? frag(cw + (i + 1) * 4096, at_w) : frag(nw, at_w);
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
-        if (i < FN) p[i & 1][j] = mfma128(fw, fx[j], f32x4{0.f, 0.f, 0.f, 0.f});
-        if (i > 0)
+        const int before = i * FM + j - 1;   // the tile whose products are scaled and added
+        f32x16& to = before < 0 ? sum[FN - 1][FM - 1] : sum[before / FM][before % FM];
+        const float sc = before < 0 ? s_old : s[before % FM];
+        f32x16 y;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sum[i - 1][j][e] = __builtin_fmaf(p[(i - 1) & 1][j][e], s[j], sum[i - 1][j][e]);
+        for (int e = 0; e < 16; ++e) y[e] = 0.f;
+        y = mfma64(fw.k[0], fx[j].k[0], y);
+        y = mfma64(fw.k[1], fx[j].k[1], y);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) to[e] = __builtin_fmaf(p[e], sc, to[e]);
+        p = y;
+        if (i == FN - 1) fx[j] = frag(nx + j * 4096, at_x);
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kValu, 8, 0);
+        __builtin_amdgcn_sched_group_barrier(kDsRead, 4, 0);
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kValu, 8, 0);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
       fw = next;
     }
   };
   issue(b0, s_w0, s_x0);
   scales(b0);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  issue(b0 + 1, s_w1, s_x1);
+#pragma unroll
+  for (int j = 0; j < FM; ++j) fx[j] = frag(s_x0 + j * 4096, at_x);
+  fw = frag(s_w0, at_w);
   for (int b = b0; b < b1; b += 2) {   // (an odd last one is followed by a block of nothing)
     step(b, s_w0, s_x0, s_w1, s_x1);
     step(b + 1, s_w1, s_x1, s_w0, s_x0);
   }
-  __builtin_amdgcn_s_waitcnt(0);   // no load into LDS outlives the workgroup
+#pragma unroll
+  for (int e = 0; e < 16; ++e) sum[FN - 1][FM - 1][e] = __builtin_fmaf(p[e], s[FM - 1], sum[FN - 1][FM - 1][e]);
+  // sum[i][j][4 q + e]: column 32 i + 8 q + 4 h + e of row 32 j + c32 of the wave's part
+  const int64_t mw = m0 + wm * FM * 32, nw = n0 + wn * FN * 32;
+  if (pl.splits > 1) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const int64_t m = mw + j * 32 + c32;
+      float* const dst = pl.part + ((int64_t)split * a.m + m) * pl.ld + nw;
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (m < a.m && nw + i * 32 + 8 * q + 4 * h < a.n)
+            *reinterpret_cast<f32x4*>(dst + i * 32 + 8 * q + 4 * h) =
+                f32x4{sum[i][j][4 * q], sum[i][j][4 * q + 1], sum[i][j][4 * q + 2], sum[i][j][4 * q + 3]};
+    }
+    __builtin_amdgcn_s_waitcnt(0);   // no load into LDS outlives the workgroup
+    return;
+  }
+  // Through LDS, so that rows are written 16 bytes a lane and side by side: from
+  // the lanes that hold them they go out in pieces of 16 bytes, and took as long as a
+  // quarter of the products (8192 x 8192 x 4096).  Row r's piece c lies at c ^ r.
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();   // nothing is read or loaded there any more
+  constexpr int P = FN * 4, RP = kWave / P;   // pieces of a row, rows of a store
+  static_assert(BN == BM && 32 * FM * 64 * FN * 2 <= BN * 128, "two waves' rows fit an array");
+  unsigned char* const mine = (wave / 2 == 0 ? s_w0 : wave / 2 == 1 ? s_w1 : wave / 2 == 2 ? s_x0 : s_x1) + (wave & 1) * (FM * 32 * P * 16);
+#pragma unroll
+  for (int j = 0; j < FM; ++j)
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint2*>(mine + (j * 32 + c32) * P * 16 + (((i * 4 + q) ^ (c32 & (P - 1))) << 4) + h * 8) =
+            make_uint2(pk_bf16(sum[i][j][4 * q], sum[i][j][4 * q + 1]), pk_bf16(sum[i][j][4 * q + 2], sum[i][j][4 * q + 3]));
+  const bool wide = ((a.o_st | (int64_t)((uintptr_t)a.out >> 1)) & 7) == 0;
+  const int row = lane / P, col = lane % P;
+  const int64_t n = nw + col * 8;
+#pragma unroll
+  for (int r = 0; r < FM * 32; r += RP) {
+    const uint4 y = *reinterpret_cast<const uint4*>(mine + (r + row) * P * 16 + ((col ^ ((r + row) & (P - 1))) << 4));
+    const int64_t m = mw + r + row;
+    if (m >= a.m || n >= a.n) continue;
+    uint16_t* const dst = a.out + m * a.o_st + n;
+    if (wide && n + 8 <= a.n) {
+      *reinterpret_cast<uint4*>(dst) = y;
+    } else {
+      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (n + e < a.n) dst[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+    }
+  }
+}
 
-  // sum[i][j][e]: column 16 i + 4 g4 + e of row 16 j + c16 of the wave's part
-  const bool wide = ((a.o_st | (int64_t)((uintptr_t)a.out >> 1)) & 3) == 0;
+// Few rows of x (at most 16 MT): bound by the reading of w.  A workgroup takes 16 NT
+// rows of w, each of its 8 waves an eighth of their blocks; their sums join in LDS, always
+// in the same order.  w's codes go straight to the registers that the
+// products read them from, x's through the wave's own LDS (side by side there, a row's
+// lanes are apart in the registers' order, which loads at a third of the rate), both a
+// block ahead, so that no barrier stands between a wave and its loads.
+template <int NT, int MT>
+__global__ void __launch_bounds__(8 * kWave, 2) k_matmul_rows(const MatmulArgs a) {
+  constexpr int kXBytes = MT * 2048, kWaves = 8;
+  constexpr int kJoin = kWaves * NT * MT * kWave * 16;
+  constexpr int kBuf = kWaves * kXBytes;
+  __shared__ __attribute__((aligned(16))) unsigned char s_x0[kJoin > kBuf ? kJoin : kBuf], s_x1[kBuf];
+  const int lane = threadIdx.x & 63, g4 = lane >> 4, c16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * 16 * NT;
+  const int across = (int)((a.k + 127) / 128);
+  const int rows_m = (int)a.m, rows_n = (int)min((int64_t)16 * NT, a.n - n0);
+
+  const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(a.w + n0 * a.w_st, (uint32_t)((rows_n - 1) * a.w_st + a.k));
+  const __amdgpu_buffer_rsrc_t rx = uniform_rsrc(a.x, (uint32_t)((rows_m - 1) * a.x_st + a.k));
+  const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(a.xs, (uint32_t)(rows_m * across) * 4u);
+  const __amdgpu_buffer_rsrc_t rt = uniform_rsrc(a.ws + n0 / 128 * across, (uint32_t)across * 4u);
+  // rows past the last repeat it; their results are not written
+  const int piece = (lane & 7) ^ (lane >> 3);
+  uint32_t ow[NT], ox[2 * MT], os[MT];
 #pragma unroll
-  for (int j = 0; j < FM; ++j) {
-    const int64_t m = m0 + (wm * FM + j) * 16 + c16;
-    if (m >= a.m) continue;
+  for (int i = 0; i < NT; ++i) ow[i] = (uint32_t)min(i * 16 + c16, rows_n - 1) * (uint32_t)a.w_st + g4 * 16;
 #pragma unroll
-    for (int i = 0; i < FN; ++i) {
-      const int64_t n = n0 + (wn * FN + i) * 16 + 4 * g4;
-      if (n >= a.n) continue;
-      const f32x4 v = sum[i][j];
-      if (pl.splits > 1) {
-        float* const dst = pl.part + ((int64_t)split * a.m + m) * a.n + n;
+  for (int u = 0; u < 2 * MT; ++u) ox[u] = (uint32_t)min(u * 8 + (lane >> 3), rows_m - 1) * (uint32_t)a.x_st + piece * 16;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < a.n) dst[e] = v[e];
-        continue;
-      }
-      uint16_t* const dst = a.out + m * a.o_st + n;
-      const uint2 y = make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
-      if (wide && n + 4 <= a.n) {
-        *reinterpret_cast<uint2*>(dst) = y;
-      } else {
-        dst[0] = (uint16_t)(y.x & 0xFFFFu);
-        if (n + 1 < a.n) dst[1] = (uint16_t)(y.x >> 16);
-        if (n + 2 < a.n) dst[2] = (uint16_t)(y.y & 0xFFFFu);
-        if (n + 3 < a.n) dst[3] = (uint16_t)(y.y >> 16);
+  for (int j = 0; j < MT; ++j) os[j] = (uint32_t)(min(j * 16 + c16, rows_m - 1) * across) * 4u;
+
+  // the wave's blocks
+  const int per = (across + kWaves - 1) / kWaves, b0 = min(wave * per, across), b1 = min(b0 + per, across);
+  const int k = min((int)a.k, b1 * 128);
+  struct Codes {
+    i32x4 w[NT][2];
+  };
+  // scales of four blocks: a lane's of one block are as many lines apart as of four
+  struct Scales {
+    f32x4 x[MT], w;
+  };
+  auto four = [&](int b, Scales& c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < MT; ++j) c.x[j] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, os[j], b * 4, 0));
+    c.w = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rt, 0, b * 4, 0));
+  };
+  auto issue = [&](int b, unsigned char* dst, Codes& c) __attribute__((always_inline)) {
+    // behind the last column there are no codes: past the buffers' ends, which read as 0
+    const uint32_t gone = b * 128 + piece * 16 >= k ? 0x80000000u : 0u;
+#pragma unroll
+    for (int u = 0; u < 2 * MT; ++u) stage16(rx, dst + u * 1024, ox[u] | gone, b);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        c.w[i][q] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                  rw, (ow[i] + q * 64) | (b * 128 + q * 64 + g4 * 16 >= k ? 0x80000000u : 0u), b * 128, 0));
+  };
+  constexpr int kOps = 2 * MT + 2 * NT;   // loads of a block
+
+  f32x4 sum[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) sum[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int at = c16 * 128 + ((g4 ^ (c16 & 7)) << 4);   // pieces g4 and g4 + 4 of row c16
+  auto multiply = [&](int b, const unsigned char* x, const Codes& c, const Scales& sc, int e4) __attribute__((always_inline)) {
+    const float ws = b < b1 ? sc.w[e4] : 0.f;   // (behind the wave's blocks the codes are 0, the scales another's)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      const i32x4 lo = *reinterpret_cast<const i32x4*>(x + j * 2048 + at), hi = *reinterpret_cast<const i32x4*>(x + j * 2048 + (at ^ 64));
+      const i32x8 fx = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      const float s = b < b1 ? sc.x[j][e4] * ws : 0.f;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const i32x4 p0 = c.w[i][0], p1 = c.w[i][1];
+        const f32x4 p = mfma128(i32x8{p0[0], p0[1], p0[2], p0[3], p1[0], p1[1], p1[2], p1[3]}, fx, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[i][j][e] = __builtin_fmaf(p[e], s, sum[i][j][e]);
       }
     }
+  };
+  unsigned char* const x0 = s_x0 + wave * kXBytes;
+  unsigned char* const x1 = s_x1 + wave * kXBytes;
+  Codes c0, c1;
+  Scales sc, next;
+  four(b0, sc);
+  issue(b0, x0, c0);
+  auto step = [&](int b, int e4, unsigned char* cur, Codes& c, unsigned char* nxt, Codes& n) __attribute__((always_inline)) {
+    issue(b + 1, nxt, n);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(kOps));   // all but what has just been asked for
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(b, cur, c, sc, e4);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  for (int b = b0; b < b1; b += 4) {   // (blocks past the last add nothing)
+    four(b + 4, next);
+    step(b, 0, x0, c0, x1, c1);
+    step(b + 1, 1, x1, c1, x0, c0);
+    if (b + 2 >= b1) break;
+    step(b + 2, 2, x0, c0, x1, c1);
+    step(b + 3, 3, x1, c1, x0, c0);
+    sc = next;
+  }
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  // sum[i][j][e]: column 16 i + 4 g4 + e of row 16 j + c16
+  f32x4* const join = reinterpret_cast<f32x4*>(s_x0);
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) join[(wave * NT * MT + i * MT + j) * kWave + lane] = sum[i][j];
+  __syncthreads();
+  if (wave >= NT * MT) return;
+  f32x4 v = join[wave * kWave + lane];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) v += join[(w * NT * MT + wave) * kWave + lane];
+  const int64_t m = wave % MT * 16 + c16, n = n0 + wave / MT * 16 + 4 * g4;
+  if (m >= a.m || n >= a.n) return;
+  uint16_t* const dst = a.out + m * a.o_st + n;
+  const uint2 y = make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+  if (n + 4 <= a.n && ((uintptr_t)dst & 7) == 0) {
+    *reinterpret_cast<uint2*>(dst) = y;
+  } else {
+    const uint32_t w[2] = {y.x, y.y};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < a.n) dst[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
   }
 }
 
 namespace {
 template <int WN, int WM, int FN, int FM>
 hipError_t launch_tile(const MatmulArgs& a, void* work, hipStream_t st) {
-  constexpr int BN = 16 * FN * WN, BM = 16 * FM * WM;
+  constexpr int BN = 32 * FN * WN, BM = 32 * FM * WM;
   const int tn = (int)((a.n + BN - 1) / BN), tm = (int)((a.m + BM - 1) / BM);
-  const Plan pl{tn, tm, 1, (int)((a.k + 127) / 128), nullptr};
+  const Plan pl{tn, tm, 1, (int)((a.k + 127) / 128), nullptr, 0};
   hipLaunchKernelGGL((k_matmul_tile<WN, WM, FN, FM>), dim3((unsigned)(tn * tm)), dim3(WN * WM * kWave), 0, st, a, pl);
   return hipGetLastError();
 }
@@ -181,9 +387,24 @@ bool matmul_q8_fits(int64_t m, int64_t n, int64_t k) { return ((m + 127) / 128) 
 
 size_t matmul_q8_workspace_bytes(int64_t m, int64_t n, int64_t k) { return 0; }
 
+namespace {
+template <int MT>
+hipError_t launch_rows(const MatmulArgs& a, hipStream_t st) {
+  // 16 rows of w to a workgroup where 32 would leave CUs without one
+  if (a.n <= 16 * 256)
+    hipLaunchKernelGGL((k_matmul_rows<1, MT>), dim3((unsigned)((a.n + 15) / 16)), dim3(8 * kWave), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_matmul_rows<2, MT>), dim3((unsigned)((a.n + 31) / 32)), dim3(8 * kWave), 0, st, a);
+  return hipGetLastError();
+}
+}  // namespace
+
 hipError_t launch_matmul_q8(const MatmulArgs& a, void* work, hipStream_t st) {
-  if (a.m * a.n >= (int64_t)256 * 256 * 200) return launch_tile<2, 4, 8, 4>(a, work, st);
-  return launch_tile<2, 2, 4, 4>(a, work, st);
+  if (a.m <= 16) return launch_rows<1>(a, st);
+  if (a.m <= 32) return launch_rows<2>(a, st);
+  if (a.m <= 64) return launch_rows<4>(a, st);
+  if (a.m * a.n >= (int64_t)256 * 256 * 200) return launch_tile<2, 4, 4, 2>(a, work, st);
+  return launch_tile<2, 2, 2, 2>(a, work, st);
 }
 
 }  // namespace misa
