@@ -3,6 +3,8 @@
 // x and w hold e4m3 codes.  A block's products are one step of
 // v_mfma_f32_16x16x128_f8f6f4, whose result is scaled in fp32 and added to the
 // running sums.
+#include <algorithm>
+
 #include "misa_common.h"
 #include "misa_launch.h"
 
@@ -37,22 +39,50 @@ struct Plan {
 };
 }  // namespace
 
+// The same unknown to the compiler, which would otherwise wait for all loads into
+// LDS before any read of the array that they fill.  Who reads waits: landed().
+// (dst: offset in LDS; no register is written)
+template <int BYTES>
+__device__ __forceinline__ void stage_far(__amdgpu_buffer_rsrc_t r, uint32_t dst, uint32_t off, uint32_t add) {
+#ifdef __HIP_DEVICE_COMPILE__
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(dst), "v"(off), "s"(r), "s"(add) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(dst), "v"(off), "s"(r), "s"(add) : "memory");
+#endif
+}
+// All of the workgroup's loads but each wave's last N have landed in LDS, and its reads are done
+template <int N>
+__device__ __forceinline__ void landed() {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+#endif
+}
+
 // A workgroup of WN x WM waves takes (32 FN WN) rows of w by (32 FM WM) rows of x, a
-// wave 32 FN by 32 FM of them.  A block's codes are staged in LDS for all waves, the
-// next block's while this one is multiplied; row r's piece c of 16 bytes lies at c ^ (r
-// / 2 & 7): a read of a piece takes 16 rows at a time, and two rows fill all banks.
+// wave 32 FN by 32 FM of them.  S blocks' codes and scales are in LDS or on their way
+// there; row r's piece c of 16 bytes lies at c ^ (r / 2 & 7): a read of a piece takes
+// 16 rows at a time, and two rows fill all banks.
 //
 // A block of a 32 x 32 tile is two matrix instructions of 64 cycles, between which
 // the tile before is scaled and added: 16 vector instructions, where such an
 // instruction leaves room for 12 beside it.  (Of 16 x 16 x 128 every second cycle of
 // the vector unit is the matrix unit's own, 4 fit beside one, and its tile needs 4.)
 // The last row of a block's tiles is multiplied behind the barrier, while the
-// next block's first operands are read.
-template <int WN, int WM, int FN, int FM>
-__global__ void __launch_bounds__(WN * WM * kWave, 2) k_matmul_tile(const MatmulArgs a, const Plan pl) {
+// next block's first operands are read.  Loads go out behind that, with more than
+// two blocks a few to a tile: a wave that asks for more than the CU takes in (64 bytes
+// a cycle) stands still, and its products with it.
+template <int WN, int WM, int FN, int FM, int S>
+__global__ void __launch_bounds__(WN * WM * kWave, WN * WM / 4) k_matmul_tile(const MatmulArgs a, const Plan pl) {
   constexpr int NW = WN * WM, BN = 32 * FN * WN, BM = 32 * FM * WM;
   constexpr int LN = BN / 8 / NW, LM = BM / 8 / NW;   // loads of a wave: 8 rows each
-  __shared__ __attribute__((aligned(16))) unsigned char s_w0[BN * 128], s_w1[BN * 128], s_x0[BM * 128], s_x1[BM * 128];
+  constexpr int kOps = LN + LM + 1;                   // and one of scales
+  constexpr int kEarly = S == 2 ? kOps : (kOps + FN - 1) / FN;   // loads of a block in the last row of tiles
+  constexpr int kTiles = FN > 1 ? (FN - 1) * FM : 1;                // tiles that share the others
+  constexpr int kX = BN * 128, kXs = kX + BM * 128, kWs = kXs + BM * 4, kStage = kWs + 256;
+  static_assert(NW > BM / 64 && S * kStage <= 160 * 1024, "a wave for w's scales; the LDS");
+  __shared__ __attribute__((aligned(16))) unsigned char s_mem[S * kStage];
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void)s_mem;
   const int lane = threadIdx.x & 63, h = lane >> 5, c32 = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave % WN, wm = wave / WN;
@@ -83,30 +113,26 @@ __global__ void __launch_bounds__(WN * WM * kWave, 2) k_matmul_tile(const Matmul
   const int piece = (lane & 7) ^ (lane >> 4) ^ ((wave & 1) << 2);   // (a load's 8 rows begin at 8 (u NW + wave))
   const uint32_t ow = (uint32_t)(lane >> 3) * (uint32_t)a.w_st + piece * 16;
   const uint32_t ox = (uint32_t)(lane >> 3) * (uint32_t)a.x_st + piece * 16;
-  // scales: 32 rows of x each, as far as there are rows; the row of blocks of w that the wave is in
-  __amdgpu_buffer_rsrc_t rs[FM];
-#pragma unroll
-  for (int j = 0; j < FM; ++j) {
-    const int row = (wm * FM + j) * 32, in = max(0, min(32, rows_m - row));
-    rs[j] = uniform_rsrc(a.xs + (in > 0 ? (m0 + row) * across : 0), (uint32_t)(in * across) * 4u);
-  }
-  const __amdgpu_buffer_rsrc_t rt = uniform_rsrc(a.ws + min(n0 + wn * FN * 32, a.n - 1) / 128 * across, (uint32_t)across * 4u);
-  const uint32_t os = (uint32_t)(c32 * across) * 4u;
+  // scales: a wave loads 64 rows of x, or (the last ones, all the same) w's rows of blocks
+  const bool of_x = wave < BM / 64;
+  const int srow = of_x ? wave * 64 : 0;
+  const int srows = of_x ? max(0, min(64, rows_m - srow)) : (rows_n + 127) / 128;
+  const __amdgpu_buffer_rsrc_t rs =
+      uniform_rsrc(of_x ? a.xs + (srows > 0 ? (m0 + srow) * across : 0) : a.ws + n0 / 128 * across, (uint32_t)(srows * across) * 4u);
+  const uint32_t os = (uint32_t)(lane * across) * 4u, sdst = of_x ? kXs + wave * 256 : kWs;
 
-  auto issue = [&](int b, unsigned char* dw, unsigned char* dx) __attribute__((always_inline)) {
+  // loads from .. to - 1 of the wave's kOps of block b: x, the scales, w
+  auto issue = [&](int b, int stage, int from, int to) __attribute__((always_inline)) {
+    const uint32_t base = lds0 + stage * kStage;
     // from kend on there are no codes: past the buffer's end too
     const uint32_t gone = b * 128 + piece * 16 >= kend ? 0x80000000u : 0u;
 #pragma unroll
-    for (int u = 0; u < LN; ++u) stage16(rw[u], dw + (u * NW + wave) * 1024, ow | gone, b);
-#pragma unroll
-    for (int u = 0; u < LM; ++u) stage16(rx[u], dx + (u * NW + wave) * 1024, ox | gone, b);
-  };
-  float xs_next[FM], ws_next;
-  auto scales = [&](int b) __attribute__((always_inline)) {
-    const uint32_t gone = b < b1 ? 0u : 0x80000000u;   // (0, so that nothing is added)
-#pragma unroll
-    for (int j = 0; j < FM; ++j) xs_next[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs[j], os | gone, b * 4, 0));
-    ws_next = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rt, gone, b * 4, 0));
+    for (int u = 0; u < kOps; ++u) {
+      if (u < from || u >= to) continue;
+      if (u < LM) stage_far<16>(rx[u < LM ? u : 0], base + kX + (u * NW + wave) * 1024, ox | gone, b * 128);
+      else if (u == LM) stage_far<4>(rs, base + sdst, b < b1 ? os : 0x80000000u, b * 4);   // (0 there, so that nothing is added)
+      else stage_far<16>(rw[u > LM ? u - LM - 1 : 0], base + ((u - LM - 1) * NW + wave) * 1024, ow | gone, b * 128);
+    }
   };
 
   f32x16 sum[FN][FM], p;
@@ -116,37 +142,47 @@ __global__ void __launch_bounds__(WN * WM * kWave, 2) k_matmul_tile(const Matmul
   for (int i = 0; i < FN; ++i)
 #pragma unroll
     for (int j = 0; j < FM; ++j) sum[i][j] = p;
-  float s_old, s[FM];   // of the tile before the block's first, of the block
-#pragma unroll
-  for (int j = 0; j < FM; ++j) s[j] = 0.f;
   // A lane's codes of row c32: pieces h, 2 + h, 4 + h, 6 + h
   struct Frag {
     i32x8 k[2];
   };
-  const int at = c32 * 128 + ((h ^ ((c32 >> 1) & 7)) << 4), at_w = at + wn * FN * 4096, at_x = at + wm * FM * 4096;
+  const int at = c32 * 128 + ((h ^ ((c32 >> 1) & 7)) << 4), at_w = at + wn * FN * 4096, at_x = at + wm * FM * 4096 + kX;
   auto frag = [&](const unsigned char* from, int lane_at) __attribute__((always_inline)) {
     i32x4 x[4];
-    // (the addresses are formed here each time: kept, those of four buffers take 16 registers)
-    asm volatile("" : "+v"(lane_at));
 #pragma unroll
     for (int q = 0; q < 4; ++q) x[q] = *reinterpret_cast<const i32x4*>(from + (lane_at ^ (q << 5)));
     return Frag{{i32x8{x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]},
                  i32x8{x[2][0], x[2][1], x[2][2], x[2][3], x[3][0], x[3][1], x[3][2], x[3][3]}}};
   };
-  Frag fx[FM], fw;
-  auto step = [&](int b, unsigned char* cw, unsigned char* cx, const unsigned char* nw, const unsigned char* nx) __attribute__((always_inline)) {
-    s_old = s[FM - 1];
+  const int at_s = kXs + (wm * FM * 32 + c32) * 4, at_t = kWs + (wn * FN * 32 / 128) * 4;
+  float s_old, s[FM];   // of the tile before the block's first, of the block
+  auto scales = [&](const unsigned char* from) __attribute__((always_inline)) {
+    const float w = *reinterpret_cast<const float*>(from + at_t);
 #pragma unroll
-    for (int j = 0; j < FM; ++j) s[j] = xs_next[j] * ws_next;
-    scales(b + 1);
+    for (int j = 0; j < FM; ++j) s[j] = *reinterpret_cast<const float*>(from + at_s + j * 128) * w;
+  };
+  Frag fx[FM], fw;
+
+#pragma unroll
+  for (int b = 0; b < S - 1; ++b) issue(b0 + b, b, 0, kOps);
+  issue(b0 + S - 1, S - 1, 0, kEarly);
+  landed<(S - 2) * kOps + kEarly>();
+#pragma unroll
+  for (int j = 0; j < FM; ++j) fx[j] = frag(s_mem + j * 4096, at_x);
+  fw = frag(s_mem, at_w);
+#pragma unroll
+  for (int j = 0; j < FM; ++j) s[j] = 0.f;
+  int stage = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int after = stage + 1 < S ? stage + 1 : 0;
+    const unsigned char* const cur = s_mem + stage * kStage;
+    const unsigned char* const nxt = s_mem + after * kStage;
+    s_old = s[FM - 1];
+    scales(cur);
 #pragma unroll
     for (int i = 0; i < FN; ++i) {
-      if (i == FN - 1) {
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();   // block b + 1 is in LDS, and nobody reads block b there any more
-        issue(b + 2, cw, cx);
-      }
-      const Frag next = i + 1 < FN ? frag(cw + (i + 1) * 4096, at_w) : frag(nw, at_w);
+      if (i == FN - 1) landed<(S - 2) * kOps>();   // block b + 1 is in LDS, and nobody reads block b there any more
+      const Frag next = i + 1 < FN ? frag(cur + (i + 1) * 4096, at_w) : frag(nxt, at_w);
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
         const int before = i * FM + j - 1;   // the tile whose products are scaled and added
@@ -160,7 +196,14 @@ __global__ void __launch_bounds__(WN * WM * kWave, 2) k_matmul_tile(const Matmul
 #pragma unroll
         for (int e = 0; e < 16; ++e) to[e] = __builtin_fmaf(p[e], sc, to[e]);
         p = y;
-        if (i == FN - 1) fx[j] = frag(nx + j * 4096, at_x);
+        if (i == FN - 1) {
+          fx[j] = frag(nxt + j * 4096, at_x);
+          issue(b + S, stage, j * kEarly / FM, (j + 1) * kEarly / FM);   // behind the reads: a load waits for those before it
+        } else {
+          constexpr int late = kOps - kEarly;
+          const int n = i * FM + j;
+          issue(b + S - 1, stage > 0 ? stage - 1 : S - 1, kEarly + n * late / kTiles, kEarly + (n + 1) * late / kTiles);
+        }
         __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
         __builtin_amdgcn_sched_group_barrier(kValu, 8, 0);
         __builtin_amdgcn_sched_group_barrier(kDsRead, 4, 0);
@@ -170,21 +213,12 @@ __global__ void __launch_bounds__(WN * WM * kWave, 2) k_matmul_tile(const Matmul
       }
       fw = next;
     }
-  };
-  issue(b0, s_w0, s_x0);
-  scales(b0);
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-  issue(b0 + 1, s_w1, s_x1);
-#pragma unroll
-  for (int j = 0; j < FM; ++j) fx[j] = frag(s_x0 + j * 4096, at_x);
-  fw = frag(s_w0, at_w);
-  for (int b = b0; b < b1; b += 2) {   // (an odd last one is followed by a block of nothing)
-    step(b, s_w0, s_x0, s_w1, s_x1);
-    step(b + 1, s_w1, s_x1, s_w0, s_x0);
+    stage = after;
   }
 #pragma unroll
   for (int e = 0; e < 16; ++e) sum[FN - 1][FM - 1][e] = __builtin_fmaf(p[e], s[FM - 1], sum[FN - 1][FM - 1][e]);
+  landed<0>();   // no load into LDS outlives the workgroup, and nothing is read there any more
+
   // sum[i][j][4 q + e]: column 32 i + 8 q + 4 h + e of row 32 j + c32 of the wave's part
   const int64_t mw = m0 + wm * FM * 32, nw = n0 + wn * FN * 32;
   if (pl.splits > 1) {
@@ -200,17 +234,14 @@ __global__ void __launch_bounds__(WN * WM * kWave, 2) k_matmul_tile(const Matmul
             *reinterpret_cast<f32x4*>(dst + i * 32 + 8 * q + 4 * h) =
                 f32x4{sum[i][j][4 * q], sum[i][j][4 * q + 1], sum[i][j][4 * q + 2], sum[i][j][4 * q + 3]};
     }
-    __builtin_amdgcn_s_waitcnt(0);   // no load into LDS outlives the workgroup
     return;
   }
   // Through LDS, so that rows are written 16 bytes a lane and side by side: from
   // the lanes that hold them they go out in pieces of 16 bytes, and took as long as a
   // quarter of the products (8192 x 8192 x 4096).  Row r's piece c lies at c ^ r.
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();   // nothing is read or loaded there any more
   constexpr int P = FN * 4, RP = kWave / P;   // pieces of a row, rows of a store
-  static_assert(BN == BM && 32 * FM * 64 * FN * 2 <= BN * 128, "two waves' rows fit an array");
-  unsigned char* const mine = (wave / 2 == 0 ? s_w0 : wave / 2 == 1 ? s_w1 : wave / 2 == 2 ? s_x0 : s_x1) + (wave & 1) * (FM * 32 * P * 16);
+  static_assert(NW * FM * 32 * P * 16 <= S * kStage, "the waves' rows fit");
+  unsigned char* const mine = s_mem + wave * (FM * 32 * P * 16);
 #pragma unroll
   for (int j = 0; j < FM; ++j)
 #pragma unroll
@@ -372,22 +403,66 @@ __global__ void __launch_bounds__(8 * kWave, 2) k_matmul_rows(const MatmulArgs a
   }
 }
 
+// The sums of a tile launch's parts, four columns a thread
+__global__ void __launch_bounds__(256) k_matmul_join(const MatmulArgs a, const Plan pl) {
+  const int64_t quads = pl.ld / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= quads * a.m) return;
+  const int64_t m = i / quads, n = (i - m * quads) * 4;
+  const float* const src = pl.part + m * pl.ld + n;
+  f32x4 v = *reinterpret_cast<const f32x4*>(src);
+  for (int s = 1; s < pl.splits; ++s) v += *reinterpret_cast<const f32x4*>(src + (int64_t)s * a.m * pl.ld);
+  uint16_t* const dst = a.out + m * a.o_st + n;
+  const uint2 y = make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+  if (n + 4 <= a.n && ((uintptr_t)dst & 7) == 0) {
+    *reinterpret_cast<uint2*>(dst) = y;
+  } else {
+    const uint32_t w[2] = {y.x, y.y};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < a.n) dst[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+  }
+}
+
 namespace {
-template <int WN, int WM, int FN, int FM>
-hipError_t launch_tile(const MatmulArgs& a, void* work, hipStream_t st) {
+// How a product is made.  The times are of a block of 128 columns: alone on their
+// CUs, tiles of 64 x 64 take 0.3 us, 128 x 64 0.38, 128 x 128 0.47 to 0.65 (by how many
+// there are); two of 128 x 128 on a CU 1.25, one of 256 x 256 2.1; 4 to 8 us a round
+// beside.  So the smallest tiles that the card holds all at once are taken, and
+// past them whichever of the two larger forms has the less time.
+enum Form { kRows, kTile64, kTile128x64, kTile128, kTwo128, kTile256 };
+struct Choice {
+  Form form;
+  int splits, per;
+};
+Choice choose(int64_t m, int64_t n, int64_t k) {
+  const int64_t across = (k + 127) / 128;
+  if (m <= 64) return Choice{kRows, 1, (int)across};
+  auto tiles = [&](int bn, int bm) { return ((n + bn - 1) / bn) * ((m + bm - 1) / bm); };
+  const int64_t small = tiles(64, 64);
+  if (small <= 128 && across >= 24) {
+    // Parts of the blocks side by side: their join is about 12 blocks' time
+    const int64_t splits = std::min<int64_t>(256 / small, across / 4), per = (across + splits - 1) / splits;
+    if (across - per > 12) return Choice{kTile64, (int)((across + per - 1) / per), (int)per};
+  }
+  if (small <= 256) return Choice{kTile64, 1, (int)across};
+  if (tiles(128, 64) <= 256) return Choice{kTile128x64, 1, (int)across};
+  if (tiles(128, 128) <= 256) return Choice{kTile128, 1, (int)across};
+  const double two = (double)((tiles(128, 128) + 511) / 512) * (1.25 * (double)across + 5.0);
+  const double large = (double)((tiles(256, 256) + 255) / 256) * (2.1 * (double)across + 8.0);
+  return Choice{two < large ? kTwo128 : kTile256, 1, (int)across};
+}
+
+template <int WN, int WM, int FN, int FM, int S>
+hipError_t launch_tile(const MatmulArgs& a, const Choice& c, void* work, hipStream_t st) {
   constexpr int BN = 32 * FN * WN, BM = 32 * FM * WM;
   const int tn = (int)((a.n + BN - 1) / BN), tm = (int)((a.m + BM - 1) / BM);
-  const Plan pl{tn, tm, 1, (int)((a.k + 127) / 128), nullptr, 0};
-  hipLaunchKernelGGL((k_matmul_tile<WN, WM, FN, FM>), dim3((unsigned)(tn * tm)), dim3(WN * WM * kWave), 0, st, a, pl);
+  const Plan pl{tn, tm, c.splits, c.per, static_cast<float*>(work), (a.n + 3) / 4 * 4};
+  hipLaunchKernelGGL((k_matmul_tile<WN, WM, FN, FM, S>), dim3((unsigned)(tn * tm * c.splits)), dim3(WN * WM * kWave), 0, st, a, pl);
+  if (c.splits > 1)
+    hipLaunchKernelGGL(k_matmul_join, dim3((unsigned)((a.m * pl.ld / 4 + 255) / 256)), dim3(256), 0, st, a, pl);
   return hipGetLastError();
 }
-}  // namespace
 
-bool matmul_q8_fits(int64_t m, int64_t n, int64_t k) { return ((m + 127) / 128) * ((n + 127) / 128) < ((int64_t)1 << 23); }
-
-size_t matmul_q8_workspace_bytes(int64_t m, int64_t n, int64_t k) { return 0; }
-
-namespace {
 template <int MT>
 hipError_t launch_rows(const MatmulArgs& a, hipStream_t st) {
   // 16 rows of w to a workgroup where 32 would leave CUs without one
@@ -399,12 +474,24 @@ hipError_t launch_rows(const MatmulArgs& a, hipStream_t st) {
 }
 }  // namespace
 
+// (a grid of fewer than 2^23 workgroups)
+bool matmul_q8_fits(int64_t m, int64_t n, int64_t k) { return ((m + 127) / 128) * ((n + 127) / 128) < ((int64_t)1 << 23); }
+
+size_t matmul_q8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  const Choice c = choose(m, n, k);
+  return c.splits > 1 ? (size_t)c.splits * (size_t)m * (size_t)((n + 3) / 4 * 4) * sizeof(float) : 0;
+}
+
 hipError_t launch_matmul_q8(const MatmulArgs& a, void* work, hipStream_t st) {
-  if (a.m <= 16) return launch_rows<1>(a, st);
-  if (a.m <= 32) return launch_rows<2>(a, st);
-  if (a.m <= 64) return launch_rows<4>(a, st);
-  if (a.m * a.n >= (int64_t)256 * 256 * 200) return launch_tile<2, 4, 4, 2>(a, work, st);
-  return launch_tile<2, 2, 2, 2>(a, work, st);
+  const Choice c = choose(a.m, a.n, a.k);
+  switch (c.form) {
+    case kRows: return a.m <= 16 ? launch_rows<1>(a, st) : a.m <= 32 ? launch_rows<2>(a, st) : launch_rows<4>(a, st);
+    case kTile64: return launch_tile<2, 2, 1, 1, 4>(a, c, work, st);
+    case kTile128x64: return launch_tile<2, 2, 2, 1, 4>(a, c, work, st);
+    case kTile128: return launch_tile<2, 4, 2, 1, 4>(a, c, work, st);
+    case kTwo128: return launch_tile<2, 2, 2, 2, 2>(a, c, work, st);
+    default: return launch_tile<2, 4, 4, 2, 2>(a, c, work, st);
+  }
 }
 
 }  // namespace misa

@@ -81,7 +81,10 @@ def operands(seed, m, n, k):
 SIZES = [(1, 1, 16), (1, 128, 128), (1, 2048, 2048), (2, 17, 144), (15, 130, 256), (16, 64, 384), (17, 257, 1504),
          (33, 127, 2064), (48, 300, 1024), (64, 1024, 512), (65, 129, 640), (100, 4099, 272), (128, 128, 128),
          (129, 255, 1920), (200, 1, 528), (257, 383, 144), (300, 513, 2048), (513, 300, 16), (1000, 130, 400),
-         (2, 16, 16384), (70, 96, 16400), (1500, 700, 256)]
+         (2, 16, 16384), (70, 96, 16400), (1500, 700, 256),
+         # forms that the sizes above do not reach: 32 columns to a workgroup, each size of tile, parts of the blocks
+         (5, 4500, 272), (30, 4200, 144), (60, 4130, 400), (128, 8200, 256), (515, 4099, 1504), (700, 8200, 272),
+         (4000, 4000, 528), (3990, 4090, 144), (65, 40, 8208), (120, 500, 4112), (300, 65, 12304)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
