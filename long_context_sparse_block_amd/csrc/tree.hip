@@ -16,10 +16,10 @@ constexpr int kLdsNodes = 2048;   // a tree's parents that a workgroup keeps in 
 constexpr int kPad = 4096;        // words of padded rows that a workgroup clears
 }  // namespace
 
-// A workgroup takes a sequence, a thread a word of a token's bits: it walks from
-// the token to the root and collects the ancestors that lie in its word.  Parents
-// come before their children, so a thread is done once it is below its word; that
-// of word 0 walks to the root and counts the depth.
+// A workgroup takes a sequence, a thread a token: it walks from the token to the root
+// and collects its ancestors, a word of bits at a time (parents come before their
+// children, so the walk goes through the words from the last to the first).  A step
+// is a read of LDS that the next one waits for, some 40 ns.
 __global__ void __launch_bounds__(kPlanThreads) k_plan_tree(int n_seq, const int32_t* parents, const int32_t* q_start,
                                                             const int32_t* kv_lens, int64_t n_tokens, int words,
                                                             uint32_t* mask, int32_t* positions) {
@@ -50,17 +50,18 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_tree(int n_seq, const int
   const int in_lds = min(m, kLdsNodes);
   for (int i = tid; i < in_lds; i += kPlanThreads) s_up[i] = parent(i);
   __syncthreads();
-  const int64_t all = (int64_t)m * words;
-  for (int64_t at = tid; at < all; at += kPlanThreads) {
-    const int i = (int)(at / words), w = (int)(at - (int64_t)i * words);
-    uint32_t bits = 0;
-    int depth = 0;
-    for (int j = i; j >= 32 * w; ++depth) {   // (j falls with every step)
-      if ((j >> 5) == w) bits |= 1u << (j & 31);
-      j = j < kLdsNodes ? s_up[j] : parent(j);
+  for (int i = tid; i < m; i += kPlanThreads) {
+    uint32_t* const row = mask + (t0 + i) * words;
+    int j = i, depth = 0;
+    for (int w = words - 1; w >= 0; --w) {
+      uint32_t bits = 0;
+      for (; j >= 32 * w; ++depth) {   // (j falls with every step)
+        if ((j >> 5) == w) bits |= 1u << (j & 31);
+        j = j < kLdsNodes ? s_up[j] : parent(j);
+      }
+      row[w] = bits;
     }
-    mask[t0 * words + at] = bits;
-    if (w == 0) positions[t0 + i] = (int32_t)(pos0 + depth - 1);
+    positions[t0 + i] = (int32_t)(pos0 + depth - 1);
   }
 }
 
@@ -95,11 +96,12 @@ __global__ void __launch_bounds__(256) k_keep_path(const KeepArgs a) {
   const int64_t col = (int64_t)(item < pieces ? item : item - pieces) * (int)sizeof(Piece);
   float* const sbase = sc < a.n_heads ? a.k_scale : a.v_scale;
   const int scol = sc < a.n_heads ? sc : sc - a.n_heads;
-  auto slot = [&](int64_t t) __attribute__((always_inline)) -> int64_t {
-    const int64_t p = t / a.page_keys;
-    if (t < 0 || p >= a.max_pages) return -1;
-    const int64_t entry = a.table[b * a.max_pages + p];
-    return entry < 0 || entry >= a.n_pages ? -1 : entry * a.page_keys + (t - p * a.page_keys);
+  // pool row of token t (below 2^31: the ABI bounds the pool), -1 where it has none
+  auto slot = [&](int64_t t) __attribute__((always_inline)) -> int {
+    const uint32_t u = (uint32_t)t, p = u / (uint32_t)a.page_keys;
+    if (t < 0 || t > 0x7fffffff || p >= a.max_pages) return -1;
+    const int entry = a.table[b * a.max_pages + p];
+    return entry < 0 || entry >= a.n_pages ? -1 : entry * a.page_keys + (int)(u - p * (uint32_t)a.page_keys);
   };
   int kept = 0;
   for (int i0 = 0; i0 < a.max_path; i0 += 64) {
@@ -112,40 +114,39 @@ __global__ void __launch_bounds__(256) k_keep_path(const KeepArgs a) {
     const int n = gone == 0 ? 64 : (int)__builtin_ctzll(gone);   // kept ones of these 64
     kept += n;
     // a row that stays, or has no place in the pages, moves nothing
-    int64_t src = -1, dst = -1;
+    int src = -1, dst = -1;
     if (lane < n && node != i) {
       src = slot(first + node);
       dst = slot(first + i);
     }
     uint64_t moves = __ballot(src >= 0 && dst >= 0);
     while (moves != 0) {
-      int64_t from[U], to[U];
+      // (behind the last one it is read again: loads behind a branch would be waited for one by one)
+      int from[U], to[U], l = 0, count = 0;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int l = moves != 0 ? (int)__builtin_ctzll(moves) : -1;
-        moves &= moves - 1;
-        const int at = max(l, 0);
-        const int64_t f = ((int64_t)__builtin_amdgcn_readlane((int)(src >> 32), at) << 32) | (uint32_t)__builtin_amdgcn_readlane((int)src, at);
-        const int64_t d = ((int64_t)__builtin_amdgcn_readlane((int)(dst >> 32), at) << 32) | (uint32_t)__builtin_amdgcn_readlane((int)dst, at);
-        from[u] = l < 0 ? -1 : f;
-        to[u] = d;
+        if (moves != 0) {
+          l = (int)__builtin_ctzll(moves);
+          moves &= moves - 1;
+          ++count;
+        }
+        from[u] = __builtin_amdgcn_readlane(src, l);
+        to[u] = __builtin_amdgcn_readlane(dst, l);
       }
       if (is_row) {
         Piece x[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (from[u] >= 0) x[u] = *reinterpret_cast<const Piece*>(base + from[u] * a.row_bytes + col);
+        for (int u = 0; u < U; ++u) x[u] = *reinterpret_cast<const Piece*>(base + (int64_t)from[u] * a.row_bytes + col);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (from[u] >= 0) *reinterpret_cast<Piece*>(base + to[u] * a.row_bytes + col) = x[u];
+          if (u < count) *reinterpret_cast<Piece*>(base + (int64_t)to[u] * a.row_bytes + col) = x[u];
       } else if (is_scale) {
         float x[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (from[u] >= 0) x[u] = sbase[from[u] * a.n_heads + scol];
+        for (int u = 0; u < U; ++u) x[u] = sbase[(int64_t)from[u] * a.n_heads + scol];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (from[u] >= 0) sbase[to[u] * a.n_heads + scol] = x[u];
+          if (u < count) sbase[(int64_t)to[u] * a.n_heads + scol] = x[u];
       }
     }
     if (n < 64) break;
