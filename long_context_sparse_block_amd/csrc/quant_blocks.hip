@@ -62,25 +62,29 @@ __device__ __forceinline__ uint2 codes8(const Eight<DT>& x, float s) {
 }
 }  // namespace
 
-// 16 lanes a block of 1 x 128
+// 8 lanes a block of 1 x 128, 16 values each (so that codes go out 16 bytes a lane)
 template <int DT>
 __global__ void __launch_bounds__(256) k_quant_rows(const char* __restrict__ x, int64_t x_bytes, int64_t rows, int64_t cols,
                                                     uint32_t across, uint8_t* __restrict__ codes, float* __restrict__ scale) {
   constexpr int E = DT == MISA_T_FP32 ? 4 : 2;
-  const int64_t block = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 16;
-  const int64_t r = block / across;
-  const int64_t c = (block - r * across) * 128 + (threadIdx.x & 15) * 8;
+  const uint32_t block = blockIdx.x * 32 + threadIdx.x / 8, row = block / across;   // (fewer than 2^27 blocks)
+  const int64_t r = row, c = (int64_t)(block - row * across) * 128 + (threadIdx.x & 7) * 16;
   const bool in = r < rows && c < cols;
-  Eight<DT> v;
+  Eight<DT> v, w;
   v.zero();
-  if (in) v.load(x + r * x_bytes + c * E);
-  float amax = amax8(v);
+  w.zero();
+  if (in) {
+    v.load(x + r * x_bytes + c * E);
+    w.load(x + r * x_bytes + (c + 8) * E);
+  }
+  float amax = __builtin_fmaxf(amax8(v), amax8(w));
 #pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o, 16));
+  for (int o = 4; o >= 1; o >>= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o, 8));
   const float s = scale_of(amax);
   if (!in) return;
-  *reinterpret_cast<uint2*>(codes + r * cols + c) = codes8(v, s);
-  if ((threadIdx.x & 15) == 0) scale[block] = s;
+  const uint2 a = codes8(v, s), b = codes8(w, s);
+  *reinterpret_cast<uint4*>(codes + r * cols + c) = make_uint4(a.x, a.y, b.x, b.y);
+  if ((threadIdx.x & 7) == 0) scale[block] = s;
 }
 
 // A workgroup a block of 128 x 128: thread t takes piece t % 16 of rows t / 16 + 16 i
@@ -117,7 +121,7 @@ static hipError_t launch_type(const char* x, int64_t rows, int64_t cols, int64_t
                               float* scale, hipStream_t st) {
   const int64_t x_bytes = x_st * (DT == MISA_T_FP32 ? 4 : 2), across = (cols + 127) / 128;
   if (block_rows == 1)
-    hipLaunchKernelGGL(k_quant_rows<DT>, dim3((unsigned)((rows * across + 15) / 16)), dim3(256), 0, st, x, x_bytes, rows,
+    hipLaunchKernelGGL(k_quant_rows<DT>, dim3((unsigned)((rows * across + 31) / 32)), dim3(256), 0, st, x, x_bytes, rows,
                        cols, (uint32_t)across, codes, scale);
   else
     hipLaunchKernelGGL(k_quant_squares<DT>, dim3((unsigned)((rows + 127) / 128 * across)), dim3(256), 0, st, x, x_bytes,

@@ -1,6 +1,6 @@
 // Tensor arguments of the Python wrappers (module _tensor_args): the pointer of a
 // dense tensor, the pointer and strides of a [tokens, heads, head_dim] or [rows,
-// columns] one, a page pool's, a workspace.  Looked up attribute by attribute from Python, each costs
+// columns] one, a page pool's, a workspace, a new output.  Looked up attribute by attribute from Python, each costs
 // three to four times as much, and a call of a few microseconds checks half a
 // dozen.
 #define PY_SSIZE_T_CLEAN
@@ -182,6 +182,26 @@ PyObject* scratch(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return Py_BuildValue("(NN)", THPVariable_Wrap(t), PyLong_FromVoidPtr(at));
 }
 
+// fresh(shape, dtype, like) -> dense uninitialised tensor on like's device, pointer
+PyObject* fresh(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 3 || !PyTuple_Check(a[0]) || !THPDtype_Check(a[1]) || !THPVariable_Check(a[2])) {
+    PyErr_SetString(PyExc_TypeError, "fresh(shape, dtype, like)");
+    return nullptr;
+  }
+  int64_t size[8];
+  const Py_ssize_t dims = PyTuple_GET_SIZE(a[0]);
+  if (dims > 8) {
+    PyErr_SetString(PyExc_TypeError, "fresh: more than 8 dimensions");
+    return nullptr;
+  }
+  for (Py_ssize_t i = 0; i < dims; ++i) size[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(a[0], i));
+  if (PyErr_Occurred()) return nullptr;
+  const at::Tensor t = at::empty(at::IntArrayRef(size, (size_t)dims), at::TensorOptions().device(THPVariable_Unpack(a[2]).device())
+                                                                          .dtype(reinterpret_cast<THPDtype*>(a[1])->scalar_type));
+  void* const at = t.data_ptr();
+  return Py_BuildValue("(NN)", THPVariable_Wrap(t), PyLong_FromVoidPtr(at));
+}
+
 // Torch throws where a tensor has no pointer, sizes or strides of its own (under
 // vmap, while tracing), and where memory runs out: its Python errors, nothing
 // past this border.
@@ -202,6 +222,8 @@ PyMethodDef methods[] = {
      "pool(pages, heads, head_dim, name, dev): pointer, code type, n_pages, page_keys of a page pool"},
     {"scratch", entry<scratch>(), METH_FASTCALL,
      "scratch(bytes, like): a workspace on like's device, and its pointer"},
+    {"fresh", entry<fresh>(), METH_FASTCALL,
+     "fresh(shape, dtype, like): a dense uninitialised tensor on like's device, and its pointer"},
     {"matrix", entry<matrix>(), METH_FASTCALL,
      "matrix(tensor, dtypes, name, dev, shape=None): pointer and row stride of a [rows, columns] tensor"},
     {"dense", entry<dense>(), METH_FASTCALL,

@@ -149,15 +149,21 @@ def _scratch_py(nbytes, like):
     return t, t.data_ptr()
 
 
+def _fresh_py(shape, dtype, like):
+    """A dense uninitialised tensor on like's device, and its pointer."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    return t, t.data_ptr()
+
+
 try:   # the same in C++ (csrc/tensor_args.cpp): a quarter of the time
-    from ._tensor_args import dense as _dense, matrix as _matrix, pool as _pool, rows as _rows, scratch as _scratch
+    from ._tensor_args import dense as _dense, fresh as _fresh, matrix as _matrix, pool as _pool, rows as _rows, scratch as _scratch
 except ModuleNotFoundError:   # not built yet
-    _dense, _matrix, _pool, _rows, _scratch = _dense_py, _matrix_py, _pool_py, _rows_py, _scratch_py
+    _dense, _fresh, _matrix, _pool, _rows, _scratch = _dense_py, _fresh_py, _matrix_py, _pool_py, _rows_py, _scratch_py
 except ImportError as e:   # built against another torch, say: every call raises, importing and building again do not
     def _dense(*args, why=str(e)):
         raise RuntimeError(f"_tensor_args does not load ({why}): build it again with "
                            "`python -m long_context_sparse_block_amd.build`")
-    _matrix = _pool = _rows = _scratch = _dense
+    _fresh = _matrix = _pool = _rows = _scratch = _dense
 
 
 def _on(stream, t, name, f, *args):
@@ -465,14 +471,17 @@ def misa_plan_tree(parents, q_start, kv_lens, words: int, plan: TreePlan | None 
     _dev(kv_lens, "kv_lens")
     T, n = parents.shape[0], kv_lens.shape[0]
     i32 = torch.int32
-    if plan is None:
-        plan = TreePlan(torch.empty((T, words), dtype=i32, device=parents.device),
-                        torch.empty(T, dtype=i32, device=parents.device))
     args = (n, _dense(parents, i32, (T,), "parents", dev), _dense(q_start, i32, (n + 1,), "q_start", dev),
-            _dense(kv_lens, i32, (n,), "kv_lens", dev), T, words, _dense(plan.mask, i32, (T, words), "mask", dev),
-            _dense(plan.positions, i32, (T,), "positions", dev))
+            _dense(kv_lens, i32, (n,), "kv_lens", dev), T, words)
+    if plan is None:
+        mask, mp = _fresh((T, max(words, 0)), i32, parents)
+        positions, pp = _fresh((T,), i32, parents)
+        plan = TreePlan(mask, positions)
+    else:
+        mp = _dense(plan.mask, i32, (T, words), "mask", dev)
+        pp = _dense(plan.positions, i32, (T,), "positions", dev)
     if T > 0:
-        _call("misa_plan_tree", load().misa_plan_tree, dev, *args)
+        _call("misa_plan_tree", load().misa_plan_tree, dev, *args, mp, pp)
     return plan
 
 
@@ -517,11 +526,13 @@ def misa_keep_path(path, q_start, kv_lens, block_table, k_pages, k_scale_pages=N
     n, most, width = path.shape[0], path.shape[-1], block_table.shape[-1]
     i32 = torch.int32
     if kept_lens is None:
-        kept_lens = torch.empty(n, dtype=i32, device=path.device)
+        kept_lens, kp = _fresh((n,), i32, path)
+    else:
+        kp = _dense(kept_lens, i32, (n,), "kept_lens", dev)
     _call("misa_keep_path", load().misa_keep_path, dev, n, _dense(path, i32, (n, most), "path", dev), most,
           _dense(q_start, i32, (n + 1,), "q_start", dev), _dense(kv_lens, i32, (n,), "kv_lens", dev),
           _dense(block_table, i32, (n, width), "block_table", dev), width, H, D, kpool, vpool, kd, ks, vs, n_pages,
-          page_keys, _dense(kept_lens, i32, (n,), "kept_lens", dev))
+          page_keys, kp)
     return kept_lens
 
 
@@ -539,14 +550,15 @@ def misa_quantize_blocks(x, block_rows: int = 1, codes=None, scale=None, stream=
         raise ValueError(f"block_rows: {block_rows}, expected 1 or 128")
     blocks = (-(-R // block_rows), -(-K // 128))
     if codes is None:
-        codes = torch.empty((R, K), dtype=torch.uint8, device=x.device)
+        codes, cp = _fresh((R, K), torch.uint8, x)
+    else:
+        cp = _dense(codes, codes.dtype if codes.dtype in _CODES else torch.uint8, (R, K), "codes", dev)
     if scale is None:
-        scale = torch.empty(blocks, dtype=torch.float32, device=x.device)
-    args = (at, _DTYPES[x.dtype], R, K, st, block_rows, _dense(codes, codes.dtype if codes.dtype in _CODES else torch.uint8,
-                                                               (R, K), "codes", dev),
-            _dense(scale, torch.float32, blocks, "scale", dev))
+        scale, sp = _fresh(blocks, torch.float32, x)
+    else:
+        sp = _dense(scale, torch.float32, blocks, "scale", dev)
     if R > 0:
-        _call("misa_quantize_blocks", load().misa_quantize_blocks, dev, *args)
+        _call("misa_quantize_blocks", load().misa_quantize_blocks, dev, at, _DTYPES[x.dtype], R, K, st, block_rows, cp, sp)
     return codes, scale
 
 
@@ -568,8 +580,10 @@ def misa_matmul_q8(x, x_scale, w, w_scale, out=None, ws=None, stream=None):
         raise ValueError(f"w: shape {tuple(w.shape)}, expected ({N}, {K})")
     across = (K + 127) // 128
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    op, ost = _matrix(out, _BF16, "out", dev, (M, N))
+        out, op = _fresh((M, N), torch.bfloat16, x)
+        ost = N
+    else:
+        op, ost = _matrix(out, _BF16, "out", dev, (M, N))
     args = (M, N, K, xp, xst, _dense(x_scale, torch.float32, (M, across), "x_scale", dev), wp, wst,
             _dense(w_scale, torch.float32, ((N + 127) // 128, across), "w_scale", dev), op, ost)
     if M == 0:
