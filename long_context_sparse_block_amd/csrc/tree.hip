@@ -5,6 +5,8 @@
 //
 // Both move a few KB: what bounds them is the launch and a chain of dependent
 // loads (lengths, then parents or path and table, then the rows).
+#include <algorithm>
+
 #include "misa_common.h"
 #include "misa_launch.h"
 
@@ -13,7 +15,6 @@ namespace misa {
 namespace {
 constexpr int kPlanThreads = 256;
 constexpr int kLdsNodes = 2048;   // a tree's parents that a workgroup keeps in LDS
-constexpr int kPad = 4096;        // words of padded rows that a workgroup clears
 }  // namespace
 
 // A workgroup takes a sequence, a thread a token: it walks from the token to the root
@@ -25,16 +26,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_tree(int n_seq, const int
                                                             uint32_t* mask, int32_t* positions) {
   __shared__ int s_up[kLdsNodes];
   const int tid = threadIdx.x;
-  if ((int)blockIdx.x >= n_seq) {   // rows of no sequence
+  if ((int)blockIdx.x >= n_seq) {   // rows of no sequence: in front of the first one, behind the last
     const int64_t lo = min(max((int64_t)q_start[0], (int64_t)0), n_tokens);
-    const int64_t hi = min(max((int64_t)q_start[n_seq], lo), n_tokens);
-    const int64_t i0 = (int64_t)(blockIdx.x - n_seq) * kPad, all = n_tokens * words;
-    for (int64_t i = i0 + tid; i < min(i0 + kPad, all); i += kPlanThreads) {
-      const int64_t t = i / words;
-      if (t >= lo && t < hi) continue;
-      mask[i] = 0;
-      if (i - t * words == 0) positions[t] = -1;
-    }
+    const int64_t hi = min(max((int64_t)q_start[n_seq], lo), n_tokens), rows = lo + n_tokens - hi;
+    const int64_t step = (int64_t)(gridDim.x - n_seq) * kPlanThreads, at = (int64_t)(blockIdx.x - n_seq) * kPlanThreads + tid;
+    for (int64_t i = at; i < rows * words; i += step) mask[i < lo * words ? i : i + (hi - lo) * words] = 0;
+    for (int64_t i = at; i < rows; i += step) positions[i < lo ? i : i + (hi - lo)] = -1;
     return;
   }
   const int64_t s = q_start[blockIdx.x], e = q_start[blockIdx.x + 1];
@@ -67,7 +64,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_tree(int n_seq, const int
 
 hipError_t launch_plan_tree(int n_seq, const int32_t* parents, const int32_t* q_start, const int32_t* kv_lens,
                             int64_t n_tokens, int words, uint32_t* mask, int32_t* positions, hipStream_t st) {
-  const int64_t pad = (n_tokens * words + kPad - 1) / kPad;
+  const int64_t pad = std::min<int64_t>(256, (n_tokens * words + 65535) / 65536);   // workgroups for rows of no sequence
   hipLaunchKernelGGL(k_plan_tree, dim3((unsigned)(n_seq + pad)), dim3(kPlanThreads), 0, st, n_seq, parents, q_start,
                      kv_lens, n_tokens, words, mask, positions);
   return hipGetLastError();

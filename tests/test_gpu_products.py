@@ -120,7 +120,7 @@ def test_product_repeats_and_shows_nan():
     assert not torch.isfinite(misa.misa_matmul_q8(x8, xs, w8, ws)[:, :128]).any()
 
 
-@pytest.mark.parametrize("m,n,k", [(4, 128, 8192), (64, 2048, 1024), (300, 300, 4096)])
+@pytest.mark.parametrize("m,n,k", [(4, 128, 8192), (64, 2048, 1024), (300, 300, 4096), (120, 500, 4112)])
 def test_product_in_graphs_and_on_streams(m, n, k):
     ops = operands(9, m, n, k)
     x8, xs, w8, ws = (t.cuda() for t in ops)

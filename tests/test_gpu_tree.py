@@ -37,6 +37,7 @@ PLANS = {
     "past_the_lds": ([2100], "chain", 66, 1, 0),
     "large": ([700, 300], "tree", 23, 9000, 0),
     "many": ([i % 5 for i in range(300)], "tree", 1, 40, 0),
+    "padded_more_than_filled": ([3, 0, 2], "tree", 2, 70000, 9),
 }
 
 
