@@ -87,6 +87,44 @@ __device__ __forceinline__ float sum_halves(float x) {
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
+// The value of lane ^ X (X = 8 .. 1), where it repeats every 2 X lanes of 16 already (X
+// = 8: always): a vector instruction, not a trip through LDS
+template <int X>
+__device__ __forceinline__ int lane_xor(int v) {
+  constexpr int ctrl = X == 8 ? 0x128 : X == 4 ? 0x124 : X == 2 ? 0x4E : 0xB1;   // row_ror 8, 4, quad_perm 2301, 1032
+  return __builtin_amdgcn_update_dpp(0, v, ctrl, 0xF, 0xF, true);
+}
+template <int X>
+__device__ __forceinline__ float lane_xor(float v) { return __int_as_float(lane_xor<X>(__float_as_int(v))); }
+// Over all lanes of a wave, in the order 32, 16, 8, 4, 2, 1 apart
+template <typename T, typename F>
+__device__ __forceinline__ T reduce_wave(T v, F f) {
+  auto other = [](T x, bool half) __attribute__((always_inline)) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    // (both halves, or rows of 16, of a swap of x with itself: x's own and the other's)
+    const auto s = half ? __builtin_amdgcn_permlane32_swap(u, u, false, false) : __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return s;
+  };
+  auto s = other(v, true);
+  v = f(__builtin_bit_cast(T, (uint32_t)s[0]), __builtin_bit_cast(T, (uint32_t)s[1]));
+  s = other(v, false);
+  v = f(__builtin_bit_cast(T, (uint32_t)s[0]), __builtin_bit_cast(T, (uint32_t)s[1]));
+  v = f(v, lane_xor<8>(v));
+  v = f(v, lane_xor<4>(v));
+  v = f(v, lane_xor<2>(v));
+  return f(v, lane_xor<1>(v));
+}
+// Sums of a wave's lanes up to each
+__device__ __forceinline__ int scan_wave(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row 0's and 2's last lane to the next row
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // lane 31 to the upper half
+  return v;
+}
+
 // Entry of the block table for token t of sequence b (entries clamped, see
 // misa_kv_pages), and the pool row it makes
 __device__ __forceinline__ int table_entry(const AttnArgs& a, int b, int t) {
@@ -261,9 +299,11 @@ __device__ __forceinline__ int wave_per(const DenseScan& w, const AttnLaunch& L,
 // CU's time.  g is exact where the units are about equally long (one chunk, a
 // batch of equal ones); else the remainders count as half a split a unit, and
 // the CUs even out but for half a split.
+// A lane weighs a cut: one after the other, every workgroup spent some 600
+// instructions on them (9 trees of 1 to 257 tokens: 65.1 us, so 63.8).
 constexpr int kCuts = 9;
 template <int D>
-__device__ __forceinline__ int tile_per(const DenseScan& w, const AttnLaunch& L, int kv_heads) {
+__device__ __forceinline__ int tile_per(const DenseScan& w, const AttnLaunch& L, int kv_heads, int lane) {
   constexpr int cut[kCuts] = {1, 2, 3, 4, 5, 6, 8, 14, 32};
   constexpr float start = D == 64 ? 4.f : 1.6f, cus = 256.f, held = D == 64 ? 3.f : 2.f;
   constexpr float one = D == 64 ? 1 / 0.45f : 1 / 0.7f, two = D == 64 ? 2 / 0.8f : 2.f;   // tiles' time beside 1, 2
@@ -271,27 +311,30 @@ __device__ __forceinline__ int tile_per(const DenseScan& w, const AttnLaunch& L,
   const float heads = (float)kv_heads, longest = (float)w.longest, units = (float)w.units * heads;
   const float fair = w.steps * heads / cus;
   const bool alike = w.steps > 0.9f * (float)w.units * longest;
-  float best = longest, lowest = INFINITY;
+  float part = 1.f;
 #pragma unroll
-  for (int j = 0; j < kCuts; ++j) {
-    const float per = fminf(longest, fmaxf((float)least, ceilf(longest * (1.f / cut[j]) - 1e-3f)));
-    const float inv = 1.f / fmaxf(per, 1.f);
-    float g, cost;
-    if (alike) {
-      g = units * ceilf(longest * inv - 1e-3f);
-      const float m = ceilf(g * (1.f / cus)), full = held * floorf(m * (1.f / held) + 1e-3f), rest = m - full;
-      cost = (full + (rest < 0.5f ? 0.f : rest < 1.5f ? one : two)) * (per + start);
-    } else {
-      g = j == 0 ? units : w.steps * heads * inv + 0.5f * units;
-      cost = fmaxf(fair + g * (start / cus) + 0.5f * per, one * (per + start));
-    }
-    if (per < longest) cost += g * 0.01f + start;
-    if (cost < lowest) {
-      lowest = cost;
-      best = per;
-    }
+  for (int j = 1; j < kCuts; ++j) part = lane == j ? 1.f / cut[j] : part;
+  const float per = fminf(longest, fmaxf((float)least, ceilf(longest * part - 1e-3f)));
+  const float inv = 1.f / fmaxf(per, 1.f);
+  float g, cost;
+  if (alike) {
+    g = units * ceilf(longest * inv - 1e-3f);
+    const float m = ceilf(g * (1.f / cus)), full = held * floorf(m * (1.f / held) + 1e-3f), rest = m - full;
+    cost = (full + (rest < 0.5f ? 0.f : rest < 1.5f ? one : two)) * (per + start);
+  } else {
+    g = lane == 0 ? units : w.steps * heads * inv + 0.5f * units;
+    cost = fmaxf(fair + g * (start / cus) + 0.5f * per, one * (per + start));
   }
-  return __builtin_amdgcn_readfirstlane((int)best);
+  if (per < longest) cost += g * 0.01f + start;
+  // the cut of least cost, the first of equal ones (no cost: the whole unit)
+  cost = lane < kCuts ? cost : INFINITY;
+  float lowest = fminf(cost, lane_xor<8>(cost));
+  lowest = fminf(lowest, lane_xor<4>(lowest));
+  lowest = fminf(lowest, lane_xor<2>(lowest));
+  lowest = fminf(lowest, lane_xor<1>(lowest));
+  const uint64_t best = __ballot(lane < kCuts && cost == lowest && cost < INFINITY);
+  if (best == 0) return __builtin_amdgcn_readfirstlane((int)longest);
+  return __builtin_amdgcn_readlane((int)per, (int)__builtin_ctzll(best));
 }
 
 // Key tiles of each of a unit's splits (the last may have fewer), n in all
@@ -340,12 +383,7 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, const AttnLaunch& L
     units += sum;
     int src = -1, i = 0, left = 0;
     if (TILES) {
-      int inc = sum;
-#pragma unroll
-      for (int o = 1; o < kWave; o <<= 1) {
-        const int x = __shfl_up(inc, o);
-        if (lane >= o) inc += x;
-      }
+      const int inc = scan_wave(sum);
       const int total = __builtin_amdgcn_readlane(inc, 63);
       if (!found && unit < base + total) {
         const int rel = (int)(unit - base);
@@ -390,14 +428,11 @@ __device__ __forceinline__ bool find_unit(const AttnArgs& a, const AttnLaunch& L
   }
   if (!found) return false;
   if (sums) {
-#pragma unroll
-    for (int x = 32; x >= 1; x >>= 1) {
-      steps += __shfl_xor(steps, x);
-      longest = max(longest, __shfl_xor(longest, x));
-      units += __shfl_xor(units, x);
-    }
+    steps = reduce_wave(steps, [](float x, float y) __attribute__((always_inline)) { return x + y; });
+    longest = reduce_wave(longest, [](int x, int y) __attribute__((always_inline)) { return max(x, y); });
+    units = reduce_wave(units, [](int x, int y) __attribute__((always_inline)) { return x + y; });
     *scan = DenseScan{steps, units, longest, 0};
-    scan->per = TILES ? tile_per<D>(*scan, L, a.n_kv_heads) : wave_per(*scan, L, a.n_kv_heads);
+    scan->per = TILES ? tile_per<D>(*scan, L, a.n_kv_heads, lane) : wave_per(*scan, L, a.n_kv_heads);
   } else {
     *scan = DenseScan{0.f, 0, 0, 0};
   }
