@@ -44,6 +44,28 @@ def test_quantize(rows, cols, block_rows, dtype):
     assert torch.equal(a.view(torch.uint8).cpu(), codes) and torch.equal(b.cpu(), scale)
 
 
+def test_quantize_borders():
+    """Quotients on and next to the borders between codes, in fp32 and at scales from the least to the largest: every
+    code is that of the correctly rounded quotient."""
+    g = torch.Generator().manual_seed(21)
+    border = torch.cat([torch.arange(8, 16) + 0.5, torch.arange(16) + 0.5])   # of mantissas 1.xxx, and below the least
+    rows = []
+    for e in list(range(-125, 118, 9)) + [-80, -81, -79, 119, 120]:
+        top = (1 + torch.rand(8, generator=g)) * 2.0 ** min(e + 8, 127)
+        s = top / torch.full_like(top, 448)
+        k = border[torch.randint(0, 24, (8, 127), generator=g)] * 2.0 ** torch.randint(-10, 5, (8, 127), generator=g)
+        x = (k * s[:, None]).clamp(max=top.amax().item())
+        x = x.view(torch.int32) + torch.randint(-2, 3, x.shape, generator=g).to(torch.int32)   # a few steps beside
+        x = x.view(torch.float32).abs().minimum(top[:, None]) * (torch.randint(0, 2, x.shape, generator=g) * 2 - 1)
+        rows.append(torch.cat([top[:, None], x], 1))
+    x = torch.cat(rows)
+    x[3, 5], x[4, 6] = -0.0, 0.0
+    codes, scale = th.quantize(x, 1)
+    got, s = misa.misa_quantize_blocks(x.cuda())
+    assert torch.equal(s.cpu(), scale)
+    assert torch.equal(got.cpu(), codes)
+
+
 @pytest.mark.parametrize("block_rows", [1, 128])
 def test_quantize_extremes(block_rows):
     """Tiny values (scales at their least), the largest, NaN and infinities."""
