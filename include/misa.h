@@ -736,9 +736,10 @@ misa_status misa_quantize_blocks(const void* x, misa_dtype dtype, int64_t rows, 
  * in bytes and multiples of 16, rows 16-byte aligned.  x_scale: float
  * [m][ceil(k / 128)], w_scale: float [ceil(n / 128)][ceil(k / 128)], dense.  out:
  * bf16 [m][n], row stride out_stride >= n (elements), overlapping no input.
- * A block's sum is formed by the matrix units (about 2^-14 of sum |x w| of the
- * block off), scaled and added up in fp32; out is rounded once.  The order of the sums is
- * fixed: the same call gives the same bits.  NaN codes and scales show in the
+ * A block's sum is formed by the matrix units, which cut each product at 2^-13 of the
+ * largest of the eight (columns 8 c .. 8 c + 7) that it is summed with first, and is scaled
+ * and added up in fp32; out is rounded once.  The order of the sums is fixed: the same
+ * call gives the same bits.  NaN codes and scales show in the
  * rows and columns that they are in.
  * k: a multiple of 16, up to 2^20 (else MISA_ERR_UNSUPPORTED).
  * ws: misa_matmul_q8_workspace_bytes() bytes (16-byte aligned; may be NULL when

@@ -126,6 +126,20 @@ def test_product(m, n, k):
     assert (out[m:] == 7).all() and (out[:, :3] == 7).all() and (out[:, 3 + n:] == 7).all()
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 40, 1024), (16, 64, 128), (40, 300, 528), (100, 300, 1024), (515, 300, 272)])
+def test_product_of_terms_that_cancel(m, n, k):
+    """Rows whose second half cancels the first in another order, over values of very different sizes: what is left is
+    some 10^-4 of the terms."""
+    g = torch.Generator().manual_seed(m + k)
+    x, w = ((torch.randn((r, k), generator=g) * torch.exp(2 * torch.randn((r, k), generator=g))).clamp(-440, 440) for r in (m, n))
+    x8, w8 = x.to(FP8).view(torch.uint8), w.to(FP8).view(torch.uint8)
+    order = torch.randperm(k // 2, generator=g)
+    x8[:, k // 2:], w8[:, k // 2:] = x8[:, :k // 2][:, order], (w8[:, :k // 2] ^ 0x80)[:, order]
+    x8[:, 0] = 0x30
+    ones = torch.ones((m, -(-k // 128))), torch.ones((-(-n // 128), -(-k // 128)))
+    th.check_product(misa.misa_matmul_q8(x8.cuda(), ones[0].cuda(), w8.cuda(), ones[1].cuda()), x8, ones[0], w8, ones[1])
+
+
 def test_product_repeats_and_shows_nan():
     m, n, k = 70, 300, 1040
     ops = operands(8, m, n, k)

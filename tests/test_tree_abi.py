@@ -1,6 +1,8 @@
 """The drafted trees' calls and the e4m3 products on the CPU: every refusal of the C ABI happens on the host before
 anything is enqueued, and the Python wrappers check their arguments."""
 import ctypes
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -131,3 +133,17 @@ def test_helpers_agree_on_a_tree_by_hand():
     assert pack(sees, 1).flatten().tolist() == [1, 3, 5, 11, 27, 32, 64]
     assert (unpack(pack(sees, 2))[:, :7].numpy() == sees).all()
     assert pack(ancestors([i - 1 for i in range(33)]), 2)[32].tolist() == [-1, 1]
+
+
+@pytest.mark.parametrize("tensor", ["vmap", "sparse", "symbolic"])
+@pytest.mark.parametrize("call", ["serving._matrix(x.select(1, 0), (torch.float32,), 'x', 0)",
+                                  "serving._fresh((-5, 2), torch.float32, x)"])
+def test_errors_of_torch_stay_errors(call, tensor):
+    """As tests/test_serving_args.py has it for the other checks: a C++ exception that passes their border would end the
+    process."""
+    from test_serving_args import PROGRAM, ROOT, TENSORS
+    r = subprocess.run([sys.executable, "-W", "ignore", "-c", PROGRAM.format(call=call, tensor=TENSORS[tensor])], cwd=ROOT,
+                       capture_output=True, text=True, timeout=120)
+    print(r.stdout, r.stderr[-500:])
+    assert r.returncode == 0
+    assert r.stdout.startswith("raised")

@@ -5,7 +5,6 @@ import math
 import numpy as np
 import torch
 
-from gpu_helpers import EPS_F8
 from serving_helpers import BF16_HALF, F32_HALF
 
 FP8 = torch.float8_e4m3fn
@@ -166,12 +165,25 @@ def values(codes, scale, block_rows):
 
 
 def product(x8, xs, w8, ws):
-    """out (fp64) and the bound on the kernel's error: half a bf16 step of the result, the matrix unit's own error of a
-    block's sum (at most 2^-12 of the sum of |x w|, gpu_helpers.EPS_F8), and in fp32 the product of two scales, the
-    scaled addition of each of the blocks, and its rounding: (blocks + 3) 2^-24 of that sum."""
+    """out (fp64) and the bound on the kernel's error.  The matrix unit sums eight neighbouring products at a time, each
+    cut (towards 0) at 2^-13 of the power of two in the largest of the eight, which itself keeps all its 8 bits: 7 x
+    2^-13 of the largest, at most, for each eight (measured: +1, -1 in another eight and 2^-13 beside the first leave
+    2^-13, with 2^-14 nothing).  Beside that the sums of the eights, the product of two scales and the scaled addition of
+    each block in fp32, (16 + blocks + 3) 2^-24 of the sum of |x w|, and half a bf16 step of the result."""
     x, w = values(x8, xs, 1), values(w8, ws, 128)
     ref, mag = x @ w.T, x.abs() @ w.abs().T
-    tol = BF16_HALF * ref.abs() + (EPS_F8 + (xs.shape[1] + 3) * F32_HALF) * mag * 1.01
+    m, k = x.shape
+    if m * k * w.shape[0] <= 1 << 27:
+        top = torch.zeros_like(ref)
+        for g in range(0, k, 8):
+            most = torch.zeros_like(ref, dtype=torch.float32)
+            for i in range(g, g + 8):
+                torch.maximum(most, x[:, i, None].abs().float() * w[None, :, i].abs().float(), out=most)
+            top += most.double()
+        top *= 1 + 2.0 ** -20
+    else:
+        top = mag   # (the largest of eight is at most their sum)
+    tol = BF16_HALF * ref.abs() + (7 * 2.0 ** -13 * top + (xs.shape[1] + 19) * F32_HALF * mag) * 1.01
     return ref, tol
 
 
