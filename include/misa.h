@@ -674,8 +674,9 @@ misa_status misa_plan_tree(int32_t n_seq, const int32_t* parents, const int32_t*
  * kv_lens[b] - m cached tokens, and new token j where bit j of its mask row is
  * set and j < m (any bits: the mask need not come from misa_plan_tree).  The
  * mask is read for the rows of sequences only.  A row that sees nothing gives
- * out = 0, lse = -inf.  All else is as in misa_attention_paged, workspace and
- * limits too; NaN and infinity in a value among a sequence's new tokens may reach
+ * out = 0, lse = -inf.  All else is as in misa_attention_paged, its limits too
+ * (where no sequence may have more than 64 rows of a kv head, chunks' workgroups take
+ * 64); ws: misa_attention_tree_workspace_bytes() bytes.  NaN and infinity in a value among a sequence's new tokens may reach
  * others of its new tokens, never another sequence.
  * mask: uint32 [n_tokens][words], 1 <= words <= 1024 (MISA_ERR_UNSUPPORTED past it).
  */

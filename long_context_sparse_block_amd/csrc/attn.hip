@@ -12,7 +12,7 @@
 
 namespace misa {
 
-hipError_t launch_attn_tile(const AttnArgs& a, const AttnLaunch& L, int D, bool fp8, int NW, hipStream_t st);
+hipError_t launch_attn_tile(const AttnArgs& a, const AttnLaunch& L, int D, bool fp8, int NW, bool halves, hipStream_t st);
 hipError_t launch_attn_wave(const AttnArgs& a, const AttnLaunch& L, int D, bool fp8, int RT, hipStream_t st);
 
 namespace {
@@ -97,6 +97,8 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a, const AttnL
 struct AttnPlan {
   int RT = 0, wave_units = 0, wave_splits = 1, wave_slots = 0;   // RT = 0: attn_wave does not run
   int NW = 0, tile_units = 0, tile_splits = 1, tile_slots = 0;   // NW = 0: attn_tile does not run
+  int BM = 0;            // rows of an attn_tile unit
+  bool halves = false;   // its waves: two for each 32 rows
   int rows_min = 0;
   int64_t wave_part = 0, tile_part = 0;   // rows of a kv head's part, a split
   size_t wave_o = 0, wave_ml = 0, wave_info = 0, tile_o = 0, tile_ml = 0, tile_info = 0, total = 0;
@@ -132,7 +134,7 @@ int choose_splits(int64_t units, int64_t slots, int64_t steps, int most, bool ex
   return best;
 }
 
-AttnPlan make_plan(const misa_attn_shape& s, const misa_kv_pages& pg, int topk) {
+AttnPlan make_plan(const misa_attn_shape& s, const misa_kv_pages& pg, int topk, bool tree) {
   AttnPlan p;
   const int64_t G = s.n_heads / s.n_kv_heads, T = s.n_tokens, KH = s.n_kv_heads;
   const int64_t ctx = topk > 0 ? topk : pg.max_pages * pg.page_keys;
@@ -144,7 +146,8 @@ AttnPlan make_plan(const misa_attn_shape& s, const misa_kv_pages& pg, int topk) 
       wave_units = T;
     } else {
       p.NW = G <= 64 ? 2 : 4;
-      tile_units = T * ((G + p.NW * 32 - 1) / (p.NW * 32));
+      p.BM = p.NW * 32;
+      tile_units = T * ((G + p.BM - 1) / p.BM);
     }
   } else {
     const int64_t new_max = s.max_new > 0 ? std::min<int64_t>(s.max_new, T) : T;
@@ -154,7 +157,9 @@ AttnPlan make_plan(const misa_attn_shape& s, const misa_kv_pages& pg, int topk) 
     } else {
       // one sequence of many rows needs attn_tile alone
       if (s.n_seq > 1 && G <= 32) p.RT = G <= 16 ? 1 : 2;
-      p.NW = rows <= 64 ? 2 : 4;
+      p.halves = tree && rows <= 64;   // (a chunk keeps its two waves, and with them the order of its sums)
+      p.NW = rows <= 64 && !p.halves ? 2 : 4;
+      p.BM = p.halves ? 64 : p.NW * 32;
     }
     p.rows_min = 16 * p.RT;
     if (p.RT > 0) wave_units = s.n_seq;
@@ -163,7 +168,7 @@ AttnPlan make_plan(const misa_attn_shape& s, const misa_kv_pages& pg, int topk) 
       // ends at once, but the one dispatched after it shares a CU: one unit too many of three cost 64 tokens over 8192 keys
       // 32.1 us instead of 26.7.)
       const int64_t n = std::min<int64_t>(s.n_seq, T * G / (p.rows_min + 1));
-      tile_units = (T * G - n) / (p.NW * 32) + n;
+      tile_units = (T * G - n) / p.BM + n;
     }
   }
   p.groups = std::max(wave_units, tile_units) * KH;
@@ -175,7 +180,7 @@ AttnPlan make_plan(const misa_attn_shape& s, const misa_kv_pages& pg, int topk) 
     p.wave_splits = choose_splits(wave_units * KH, p.wave_slots, (ctx + 127) / 128, 64, topk > 0);
   }
   if (p.NW > 0) {
-    const int64_t BM = p.NW * 32;
+    const int64_t BM = p.BM;
     const int64_t est = topk > 0 ? tile_units : (T * G + BM - 1) / BM;
     p.tile_slots = s.head_dim == 64 ? 768 : 512;   // LDS, and registers at head_dim 64
     p.tile_splits = choose_splits(est * KH, p.tile_slots, (ctx + 63) / 64, 32, topk > 0);
@@ -184,7 +189,7 @@ AttnPlan make_plan(const misa_attn_shape& s, const misa_kv_pages& pg, int topk) 
   size_t off = 0;
   // (see AttnLaunch)
   p.wave_part = (int64_t)p.wave_units * 16 * p.RT;
-  p.tile_part = (int64_t)p.tile_units * 32 * p.NW;
+  p.tile_part = (int64_t)p.tile_units * p.BM;
   if (topk == 0) {
     p.wave_part = std::min<int64_t>(T * G, p.wave_part);
     p.tile_part = std::min<int64_t>(T * G, p.tile_part);
@@ -213,18 +218,18 @@ AttnPlan make_plan(const misa_attn_shape& s, const misa_kv_pages& pg, int topk) 
 
 }  // namespace
 
-bool attn_fits(const misa_attn_shape& s, const misa_kv_pages& pg, int topk) {
-  return make_plan(s, pg, topk).groups <= ((int64_t)1 << 23);
+bool attn_fits(const misa_attn_shape& s, const misa_kv_pages& pg, int topk, bool tree) {
+  return make_plan(s, pg, topk, tree).groups <= ((int64_t)1 << 23);
 }
 
-size_t attn_workspace_bytes(const misa_attn_shape& s, const misa_kv_pages& pg, int topk) {
-  return make_plan(s, pg, topk).total;
+size_t attn_workspace_bytes(const misa_attn_shape& s, const misa_kv_pages& pg, int topk, bool tree) {
+  return make_plan(s, pg, topk, tree).total;
 }
 
 hipError_t launch_attention(const misa_attn_shape& s, const misa_kv_pages& pg, const uint16_t* q,
                             const int32_t* q_start, const int32_t* kv_lens, const int32_t* idx, int topk,
                             const uint32_t* tree, int tree_words, uint16_t* out, float* lse, void* ws, hipStream_t st) {
-  const AttnPlan p = make_plan(s, pg, topk);
+  const AttnPlan p = make_plan(s, pg, topk, tree != nullptr);
   const bool pow2 = (pg.page_keys & (pg.page_keys - 1)) == 0;
   const AttnArgs a{q, s.q_stride_token, s.q_stride_head, pg.k, pg.v, pg.k_scale, pg.v_scale, pg.block_table,
                    pg.max_pages, (int)pg.n_pages, pg.page_keys, pow2 ? __builtin_ctz((unsigned)pg.page_keys) : -1, q_start,
@@ -233,17 +238,17 @@ hipError_t launch_attention(const misa_attn_shape& s, const misa_kv_pages& pg, c
   const bool fp8 = pg.kdtype == MISA_K_FP8_E4M3;
   char* base = static_cast<char*>(ws);
   const int64_t all = s.n_tokens * (s.n_heads / s.n_kv_heads);   // rows of a kv head
-  const AttnLaunch T{p.tile_units, p.tile_splits, p.tile_slots, p.rows_min, 32 * p.NW, p.tile_part == all, p.tile_part,
+  const AttnLaunch T{p.tile_units, p.tile_splits, p.tile_slots, p.rows_min, p.BM, p.tile_part == all, p.tile_part,
                      reinterpret_cast<float*>(base + p.tile_o), reinterpret_cast<float2*>(base + p.tile_ml),
                      reinterpret_cast<int4*>(base + p.tile_info)};
   const AttnLaunch W{p.wave_units, p.wave_splits, p.wave_slots, p.rows_min, 16 * p.RT, p.wave_part == all, p.wave_part,
                      reinterpret_cast<float*>(base + p.wave_o), reinterpret_cast<float2*>(base + p.wave_ml),
                      reinterpret_cast<int4*>(base + p.wave_info)};
   hipError_t e = hipSuccess;
-  if (p.NW > 0) e = launch_attn_tile(a, T, s.head_dim, fp8, p.NW, st);
+  if (p.NW > 0) e = launch_attn_tile(a, T, s.head_dim, fp8, p.NW, p.halves, st);
   if (e == hipSuccess && p.RT > 0) e = launch_attn_wave(a, W, s.head_dim, fp8, p.RT, st);
   const int lanes = s.head_dim / 4;   // of a row
-  const int64_t n_tile = p.NW > 0 && p.tile_splits > 1 ? (int64_t)p.tile_units * s.n_kv_heads * p.NW * 32 * lanes / 256 : 0;
+  const int64_t n_tile = p.NW > 0 && p.tile_splits > 1 ? (int64_t)p.tile_units * s.n_kv_heads * p.BM * lanes / 256 : 0;
   const int64_t n_wave = p.RT > 0 && p.wave_splits > 1 ? (int64_t)p.wave_units * s.n_kv_heads * p.RT * 16 * lanes / 256 : 0;
   if (e != hipSuccess || n_tile + n_wave == 0) return e;
   const dim3 grid((unsigned)(n_tile + n_wave));

@@ -42,10 +42,19 @@ struct Fp8Stage {
 };
 }  // namespace
 
-template <int D, bool FP8, AttnMode MODE, int NW>
+// HALVES (trees of at most 64 rows a kv head): the four waves are two for each 32
+// rows, one for each half of a tile's keys, and join at the end.  Over e4m3
+// pages two waves leave one on a SIMD, which then waits for its own loads (47% of
+// its time, matrix unit 19%): 64 trees of 16 tokens over 16K keys, 32 / 8 heads of
+// 128, 597 -> 461 us, heads of 64 365 -> 325; one tree of 16 over 32K 49 -> 34.  Over bf16
+// pages, bound by loads, 662 -> 654, and one tree of 12 over 8K 21.5 -> 19.6.
+// 64 trees of 12, heads of 64, e4m3 (a quarter of the rows empty): 324 -> 335.
+template <int D, bool FP8, AttnMode MODE, int NW, bool HALVES>
 __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const AttnArgs a, const AttnLaunch L) {
   constexpr bool SEL = MODE == kSelected, TREE = MODE == kTree;
-  constexpr int NT = NW * kWave, BM = NW * 32;
+  constexpr int NT = NW * kWave, BM = HALVES ? 64 : NW * 32;
+  constexpr int KB = HALVES ? 1 : 2;   // blocks of 32 keys of a tile that a wave takes
+  static_assert(!HALVES || NW == 4, "two waves for each 32 rows");
   constexpr int RB = D * 2;            // bytes of a bf16 row
   constexpr int P = D / 8;             // its 16-byte pieces
   constexpr int RPI = kWave / P;       // rows of one wave-wide 16-byte load
@@ -114,7 +123,8 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
   }
 
   // this lane's query row (rows past the end repeat the last one and are not written)
-  const int r = r0 + wave * 32 + c32;
+  const int rw = HALVES ? wave & 1 : wave, half = HALVES ? wave >> 1 : 0;   // its rows, its keys
+  const int r = r0 + rw * 32 + c32;
   const bool live = r < nrows;
   const int rc = min(r, nrows - 1);
   const int qi = SEL ? 0 : rc / G, qh = g * G + (SEL ? rc : rc - qi * G);
@@ -215,34 +225,38 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
 
   auto compute = [&](const unsigned char* sk, const unsigned char* sv, const float* sks, const float* svs, int jt,
                      uint64_t mask) __attribute__((always_inline)) {
-    f32x16 s[2];
+    const int key0 = half * 32;   // the wave's first key of the tile
+    sk += key0 * RB;
+    sv += key0 * RB;
+    f32x16 s[KB];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[kb][e] = 0.f;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
+      for (int kb = 0; kb < KB; ++kb) {
         const bf16x8 kf = as_bf16x8(*reinterpret_cast<const uint4*>(sk + kb * 32 * RB + (k_base ^ (ks << 5))));
         s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[ks], s[kb], 0, 0, 0);
       }
     }
     // six reads ahead of the products (left alone, the compiler waits for each)
-    __builtin_amdgcn_sched_group_barrier(kDsRead, 6, 0);
+    constexpr int kAhead = KB * KS < 6 ? KB * KS : 6;
+    __builtin_amdgcn_sched_group_barrier(kDsRead, kAhead, 0);
 #pragma unroll
-    for (int i = 0; i < 2 * KS - 6; ++i) {
+    for (int i = 0; i < KB * KS - kAhead; ++i) {
       __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
       __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(kMfma, 6, 0);
-    // key of s[kb][4 j + i]: kb 32 + 8 j + 4 h + i
+    __builtin_amdgcn_sched_group_barrier(kMfma, kAhead, 0);
+    // key of s[kb][4 j + i]: key0 + kb 32 + 8 j + 4 h + i
     if constexpr (FP8) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const f32x4 w = *reinterpret_cast<const f32x4*>(sks + kb * 32 + 8 * j + 4 * h);
+          const f32x4 w = *reinterpret_cast<const f32x4*>(sks + key0 + kb * 32 + 8 * j + 4 * h);
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[kb][4 * j + i] *= w[i];
         }
@@ -251,34 +265,34 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
       if (mask != ~0ull) {
         const uint32_t mw[2] = {(uint32_t)mask >> (4 * h), (uint32_t)(mask >> 32) >> (4 * h)};
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             if (!((mw[kb] >> (8 * (e >> 2) + (e & 3))) & 1)) s[kb][e] = -INFINITY;
       }
     } else if (TREE) {
       if ((jt + 1) * kBN > kfull) {
-        uint32_t mw[2];
-        tree_bits<2>(a, qrow, (int)(jt * kBN - pos0), mw);
+        uint32_t mw[KB];
+        tree_bits<KB>(a, qrow, (int)(jt * kBN + key0 - pos0), mw);
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          mw[kb] = (mw[kb] & low_bits(kend - jt * kBN - kb * 32)) >> (4 * h);
+        for (int kb = 0; kb < KB; ++kb) {
+          mw[kb] = (mw[kb] & low_bits(kend - jt * kBN - key0 - kb * 32)) >> (4 * h);
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             if (!((mw[kb] >> (8 * (e >> 2) + (e & 3))) & 1)) s[kb][e] = -INFINITY;
         }
       }
     } else if ((jt + 1) * kBN > kfull) {
-      const int lim = vis - jt * kBN - 4 * h;   // the row sees the tile's keys below this
+      const int lim = vis - jt * kBN - key0 - 4 * h;   // the row sees the tile's keys below this
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           if (kb * 32 + 8 * (e >> 2) + (e & 3) >= lim) s[kb][e] = -INFINITY;
     }
     float top = s[0][0];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int e = 0; e < 16; ++e) top = fmaxf(top, s[kb][e]);
     top = max_halves(top) * sc;
@@ -293,9 +307,9 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
         for (int e = 0; e < 16; ++e) o[i][e] *= keep;
     }
     const float mu = m == -INFINITY ? 0.f : m;
-    bf16x8 pf[4];
+    bf16x8 pf[2 * KB];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int kb = 0; kb < KB; ++kb) {
       float p[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) p[e] = exp2_raw(__builtin_fmaf(s[kb][e], sc, -mu));
@@ -306,7 +320,7 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
       if constexpr (FP8) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const f32x4 w = *reinterpret_cast<const f32x4*>(svs + kb * 32 + 8 * j + 4 * h);
+          const f32x4 w = *reinterpret_cast<const f32x4*>(svs + key0 + kb * 32 + 8 * j + 4 * h);
 #pragma unroll
           for (int i = 0; i < 4; ++i) p[4 * j + i] *= w[i];
         }
@@ -318,7 +332,7 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < 2 * KB; ++t) {
 #pragma unroll
       for (int db = 0; db < DB; ++db) {
         const int x = (db ^ vx) << 6;
@@ -328,7 +342,7 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
     }
     __builtin_amdgcn_sched_group_barrier(kDsRead, 8, 0);
 #pragma unroll
-    for (int i = 0; i < 4 * DB - 4; ++i) {
+    for (int i = 0; i < 2 * KB * DB - 4; ++i) {
       __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
       __builtin_amdgcn_sched_group_barrier(kDsRead, 2, 0);
     }
@@ -413,6 +427,32 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
   }
 
   l = sum_halves(l);
+  if constexpr (HALVES) {
+    // The second half's waves onto the first's, relative to the joint maximum
+    static_assert(4 * DB * kWave * sizeof(f32x4) <= sizeof(s_k0), "a wave's sums fit a tile");
+    __syncthreads();   // nobody reads tiles any more
+    f32x4* const so = reinterpret_cast<f32x4*>(rw == 0 ? s_k0 : s_k1);   // [4 DB][lane]
+    float2* const sml = reinterpret_cast<float2*>(s_v0) + rw * kWave;
+    if (half == 1) {
+#pragma unroll
+      for (int i = 0; i < 4 * DB; ++i)
+        so[i * kWave + lane] = f32x4{o[i / 4][4 * (i % 4)], o[i / 4][4 * (i % 4) + 1], o[i / 4][4 * (i % 4) + 2], o[i / 4][4 * (i % 4) + 3]};
+      sml[lane] = make_float2(m, l);
+    }
+    __syncthreads();
+    if (half == 1) return;
+    const float2 other = sml[lane];
+    const float mn = fmaxf(m, other.x);
+    const float f0 = m == -INFINITY ? 0.f : exp2_raw(m - mn), f1 = other.x == -INFINITY ? 0.f : exp2_raw(other.x - mn);
+    m = mn;
+    l = l * f0 + other.y * f1;
+#pragma unroll
+    for (int i = 0; i < 4 * DB; ++i) {
+      const f32x4 x = so[i * kWave + lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i / 4][4 * (i % 4) + e] = __builtin_fmaf(o[i / 4][4 * (i % 4) + e], f0, x[e] * f1);
+    }
+  }
   // o[db][4 j + i] of the lane: element db 32 + 8 j + 4 h + i of row r
   if (in_use == 1) {
     if (!live) return;
@@ -429,7 +469,7 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
   }
   if (!live) return;
   const PartPlace part = part_place<SEL>(L, a.n_kv_heads, G, BM, g, unit, tok0, r0, nrows);
-  const int64_t pr = part.begin + split * part.step + wave * 32 + c32;
+  const int64_t pr = part.begin + split * part.step + rw * 32 + c32;
   if (h == 0) L.part_ml[pr] = make_float2(m, l);
   if (l != 0.f) {
 #pragma unroll
@@ -442,25 +482,29 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
 }
 
 template <int D, bool FP8, AttnMode MODE>
-static hipError_t launch_nw(const AttnArgs& a, const AttnLaunch& L, int NW, hipStream_t st) {
+static hipError_t launch_nw(const AttnArgs& a, const AttnLaunch& L, int NW, bool halves, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)L.n_units * L.n_splits * a.n_kv_heads));
-  if (NW == 2) hipLaunchKernelGGL((k_attn_tile<D, FP8, MODE, 2>), grid, dim3(128), 0, st, a, L);
-  else hipLaunchKernelGGL((k_attn_tile<D, FP8, MODE, 4>), grid, dim3(256), 0, st, a, L);
+  if constexpr (MODE == kTree) {
+    if (halves) hipLaunchKernelGGL((k_attn_tile<D, FP8, MODE, 4, true>), grid, dim3(256), 0, st, a, L);
+    else hipLaunchKernelGGL((k_attn_tile<D, FP8, MODE, 4, false>), grid, dim3(256), 0, st, a, L);
+    return hipGetLastError();
+  } else if (NW == 2) hipLaunchKernelGGL((k_attn_tile<D, FP8, MODE, 2, false>), grid, dim3(128), 0, st, a, L);
+  else hipLaunchKernelGGL((k_attn_tile<D, FP8, MODE, 4, false>), grid, dim3(256), 0, st, a, L);
   return hipGetLastError();
 }
 
 template <int D, bool FP8>
-static hipError_t launch_mode(const AttnArgs& a, const AttnLaunch& L, int NW, hipStream_t st) {
+static hipError_t launch_mode(const AttnArgs& a, const AttnLaunch& L, int NW, bool halves, hipStream_t st) {
   switch (mode_of(a)) {
-    case kSelected: return launch_nw<D, FP8, kSelected>(a, L, NW, st);
-    case kTree: return launch_nw<D, FP8, kTree>(a, L, NW, st);
-    default: return launch_nw<D, FP8, kCausal>(a, L, NW, st);
+    case kSelected: return launch_nw<D, FP8, kSelected>(a, L, NW, halves, st);
+    case kTree: return launch_nw<D, FP8, kTree>(a, L, NW, halves, st);
+    default: return launch_nw<D, FP8, kCausal>(a, L, NW, halves, st);
   }
 }
 
-hipError_t launch_attn_tile(const AttnArgs& a, const AttnLaunch& L, int D, bool fp8, int NW, hipStream_t st) {
-  if (D == 128) return fp8 ? launch_mode<128, true>(a, L, NW, st) : launch_mode<128, false>(a, L, NW, st);
-  return fp8 ? launch_mode<64, true>(a, L, NW, st) : launch_mode<64, false>(a, L, NW, st);
+hipError_t launch_attn_tile(const AttnArgs& a, const AttnLaunch& L, int D, bool fp8, int NW, bool halves, hipStream_t st) {
+  if (D == 128) return fp8 ? launch_mode<128, true>(a, L, NW, halves, st) : launch_mode<128, false>(a, L, NW, halves, st);
+  return fp8 ? launch_mode<64, true>(a, L, NW, halves, st) : launch_mode<64, false>(a, L, NW, halves, st);
 }
 
 }  // namespace misa

@@ -200,8 +200,8 @@ struct AttnArgs {
 };
 // topk = 0: over every visible key, or, with ancestor bits (tree != nullptr), those
 // of a drafted token.  attn_fits: the launch's grid is in range.
-bool attn_fits(const misa_attn_shape& s, const misa_kv_pages& pg, int topk);
-size_t attn_workspace_bytes(const misa_attn_shape& s, const misa_kv_pages& pg, int topk);
+bool attn_fits(const misa_attn_shape& s, const misa_kv_pages& pg, int topk, bool tree);
+size_t attn_workspace_bytes(const misa_attn_shape& s, const misa_kv_pages& pg, int topk, bool tree);
 hipError_t launch_attention(const misa_attn_shape& s, const misa_kv_pages& pg, const uint16_t* q,
                             const int32_t* q_start, const int32_t* kv_lens, const int32_t* idx, int topk,
                             const uint32_t* tree, int tree_words, uint16_t* out, float* lse, void* ws, hipStream_t st);

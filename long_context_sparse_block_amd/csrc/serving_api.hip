@@ -84,8 +84,8 @@ misa_status attention(const misa_attn_shape* s, const misa_kv_pages* p, const ui
                       const int32_t* kv_lens, const int32_t* idx, int32_t topk, const uint32_t* mask, int32_t words,
                       uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
   MISA_TRY(check_attn_pointers(p, q, q_start, kv_lens, out));
-  if (!misa::attn_fits(*s, *p, topk)) return MISA_ERR_UNSUPPORTED;
-  const size_t need = misa::attn_workspace_bytes(*s, *p, topk);
+  if (!misa::attn_fits(*s, *p, topk, mask != nullptr)) return MISA_ERR_UNSUPPORTED;
+  const size_t need = misa::attn_workspace_bytes(*s, *p, topk, mask != nullptr);
   if (need > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < need)) return MISA_ERR_WORKSPACE;
   if (s->n_tokens == 0) return MISA_OK;
   return from_hip(misa::launch_attention(*s, *p, q, q_start, kv_lens, idx, topk, mask, words, out, lse, ws,
@@ -183,7 +183,7 @@ misa_status misa_write_pages(int64_t n_tokens, int32_t n_heads, int32_t head_dim
 
 size_t misa_attention_paged_workspace_bytes(const misa_attn_shape* shape, const misa_kv_pages* pages) {
   if (check_attn(shape, pages) != MISA_OK) return 0;
-  return misa::attn_workspace_bytes(*shape, *pages, 0);
+  return misa::attn_workspace_bytes(*shape, *pages, 0, false);
 }
 
 misa_status misa_attention_paged(const misa_attn_shape* shape, const misa_kv_pages* pages, const uint16_t* q,
@@ -196,7 +196,7 @@ misa_status misa_attention_paged(const misa_attn_shape* shape, const misa_kv_pag
 size_t misa_attention_selected_workspace_bytes(const misa_attn_shape* shape, const misa_kv_pages* pages,
                                                int32_t topk) {
   if (check_attn(shape, pages) != MISA_OK || topk < 1 || topk > MISA_MAX_TOPK) return 0;
-  return misa::attn_workspace_bytes(*shape, *pages, topk);
+  return misa::attn_workspace_bytes(*shape, *pages, topk, false);
 }
 
 misa_status misa_attention_selected(const misa_attn_shape* shape, const misa_kv_pages* pages, const uint16_t* q,
@@ -225,7 +225,8 @@ misa_status misa_plan_tree(int32_t n_seq, const int32_t* parents, const int32_t*
 }
 
 size_t misa_attention_tree_workspace_bytes(const misa_attn_shape* shape, const misa_kv_pages* pages) {
-  return misa_attention_paged_workspace_bytes(shape, pages);
+  if (check_attn(shape, pages) != MISA_OK) return 0;
+  return misa::attn_workspace_bytes(*shape, *pages, 0, true);
 }
 
 misa_status misa_attention_tree(const misa_attn_shape* shape, const misa_kv_pages* pages, const uint16_t* q,

@@ -421,8 +421,12 @@ def _attention(name, q, k_pages, v_pages, block_table, q_start, kv_lens, idx, k_
     if T == 0:
         return out, lse
     if ws is None:
-        need = (lib.misa_attention_selected_workspace_bytes(shape, pages, topk) if name == "misa_attention_selected"
-                else lib.misa_attention_paged_workspace_bytes(shape, pages))   # (a tree's is the same)
+        if name == "misa_attention_selected":
+            need = lib.misa_attention_selected_workspace_bytes(shape, pages, topk)
+        elif name == "misa_attention_tree":
+            need = lib.misa_attention_tree_workspace_bytes(shape, pages)
+        else:
+            need = lib.misa_attention_paged_workspace_bytes(shape, pages)
         ws, at = _scratch(need, q) if need else (None, None)   # (ws stays until the call has been made)
         _call(name, fn, dev, *args, at, need)
     else:

@@ -98,6 +98,9 @@ CASES = {   # lens, new, heads, kv heads, page
     "word_edges": ([95, 96, 97, 128, 161], [31, 32, 33, 64, 97], 2, 2, 32),
     "group_of_40": ([333, 77], [3, 9], 40, 1, 16),
     "one_long_tree": ([700], [333], 4, 2, 64),
+    "rows_64": ([9000], [16], 8, 2, 64),                        # at most 64 rows of a kv head, cut in splits
+    "rows_64_short": ([16, 30, 45, 97, 64, 20], [16, 15, 1, 12, 9, 16], 8, 2, 16),   # the same, some over one half of a tile's keys
+    "rows_20_of_40": ([6000, 5000, 1], [20, 18, 1], 6, 3, 64),
 }
 
 
@@ -116,7 +119,7 @@ def test_attention(name, dim, fp8):
 
 
 @pytest.mark.parametrize("dim,fp8", [(64, False), (128, True)])
-@pytest.mark.parametrize("name", ["few_rows", "rows_33", "word_edges", "no_prefix"])
+@pytest.mark.parametrize("name", ["few_rows", "rows_33", "word_edges", "no_prefix", "rows_64_short"])
 def test_attention_under_any_mask(name, dim, fp8):
     """Masks that no tree gives: a token without itself, without anything, with later ones, bits behind the sequence's
     tokens; and words more than needed."""
