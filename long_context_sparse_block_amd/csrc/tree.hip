@@ -20,27 +20,31 @@ constexpr int kPlanThreads = 256;
 constexpr int kLdsNodes = 2048;   // a tree's parents that a workgroup keeps in LDS
 }  // namespace
 
-// A workgroup takes a sequence, a thread a token: it walks from the token to the root
+// `slices` workgroups take a sequence, a thread a token: it walks from the token to the root
 // and collects its ancestors, a word of bits at a time (parents come before their
 // children, so the walk goes through the words from the last to the first).  A step
-// is a read of LDS that the next one waits for, some 40 ns.
+// is a read of LDS that the next one waits for, some 40 ns, more when many waves
+// of a CU walk: a slice for every 256 tokens that the words hold (4 trees of 2048
+// tokens, walks of 800 steps, 316 us in one slice, 69 in eight; one of 1024 85, 34).
 __global__ void __launch_bounds__(kPlanThreads) k_plan_tree(int n_seq, const int32_t* parents, const int32_t* q_start,
                                                             const int32_t* kv_lens, int64_t n_tokens, int words,
                                                             uint32_t* mask, int32_t* positions) {
   __shared__ int s_up[kLdsNodes];
   const int tid = threadIdx.x;
-  if ((int)blockIdx.x >= n_seq) {   // rows of no sequence: in front of the first one, behind the last
+  const int b = blockIdx.x, slice = blockIdx.y, slices = gridDim.y;
+  if (b >= n_seq) {   // rows of no sequence: in front of the first one, behind the last
     const int64_t lo = min(max((int64_t)q_start[0], (int64_t)0), n_tokens);
     const int64_t hi = min(max((int64_t)q_start[n_seq], lo), n_tokens), rows = lo + n_tokens - hi;
-    const int64_t step = (int64_t)(gridDim.x - n_seq) * kPlanThreads, at = (int64_t)(blockIdx.x - n_seq) * kPlanThreads + tid;
+    const int64_t step = (int64_t)(gridDim.x - n_seq) * slices * kPlanThreads;
+    const int64_t at = ((int64_t)(b - n_seq) * slices + slice) * kPlanThreads + tid;
     for (int64_t i = at; i < rows * words; i += step) mask[i < lo * words ? i : i + (hi - lo) * words] = 0;
     for (int64_t i = at; i < rows; i += step) positions[i < lo ? i : i + (hi - lo)] = -1;
     return;
   }
-  const int64_t s = q_start[blockIdx.x], e = q_start[blockIdx.x + 1];
+  const int64_t s = q_start[b], e = q_start[b + 1];
   const int64_t t0 = min(max(s, (int64_t)0), n_tokens);
   const int m = (int)max((int64_t)0, min(e, n_tokens) - t0);
-  const int64_t pos0 = (int64_t)max(kv_lens[blockIdx.x], 0) - (e - s);
+  const int64_t pos0 = (int64_t)max(kv_lens[b], 0) - (e - s);
   const int32_t* const up = parents + t0;
   // an entry that does not name a token before its own makes that a root
   auto parent = [&](int i) __attribute__((always_inline)) {
@@ -50,7 +54,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_tree(int n_seq, const int
   const int in_lds = min(m, kLdsNodes);
   for (int i = tid; i < in_lds; i += kPlanThreads) s_up[i] = parent(i);
   __syncthreads();
-  for (int i = tid; i < m; i += kPlanThreads) {
+  for (int i = slice * kPlanThreads + tid; i < m; i += slices * kPlanThreads) {
     uint32_t* const row = mask + (t0 + i) * words;
     int j = i, depth = 0;
     for (int w = words - 1; w >= 0; --w) {
@@ -67,9 +71,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_tree(int n_seq, const int
 
 hipError_t launch_plan_tree(int n_seq, const int32_t* parents, const int32_t* q_start, const int32_t* kv_lens,
                             int64_t n_tokens, int words, uint32_t* mask, int32_t* positions, hipStream_t st) {
-  const int64_t pad = std::min<int64_t>(256, (n_tokens * words + 65535) / 65536);   // workgroups for rows of no sequence
-  hipLaunchKernelGGL(k_plan_tree, dim3((unsigned)(n_seq + pad)), dim3(kPlanThreads), 0, st, n_seq, parents, q_start,
-                     kv_lens, n_tokens, words, mask, positions);
+  const int slices = (words + 7) / 8;
+  const int64_t pad = std::min<int64_t>((256 + slices - 1) / slices, (n_tokens * words + 65535) / 65536);   // for rows of no sequence
+  hipLaunchKernelGGL(k_plan_tree, dim3((unsigned)(n_seq + pad), (unsigned)slices), dim3(kPlanThreads), 0, st, n_seq, parents,
+                     q_start, kv_lens, n_tokens, words, mask, positions);
   return hipGetLastError();
 }
 
