@@ -674,10 +674,10 @@ misa_status misa_plan_tree(int32_t n_seq, const int32_t* parents, const int32_t*
  * kv_lens[b] - m cached tokens, and new token j where bit j of its mask row is
  * set and j < m (any bits: the mask need not come from misa_plan_tree).  The
  * mask is read for the rows of sequences only.  A row that sees nothing gives
- * out = 0, lse = -inf.  All else is as in misa_attention_paged, its limits too
- * (where no sequence may have more than 64 rows of a kv head, chunks' workgroups take
- * 64); ws: misa_attention_tree_workspace_bytes() bytes.  NaN and infinity in a value among a sequence's new tokens may reach
- * others of its new tokens, never another sequence.
+ * out = 0, lse = -inf.  All else is as in misa_attention_paged, its limits too.
+ * NaN and infinity in a value among a sequence's new tokens may reach others of
+ * its new tokens, never another sequence.
+ * ws: misa_attention_tree_workspace_bytes() bytes, as misa_attention_paged's.
  * mask: uint32 [n_tokens][words], 1 <= words <= 1024 (MISA_ERR_UNSUPPORTED past it).
  */
 misa_status misa_attention_tree(const misa_attn_shape* shape, const misa_kv_pages* pages, const uint16_t* q,
@@ -720,9 +720,9 @@ misa_status misa_keep_path(int32_t n_seq, const int32_t* path, int32_t max_path,
  *   scale = fp32(amax / 448), at least 2^-126; 1 for a block of zeros
  *   codes = e4m3fn round-to-nearest-even of fp32(x / scale)
  * the rule of misa_quantize_q, which this call equals bit for bit for heads of 128
- * (block_rows = 1) but where a row's values all lie below 448 * 2^-126.  NaN becomes the NaN code and leaves its block's scale
- * alone; a block with an infinity has scale infinity, its infinities NaN codes,
- * the rest 0.
+ * (block_rows = 1) but where a row's values all lie below 448 * 2^-126.  NaN
+ * becomes the NaN code and leaves its block's scale alone; a block with an
+ * infinity has scale infinity, its infinities NaN codes, the rest 0.
  * x: bf16, fp16 or fp32, row stride x_stride (elements), 16-byte aligned rows.
  * codes: [rows][cols] dense, 16-byte aligned.  scale: float
  * [ceil(rows / block_rows)][ceil(cols / 128)].  cols: a multiple of 16, up to 2^20;

@@ -25,6 +25,10 @@
 // e4m3: 243 to 249 us), but few rows with a few heavy keys average a weight's
 // rounding out too little.
 //
+// A tree's rows of up to 4 (8) tokens come here too; the new tokens' tiles apply
+// the mask row's bits, the prefix's none (64 trees of 4 over 8..16K keys, 32 / 8 heads of
+// 128, bf16: 587 us, 5.5 TB/s).
+//
 // Measured: 64 decodes over 8..16K keys, 32 / 8 heads of 128: bf16 577-599 us by card
 // (3.2 GB, 5.4 TB/s), e4m3 346-363 us; one token over 32K keys 37 us; 1000 tokens x
 // 2048 picks, 32 / 4 heads, e4m3: 249-253 us (2.1 GB of gathered rows; vector unit

@@ -7,14 +7,14 @@
 // matrix unit sums eight neighbouring products at a time, each cut at 2^-13 of the
 // largest (measured; the eights are added up without further loss): with codes of 4 bits
 // and a result of 8 that costs nothing seen, the relative error of the results here is
-// 0.0017 in all, bf16's own rounding.  w is the instructions' first operand, so that a lane's results are one
-// row of x, whose scale is one factor a lane.
+// 0.0017 in all, bf16's own rounding.  w is the instructions' first operand, so that
+// a lane's results are one row of x, whose scale is one factor a lane.
 //
 // Measured: 8192 x 8192 x 4096 272-282 us by card (1952 to 2018 TFLOP/s; the library's
 // product of the same codes with one scale for all 227 us), 8192 x 4096 x 8192 258 us
 // (2129); the clock falls to 1.75-1.9 GHz there, MFMA is busy 0.50-0.56 of the time, the
-// vector unit 0.36-0.45.  515 x 4099 x 1504 13.2 us, 64 x 8192 x 2048 7.9 us, 1 x 8192 x 4096
-// 7.9 us (33.6 MB, 4.3 TB/s).
+// vector unit 0.36-0.45.  515 x 4099 x 1504 13-14 us, 64 x 8192 x 2048 7.6-8.4 us, 1 x 8192 x
+// 4096 7.9 us (33.6 MB, 4.3 TB/s).
 // Tried on the large tiles and not kept: a workgroup that goes on to the next tile with
 // its first block on the way (286 us; the results leave in smaller pieces, 18
 // registers are spilled), a second barrier in the middle of a block to ask for the

@@ -318,3 +318,79 @@ def test_a_verifying_step_equals_decoding_the_kept_path():
     again = step(d, after, lens, torch.ones(2, **i32))
     for x, y in zip(last[:3], again[:3]):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_captured_verifying_step(fp8):
+    """The whole step in one graph, replayed with other lengths, trees, paths and hidden states: the same bits as eager
+    calls, in the pages too."""
+    g = torch.Generator().manual_seed(31)
+    H, KH, D, hid, page, width, n, T = 8, 2, 64, 384, 16, 30, 3, 40
+    dev, i32 = "cuda", dict(dtype=torch.int32, device="cuda")
+    wide = (H + 2 * KH) * D
+    w_in = misa.misa_quantize_blocks((torch.randn((wide, hid), generator=g) / math.sqrt(hid)).to(dev), 128)
+    w_out = misa.misa_quantize_blocks((torch.randn((hid, H * D), generator=g) / math.sqrt(H * D)).to(dev), 128)
+    f, ms = misa.rope_inv_freq(D, device=dev)
+    shape = (n * width, page, KH, D)
+
+    def inputs(seed, cached, new):
+        g = torch.Generator().manual_seed(seed)
+        parents = sum((th.random_parents(g, m, "tree") for m in new), [])
+        path = torch.full((n, 5), -1, dtype=torch.int32)
+        for b, m in enumerate(new):
+            node, up = m - 1, []
+            while node >= 0:
+                up.append(node)
+                node = parents[sum(new[:b]) + node]
+            up = sorted(up)[:5]
+            path[b, :len(up)] = torch.tensor(up, dtype=torch.int32)
+        k = torch.randn(shape, generator=g)
+        v = torch.randn(shape, generator=g)
+        order = torch.randperm(n * width, generator=g).to(torch.int32)
+        table = torch.full((n, width), -1, dtype=torch.int32)
+        for b, c in enumerate(cached):
+            taken = -(-c // page)
+            table[b, :taken] = order[:taken]
+            order = order[taken:]
+        free = torch.zeros(n * width, dtype=torch.int32)
+        free[:len(order)] = order
+        s = dict(hidden=torch.randn((T, hid), generator=g).bfloat16(), parents=torch.tensor(parents + [0] * (T - len(parents)), dtype=torch.int32),
+                 path=path, cached=torch.tensor(cached, dtype=torch.int32), new=torch.tensor(new, dtype=torch.int32), table=table,
+                 free=free, k=k.bfloat16(), v=v.bfloat16())
+        if fp8:
+            s["k"], s["v"] = (x.to(torch.float8_e4m3fn).view(torch.uint8) for x in (k, v))
+            s["ks"], s["vs"] = (0.5 + torch.rand(shape[:3], generator=g) for _ in range(2))
+        return {name: x.to(dev) for name, x in s.items()}
+
+    def step(s):
+        y = misa.misa_matmul_q8(*misa.misa_quantize_blocks(s["hidden"]), *w_in).view(T, -1, D)
+        p = misa.misa_plan_pages(s["cached"], s["new"], s["free"], s["table"], page, T)
+        tree = misa.misa_plan_tree(s["parents"], p.q_start, p.kv_lens, 1)
+        q = misa.misa_rope(y[:, :H], tree.positions, f, mscale=ms)
+        ks, vs = s.get("ks"), s.get("vs")
+        misa.misa_write_pages(y[:, H:H + KH], p.slots, s["k"], ks, v=y[:, H + KH:], v_pages=s["v"], v_scale_pages=vs,
+                              positions=tree.positions, inv_freq=f, mscale=ms)
+        o, _ = misa.misa_attention_tree(q, s["k"], s["v"], s["table"], p.q_start, p.kv_lens, tree.mask, ks, vs, max_new=16,
+                                        out=torch.zeros_like(q))
+        out = misa.misa_matmul_q8(*misa.misa_quantize_blocks(o.view(T, H * D)), *w_out)
+        kept = misa.misa_keep_path(s["path"], p.q_start, p.kv_lens, s["table"], s["k"], ks, s["v"], vs)
+        return o, out, kept
+
+    cases = [(1, [100, 333, 7], [9, 16, 12]), (2, [0, 464, 31], [16, 1, 16]), (3, [50, 0, 201], [0, 13, 5])]
+    wants = []
+    for c in cases:
+        s = inputs(*c)
+        wants.append((step(s), s))
+    static = inputs(*cases[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(static)
+    for c, (want, after) in list(zip(cases, wants)) * 2:
+        for name, x in inputs(*c).items():
+            static[name].copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+        for name in after:
+            assert torch.equal(static[name].view(torch.uint8), after[name].view(torch.uint8)), name

@@ -48,7 +48,7 @@ def test_tree_attention_refusals(lib):
         assert call(**bad) == -2, bad
     long = pool(max_pages=4096)
     need = misa.misa_attention_tree_workspace_bytes(attn(), long)
-    assert need > 0
+    assert need == misa.misa_attention_paged_workspace_bytes(attn(), long) > 0
     assert call(nb=need - 1) == -3 and call(ws=None) == -3 and call(ws=at(5, 4)) == -3
     assert call(s=attn(n_tokens=0)) == 0
     assert misa.misa_attention_tree_workspace_bytes(attn(n_heads=7), pool()) == 0
