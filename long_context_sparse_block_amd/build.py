@@ -41,7 +41,7 @@ def tensor_args_command(out: str) -> list[str]:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-            *(f"-I{p}" for p in [*include_paths(), sysconfig.get_paths()["include"]]),
+            *(f"-I{p}" for p in [INCLUDE, *include_paths(), sysconfig.get_paths()["include"]]),
             os.path.join(CSRC, "tensor_args.cpp"), "-o", out, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 

@@ -157,13 +157,15 @@ def _fresh_py(shape, dtype, like):
 
 try:   # the same in C++ (csrc/tensor_args.cpp): a quarter of the time
     from ._tensor_args import dense as _dense, fresh as _fresh, matrix as _matrix, pool as _pool, rows as _rows, scratch as _scratch
+    from . import _tensor_args as _cpp
 except ModuleNotFoundError:   # not built yet
+    _cpp = None
     _dense, _fresh, _matrix, _pool, _rows, _scratch = _dense_py, _fresh_py, _matrix_py, _pool_py, _rows_py, _scratch_py
 except ImportError as e:   # built against another torch, say: every call raises, importing and building again do not
     def _dense(*args, why=str(e)):
         raise RuntimeError(f"_tensor_args does not load ({why}): build it again with "
                            "`python -m long_context_sparse_block_amd.build`")
-    _fresh = _matrix = _pool = _rows = _scratch = _dense
+    _cpp, _fresh, _matrix, _pool, _rows, _scratch = None, *[_dense] * 5
 
 
 def _on(stream, t, name, f, *args):
@@ -178,12 +180,24 @@ def _on(stream, t, name, f, *args):
         return f(*args)
 
 
-def _call(name, fn, dev, *args):
-    """fn(*args, current stream's handle) on GPU `dev`."""
+_entries = {}   # what calls an entry point: C++, or ctypes where that is not built
+
+
+def _entry(name):
+    fn = getattr(load(), name)
+    if _cpp is not None:
+        _cpp.bind(name, ctypes.cast(fn, ctypes.c_void_p).value)
+        fn = getattr(_cpp, name)
+    _entries[name] = fn
+    return fn
+
+
+def _call(name, dev, *args):
+    """The entry point's call with args and the current stream's handle, on GPU `dev`."""
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            return _call(name, fn, dev, *args)
-    st = fn(*args, _raw_stream(dev))
+            return _call(name, dev, *args)
+    st = (_entries.get(name) or _entry(name))(*args, _raw_stream(dev))
     if st != 0:
         _check(st, name)
 
@@ -215,7 +229,7 @@ def misa_plan_pages(cached_lens, new_lens, free_pages, block_table, page_keys: i
                 _dense(plan.positions, i32, (n_tokens,), "positions", dev), n_tokens,
                 _dense(plan.n_taken, i32, (1,), "n_taken", dev))
     n_free, width = free_pages.shape[0], block_table.shape[-1]
-    _call("misa_plan_pages", load().misa_plan_pages, dev, n, _dense(cached_lens, i32, (n,), "cached_lens", dev),
+    _call("misa_plan_pages", dev, n, _dense(cached_lens, i32, (n,), "cached_lens", dev),
           _dense(new_lens, i32, (n,), "new_lens", dev), page_keys, _dense(free_pages, i32, (n_free,), "free_pages", dev),
           n_free, _dense(block_table, i32, (n, width), "block_table", dev), width, *outs)
     return plan
@@ -315,7 +329,7 @@ def misa_rope(x, positions, inv_freq, layout: str = "half", rot_start: int = 0, 
     op, ost, osh = _rows(out, (x.dtype,), "out", dev, x.shape)
     spec = _rope_spec(positions, inv_freq, layout, rot_start, mscale, backward, T, dev)
     if T > 0:
-        _call("misa_rope", load().misa_rope, dev, spec, xp, _DTYPES[x.dtype], T, H, D, xst, xsh, op, ost, osh)
+        _call("misa_rope", dev, spec, xp, _DTYPES[x.dtype], T, H, D, xst, xsh, op, ost, osh)
     return out
 
 
@@ -359,7 +373,7 @@ def misa_write_pages(k, slots, k_pages, k_scale_pages=None, v=None, v_pages=None
     if inv_freq is not None:
         spec = _rope_spec(positions, inv_freq, layout, rot_start, mscale, False, T, dev)
     if T > 0:
-        _call("misa_write_pages", load().misa_write_pages, dev, T, H, D, kp, kst, ksh, vp, vst or 0, vsh or 0, sp,
+        _call("misa_write_pages", dev, T, H, D, kp, kst, ksh, vp, vst or 0, vsh or 0, sp,
               spec, kpool, vpool, kd, ks, vs, n_pages, page_keys)
 
 
@@ -404,14 +418,10 @@ def _attention(name, q, k_pages, v_pages, block_table, q_start, kv_lens, idx, k_
         if idx.dim() == 3 and idx.shape[0] * idx.shape[1] == T and idx.is_contiguous():
             idx = idx.view(T, topk)
         args += [_dense(idx, i32, (T, topk), "idx", dev), topk]
-        fn = lib.misa_attention_selected
     elif name == "misa_attention_tree":
         _dev(idx, "mask")
         words = idx.shape[-1]
         args += [_dense(idx, i32, (T, words), "mask", dev), words]
-        fn = lib.misa_attention_tree
-    else:
-        fn = lib.misa_attention_paged
     if out is None:
         out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
     args.append(_dense(out, torch.bfloat16, (T, H, D), "out", dev))
@@ -428,11 +438,11 @@ def _attention(name, q, k_pages, v_pages, block_table, q_start, kv_lens, idx, k_
         else:
             need = lib.misa_attention_paged_workspace_bytes(shape, pages)
         ws, at = _scratch(need, q) if need else (None, None)   # (ws stays until the call has been made)
-        _call(name, fn, dev, *args, at, need)
+        _call(name, dev, *args, at, need)
     else:
         if ws.get_device() != dev or not ws.is_contiguous():
             raise ValueError(f"ws must be a dense tensor on cuda:{dev}")
-        _call(name, fn, dev, *args, ws.data_ptr(), ws.numel() * ws.element_size())
+        _call(name, dev, *args, ws.data_ptr(), ws.numel() * ws.element_size())
     return out, lse
 
 
@@ -485,7 +495,7 @@ def misa_plan_tree(parents, q_start, kv_lens, words: int, plan: TreePlan | None 
         mp = _dense(plan.mask, i32, (T, words), "mask", dev)
         pp = _dense(plan.positions, i32, (T,), "positions", dev)
     if T > 0:
-        _call("misa_plan_tree", load().misa_plan_tree, dev, *args, mp, pp)
+        _call("misa_plan_tree", dev, *args, mp, pp)
     return plan
 
 
@@ -533,7 +543,7 @@ def misa_keep_path(path, q_start, kv_lens, block_table, k_pages, k_scale_pages=N
         kept_lens, kp = _fresh((n,), i32, path)
     else:
         kp = _dense(kept_lens, i32, (n,), "kept_lens", dev)
-    _call("misa_keep_path", load().misa_keep_path, dev, n, _dense(path, i32, (n, most), "path", dev), most,
+    _call("misa_keep_path", dev, n, _dense(path, i32, (n, most), "path", dev), most,
           _dense(q_start, i32, (n + 1,), "q_start", dev), _dense(kv_lens, i32, (n,), "kv_lens", dev),
           _dense(block_table, i32, (n, width), "block_table", dev), width, H, D, kpool, vpool, kd, ks, vs, n_pages,
           page_keys, kp)
@@ -562,7 +572,7 @@ def misa_quantize_blocks(x, block_rows: int = 1, codes=None, scale=None, stream=
     else:
         sp = _dense(scale, torch.float32, blocks, "scale", dev)
     if R > 0:
-        _call("misa_quantize_blocks", load().misa_quantize_blocks, dev, at, _DTYPES[x.dtype], R, K, st, block_rows, cp, sp)
+        _call("misa_quantize_blocks", dev, at, _DTYPES[x.dtype], R, K, st, block_rows, cp, sp)
     return codes, scale
 
 
@@ -600,5 +610,5 @@ def misa_matmul_q8(x, x_scale, w, w_scale, out=None, ws=None, stream=None):
         if ws.get_device() != dev or not ws.is_contiguous():
             raise ValueError(f"ws must be a dense tensor on cuda:{dev}")
         at, need = ws.data_ptr(), ws.numel() * ws.element_size()
-    _call("misa_matmul_q8", lib.misa_matmul_q8, dev, *args, at, need)
+    _call("misa_matmul_q8", dev, *args, at, need)
     return out

@@ -147,3 +147,32 @@ def test_errors_of_torch_stay_errors(call, tensor):
     print(r.stdout, r.stderr[-500:])
     assert r.returncode == 0
     assert r.stdout.startswith("raised")
+
+
+def test_the_calls_without_ctypes(lib):
+    """The wrappers' calls turn their arguments into C's themselves: the same status as through ctypes, and an error for
+    what is no such argument."""
+    from long_context_sparse_block_amd import _tensor_args, serving
+    names = ("misa_plan_pages", "misa_rope", "misa_write_pages", "misa_attention_paged", "misa_attention_selected",
+             "misa_plan_tree", "misa_attention_tree", "misa_keep_path", "misa_quantize_blocks", "misa_matmul_q8")
+    for name in names:
+        call, n = serving._entry(name), len(getattr(lib, name).argtypes)
+        assert call is getattr(_tensor_args, name)
+        zeros = [None if t is ctypes.c_void_p else 0 for t in getattr(lib, name).argtypes]
+        assert call(*zeros) == getattr(lib, name)(*zeros) == -1, name
+        for args in (zeros[:-1], zeros + [0]):
+            with pytest.raises(TypeError, match=str(n)):
+                call(*args)
+    quantize, matmul = serving._entry("misa_quantize_blocks"), serving._entry("misa_matmul_q8")
+    good = [at(1).value, 0, 4, 256, 256, 128, at(2).value, at(3).value, None]
+    for i, bad, status in ((1, 7, -1), (2, -1, -1), (3, 24, -2), (4, 4, -1), (5, 2, -1), (6, at(2, 8).value, -1), (2, 1 << 40, -2)):
+        args = good[:i] + [bad] + good[i + 1:]
+        assert quantize(*args) == lib.misa_quantize_blocks(*args) == status, (i, bad)
+    for i, bad, error in ((1, 1 << 31, OverflowError), (5, -(1 << 31) - 1, OverflowError),
+                          (2, 1 << 63, OverflowError), (2, 1.5, TypeError), (0, "x", TypeError), (0, 1.5, TypeError)):
+        with pytest.raises(error):
+            quantize(*good[:i], bad, *good[i + 1:])
+    with pytest.raises((OverflowError, TypeError)):
+        matmul(*[1] * 12, -1, None)
+    with pytest.raises(ValueError, match="no serving call"):
+        _tensor_args.bind("misa_topk", 0)
