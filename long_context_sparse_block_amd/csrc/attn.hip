@@ -32,7 +32,9 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a, const AttnL
   const uint32_t i = is_tile ? blockIdx.x : blockIdx.x - n_tile;
   const int G = a.n_heads / a.n_kv_heads;
   const uint32_t per = (uint32_t)S.rows / RW;   // workgroups of a unit and kv head
-  const int rr = (int)(i % per) * RW + (int)threadIdx.x / LR, piece = (int)threadIdx.x % LR;
+  // attn_tile's parts lie as pieces of 16 bytes, [piece][row], attn_wave's as rows
+  const int rr = (int)(i % per) * RW + (is_tile ? (int)threadIdx.x % RW : (int)threadIdx.x / LR);
+  const int piece = is_tile ? (int)threadIdx.x / RW : (int)threadIdx.x % LR;
   const int g = (int)(i / per % (uint32_t)a.n_kv_heads), unit = (int)(i / per / (uint32_t)a.n_kv_heads);
   int r0, nrows, tok0, n = S.n_splits;
   if (SEL) {
@@ -53,7 +55,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a, const AttnL
   const PartPlace part = part_place<SEL>(S, a.n_kv_heads, G, S.rows, g, unit, tok0, r0, nrows);
   const int64_t pr = part.begin + rr;
   const float2* const ml = S.part_ml + pr;
-  const float* const po = S.part_o + pr * D + piece * 4;
+  const float* const po = S.part_o + (is_tile ? part.begin * D + (piece * part.step + rr) * 4 : pr * D + piece * 4);
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
   float top = -INFINITY, sum = 0.f;
   auto some = [&](int s0, auto count) __attribute__((always_inline)) {

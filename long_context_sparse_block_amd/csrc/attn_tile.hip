@@ -474,14 +474,19 @@ __global__ void __launch_bounds__(NW * kWave, D == 64 ? 3 : 2) k_attn_tile(const
   }
   if (!live) return;
   const PartPlace part = part_place<SEL>(L, a.n_kv_heads, G, BM, g, unit, tok0, r0, nrows);
-  const int64_t pr = part.begin + split * part.step + rw * 32 + c32;
-  if (h == 0) L.part_ml[pr] = make_float2(m, l);
+  const int64_t p0 = part.begin + split * part.step;
+  const int row = rw * 32 + c32;
+  if (h == 0) L.part_ml[p0 + row] = make_float2(m, l);
   if (l != 0.f) {
+    // Pieces of 16 bytes, [piece][row]: a store's lanes fill lines, where
+    // rows one after the other leave 32 lines a quarter written each (one tree or chunk
+    // of 64 tokens over 8192 keys: 25.6 -> 24.3 us; 64 selected decodes 26.3 -> 25.2)
+    float* const po = L.part_o + p0 * D + row * 4;
 #pragma unroll
     for (int db = 0; db < DB; ++db)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<f32x4*>(L.part_o + pr * D + db * 32 + 8 * j + 4 * h) =
+        *reinterpret_cast<f32x4*>(po + (db * 8 + 2 * j + h) * part.step * 4) =
             f32x4{o[db][4 * j], o[db][4 * j + 1], o[db][4 * j + 2], o[db][4 * j + 3]};
   }
 }
