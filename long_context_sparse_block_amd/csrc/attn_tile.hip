@@ -23,7 +23,7 @@
 // heads 172 -> 214.
 // Trees (the rows of a unit see the prefix, and of the new tokens those whose bits
 // are set: a word or two of the mask row a tile) cost what a chain costs: 64 tokens
-// over 8192 keys 25.6 us (25.3 as a chain; the call, of which the join 5), 64 trees of
+// over 8192 keys 24.3 us (24.1 as a chain; the call, of which the join 5), 64 trees of
 // 16 over 8..16K 655-670 us (5 TB/s of keys and values), nine of 1 to 257 over e4m3
 // pages, heads of 64, 59-64 us.
 // 32 rows a wave: with 64, or with scores formed a tile ahead, the registers
