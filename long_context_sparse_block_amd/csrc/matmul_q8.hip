@@ -52,7 +52,7 @@ constexpr int kValu = 0x2, kMfma = 0x8, kDsRead = 0x100;   // instruction classe
 struct Plan {
   int tiles_n, tiles_m;   // output tiles
   int splits, per;        // parts of the blocks, and blocks of a part
-  float* part;            // splits > 1: the parts' sums [split][m][ld]
+  float* part;            // splits > 1: the parts' sums [split][ld / 4][m][4], so that a store's lanes fill lines
   int64_t ld;             // n, rounded up to 4
 };
 }  // namespace
@@ -243,13 +243,13 @@ __global__ void __launch_bounds__(WN * WM * kWave, WN * WM / 4) k_matmul_tile(co
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
       const int64_t m = mw + j * 32 + c32;
-      float* const dst = pl.part + ((int64_t)split * a.m + m) * pl.ld + nw;
+      float* const dst = pl.part + (int64_t)split * a.m * pl.ld + nw * a.m + m * 4;
 #pragma unroll
       for (int i = 0; i < FN; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           if (m < a.m && nw + i * 32 + 8 * q + 4 * h < a.n)
-            *reinterpret_cast<f32x4*>(dst + i * 32 + 8 * q + 4 * h) =
+            *reinterpret_cast<f32x4*>(dst + (i * 32 + 8 * q + 4 * h) * a.m) =
                 f32x4{sum[i][j][4 * q], sum[i][j][4 * q + 1], sum[i][j][4 * q + 2], sum[i][j][4 * q + 3]};
     }
     return;
@@ -433,12 +433,12 @@ __global__ void __launch_bounds__(8 * kWave, 2) k_matmul_rows(const MatmulArgs a
   }
 }
 
-// The sums of a tile launch's parts, four columns a thread
+// The sums of a tile launch's parts, four columns of a row a thread, eight rows side by side
 __global__ void __launch_bounds__(256) k_matmul_join(const MatmulArgs a, const Plan pl) {
   const int64_t quads = pl.ld / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= quads * a.m) return;
-  const int64_t m = i / quads, n = (i - m * quads) * 4;
-  const float* const src = pl.part + m * pl.ld + n;
+  const int64_t rows = i / (quads * 8), at = i - rows * quads * 8, m = rows * 8 + at % 8, n = at / 8 * 4;
+  if (m >= a.m) return;
+  const float* const src = pl.part + n * a.m + m * 4;
   f32x4 v = *reinterpret_cast<const f32x4*>(src);
   for (int s = 1; s < pl.splits; ++s) v += *reinterpret_cast<const f32x4*>(src + (int64_t)s * a.m * pl.ld);
   uint16_t* const dst = a.out + m * a.o_st + n;
@@ -457,8 +457,11 @@ namespace {
 // How a product is made.  The times are of a block of 128 columns: alone on their
 // CUs, tiles of 64 x 64 take 0.3 us, 128 x 64 0.38, 128 x 128 0.47 to 0.65 (by how many
 // there are); two of 128 x 128 on a CU 1.25, one of 256 x 256 2.1; 4 to 8 us a round
-// beside.  So the smallest tiles that the card holds all at once are taken, and
-// past them whichever of the two larger forms has the less time.
+// beside.  Tiles that the card holds all at once may take parts of the blocks side by
+// side, as many as it holds; the parts are then written and read again (at 6 TB/s, and
+// 2.5 us more).  Whole against in parts: 105 x 555 x 2464 10.3 and 8.1 us, 512 x 2048 x 7168
+// (256 tiles of 64 x 64 against four parts of 128 x 128) 22.5 and 20.0, 1024 x 1024 x 8192 26.6
+// and 22.5; 515 x 1003 x 3600 and what is shorter stays whole.
 enum Form { kRows, kTile64, kTile128x64, kTile128, kTwo128, kTile256 };
 struct Choice {
   Form form;
@@ -468,18 +471,26 @@ Choice choose(int64_t m, int64_t n, int64_t k) {
   const int64_t across = (k + 127) / 128;
   if (m <= 64) return Choice{kRows, 1, (int)across};
   auto tiles = [&](int bn, int bm) { return ((n + bn - 1) / bn) * ((m + bm - 1) / bm); };
-  const int64_t small = tiles(64, 64);
-  if (small <= 128 && across >= 24) {
-    // Parts of the blocks side by side: their join is about 12 blocks' time
-    const int64_t splits = std::min<int64_t>(256 / small, across / 4), per = (across + splits - 1) / splits;
-    if (across - per > 12) return Choice{kTile64, (int)((across + per - 1) / per), (int)per};
-  }
-  if (small <= 256) return Choice{kTile64, 1, (int)across};
-  if (tiles(128, 64) <= 256) return Choice{kTile128x64, 1, (int)across};
-  if (tiles(128, 128) <= 256) return Choice{kTile128, 1, (int)across};
   const double two = (double)((tiles(128, 128) + 511) / 512) * (1.25 * (double)across + 5.0);
   const double large = (double)((tiles(256, 256) + 255) / 256) * (2.1 * (double)across + 8.0);
-  return Choice{two < large ? kTwo128 : kTile256, 1, (int)across};
+  Choice best{two < large ? kTwo128 : kTile256, 1, (int)across};
+  double least = std::min(two, large);
+  constexpr struct { Form form; int bn, bm; double block; } small[] = {
+      {kTile64, 64, 64, 0.3}, {kTile128x64, 128, 64, 0.38}, {kTile128, 128, 128, 0.5}};
+  bool fits = false;
+  for (const auto& f : small) {
+    const int64_t held = 256 / tiles(f.bn, f.bm);   // parts that the card holds
+    for (int64_t s = 1; s <= held && (s == 1 || across >= 4 * s); ++s) {
+      const int64_t per = (across + s - 1) / s;
+      if (s > 1 && (across + per - 1) / per != s) continue;
+      const double cost = f.block * (double)per + 4.5 + (s > 1 ? 2.5 + 8.0 * (double)(s * m * n) / 6e6 : 0.0);
+      if (fits && cost >= 0.95 * least) continue;   // (of nearly equal ones the smaller form, and fewer parts)
+      fits = true;
+      least = cost;
+      best = Choice{f.form, (int)s, (int)per};
+    }
+  }
+  return best;
 }
 
 template <int WN, int WM, int FN, int FM, int S>
@@ -489,7 +500,7 @@ hipError_t launch_tile(const MatmulArgs& a, const Choice& c, void* work, hipStre
   const Plan pl{tn, tm, c.splits, c.per, static_cast<float*>(work), (a.n + 3) / 4 * 4};
   hipLaunchKernelGGL((k_matmul_tile<WN, WM, FN, FM, S>), dim3((unsigned)(tn * tm * c.splits)), dim3(WN * WM * kWave), 0, st, a, pl);
   if (c.splits > 1)
-    hipLaunchKernelGGL(k_matmul_join, dim3((unsigned)((a.m * pl.ld / 4 + 255) / 256)), dim3(256), 0, st, a, pl);
+    hipLaunchKernelGGL(k_matmul_join, dim3((unsigned)(((a.m + 7) / 8 * 8 * pl.ld / 4 + 255) / 256)), dim3(256), 0, st, a, pl);
   return hipGetLastError();
 }
 

@@ -106,7 +106,8 @@ SIZES = [(1, 1, 16), (1, 128, 128), (1, 2048, 2048), (2, 17, 144), (15, 130, 256
          (2, 16, 16384), (70, 96, 16400), (1500, 700, 256),
          # forms that the sizes above do not reach: 32 columns to a workgroup, each size of tile, parts of the blocks
          (5, 4500, 272), (30, 4200, 144), (60, 4130, 400), (128, 8200, 256), (515, 4099, 1504), (700, 8200, 272),
-         (4000, 4000, 528), (3990, 4090, 144), (65, 40, 8208), (120, 500, 4112), (300, 65, 12304)]
+         (4000, 4000, 528), (3990, 4090, 144), (65, 40, 8208), (120, 500, 4112), (300, 65, 12304),
+         (500, 1003, 5008), (500, 515, 12304)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
