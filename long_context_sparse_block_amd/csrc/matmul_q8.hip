@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(WN * WM * kWave, WN * WM / 4) k_matmul_tile(co
   }
 }
 
-// Few rows of x (at most 16 MT): bound by the reading of w.  A workgroup takes 16 NT
+// Few rows of x (at most 16 MT; not of the longest): bound by the reading of w.  A workgroup takes 16 NT
 // rows of w, each of its 8 waves an eighth of their blocks; their sums join in LDS, always
 // in the same order.  w's codes go straight to the registers that the
 // products read them from, x's through the wave's own LDS (side by side there, a row's
@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(256) k_matmul_join(const MatmulArgs a, const P
   if (m >= a.m) return;
   const float* const src = pl.part + n * a.m + m * 4;
   f32x4 v = *reinterpret_cast<const f32x4*>(src);
+#pragma unroll 8
   for (int s = 1; s < pl.splits; ++s) v += *reinterpret_cast<const f32x4*>(src + (int64_t)s * a.m * pl.ld);
   uint16_t* const dst = a.out + m * a.o_st + n;
   const uint2 y = make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
@@ -461,7 +462,8 @@ namespace {
 // side, as many as it holds; the parts are then written and read again (at 6 TB/s, and
 // 2.5 us more).  Whole against in parts: 105 x 555 x 2464 10.3 and 8.1 us, 512 x 2048 x 7168
 // (256 tiles of 64 x 64 against four parts of 128 x 128) 22.5 and 20.0, 1024 x 1024 x 8192 26.6
-// and 22.5; 515 x 1003 x 3600 and what is shorter stays whole.
+// and 22.5; 515 x 1003 x 3600 and what is shorter stays whole.  Few rows: 64 x 1024 x 16384 by
+// k_matmul_rows 22.4, in parts of tiles 10.4, 64 x 128 x 8192 12.4 and 9.1, 64 x 128 x 4096 8.1 and 8.3.
 enum Form { kRows, kTile64, kTile128x64, kTile128, kTwo128, kTile256 };
 struct Choice {
   Form form;
@@ -469,7 +471,7 @@ struct Choice {
 };
 Choice choose(int64_t m, int64_t n, int64_t k) {
   const int64_t across = (k + 127) / 128;
-  if (m <= 64) return Choice{kRows, 1, (int)across};
+  if (m == 0) return Choice{kRows, 1, (int)across};   // nothing to make
   auto tiles = [&](int bn, int bm) { return ((n + bn - 1) / bn) * ((m + bm - 1) / bm); };
   const double two = (double)((tiles(128, 128) + 511) / 512) * (1.25 * (double)across + 5.0);
   const double large = (double)((tiles(256, 256) + 255) / 256) * (2.1 * (double)across + 8.0);
@@ -478,6 +480,12 @@ Choice choose(int64_t m, int64_t n, int64_t k) {
   constexpr struct { Form form; int bn, bm; double block; } small[] = {
       {kTile64, 64, 64, 0.3}, {kTile128x64, 128, 64, 0.38}, {kTile128, 128, 128, 0.5}};
   bool fits = false;
+  if (m <= 64) {   // (an eighth of the blocks one after another: where that is long, parts of tiles)
+    const double alone = m <= 16 ? 2.45 : m <= 32 ? 2.9 : 3.65, block = m <= 16 ? 0.6 : m <= 32 ? 0.78 : 1.1;
+    best = Choice{kRows, 1, (int)across};
+    least = alone + block * (double)((across + 7) / 8);
+    fits = true;
+  }
   for (const auto& f : small) {
     const int64_t held = 256 / tiles(f.bn, f.bm);   // parts that the card holds
     for (int64_t s = 1; s <= held && (s == 1 || across >= 4 * s); ++s) {
