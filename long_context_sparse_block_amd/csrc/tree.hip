@@ -78,6 +78,20 @@ hipError_t launch_plan_tree(int n_seq, const int32_t* parents, const int32_t* q_
   return hipGetLastError();
 }
 
+// Which entry of a path a lane reads for entry i: itself, or, where the path has none, its first or last one, whose
+// value the lane does not use
+__host__ __device__ constexpr int path_entry(int i, int max_path) { return i < 0 ? 0 : i < max_path ? i : max_path - 1; }
+// in the path for every lane's entry and the one before it, of paths of one entry too
+constexpr bool path_entries_inside(int max_path) {
+  for (int i = -1; i < (max_path + 63) / 64 * 64; ++i) {
+    const int at = path_entry(i, max_path);
+    if (at < 0 || at >= max_path || (i >= 0 && i < max_path && at != i)) return false;
+  }
+  return true;
+}
+static_assert(path_entries_inside(1) && path_entries_inside(2) && path_entries_inside(63) && path_entries_inside(64) &&
+              path_entries_inside(65) && path_entries_inside(130), "a path's loads stay in it");
+
 // A workgroup takes a sequence (and, of wide rows, some of their pieces), a thread
 // a piece of every row: 16 (or 8) bytes of the keys or values, or one scale.  Row i
 // of the kept ones comes from place path[i] >= i, and path rises, so a thread that
@@ -112,8 +126,8 @@ __global__ void __launch_bounds__(256) k_keep_path(const KeepArgs a) {
   for (int i0 = 0; i0 < a.max_path; i0 += 64) {
     const int i = i0 + lane;
     const int32_t* const path = a.path + (int64_t)b * a.max_path;
-    const int node = path[min(i, a.max_path - 1)];
-    const int before = i > 0 ? path[min(i, a.max_path - 1) - 1] : -1;
+    const int node = path[path_entry(i, a.max_path)];
+    const int last = path[path_entry(i - 1, a.max_path)], before = i > 0 ? last : -1;
     const bool ok = i < a.max_path && node > before && node >= 0 && node < m;
     const uint64_t gone = ~__ballot(ok);
     const int n = gone == 0 ? 64 : (int)__builtin_ctzll(gone);   // kept ones of these 64
