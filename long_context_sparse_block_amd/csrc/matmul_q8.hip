@@ -59,14 +59,15 @@ struct Plan {
 
 // The same unknown to the compiler, which would otherwise wait for all loads into
 // LDS before any read of the array that they fill.  Who reads waits: landed().
-// (dst: offset in LDS; no vector register is written, and m0 nothing else in the kernel uses)
+// (dst: offset in LDS, by way of m0, which the compiler writes; it does not count the wait state that a load into LDS
+// takes behind that.  No vector register is written.)
 template <int BYTES>
 __device__ __forceinline__ void stage_far(__amdgpu_buffer_rsrc_t r, uint32_t dst, uint32_t off, uint32_t add) {
 #ifdef __HIP_DEVICE_COMPILE__
   if constexpr (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(dst), "v"(off), "s"(r), "s"(add) : "memory");
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"{m0}"(dst), "v"(off), "s"(r), "s"(add) : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(dst), "v"(off), "s"(r), "s"(add) : "memory");
+    asm volatile("s_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"{m0}"(dst), "v"(off), "s"(r), "s"(add) : "memory");
 #endif
 }
 // All of the workgroup's loads but each wave's last N have landed in LDS, and its reads are done
