@@ -7,7 +7,7 @@ an accepted path's rows, and e4m3 projections with a scale for each block of 128
 As in _lib: argument marshalling only, raw device pointers and the current HIP
 stream (of the tensors' own device) go to the library, and there is no
 fallback.  misa_rope takes part in autograd; the other calls serve, and their
-outputs have no gradient.
+outputs have no gradient (misa_attention_tree's say so when asked for one).
 """
 from __future__ import annotations
 
@@ -499,12 +499,39 @@ def misa_plan_tree(parents, q_start, kv_lens, words: int, plan: TreePlan | None 
     return plan
 
 
+def _wants_grad(t):
+    return t is not None and t.requires_grad
+
+
+class _NoBackward(torch.autograd.Function):
+    """A call without a backward pass, of inputs that require a gradient: its outputs require one too, and asking them
+    for it is an error, where outputs cut off the graph would lose it without a word."""
+
+    @staticmethod
+    def forward(ctx, name, call, *inputs):
+        ctx.call_name = name
+        return call()
+
+    @staticmethod
+    def backward(ctx, *g):
+        raise RuntimeError(f"{ctx.call_name} has no backward pass: detach its inputs, or call it under torch.no_grad()")
+
+
 def misa_attention_tree(q, k_pages, v_pages, block_table, q_start, kv_lens, mask, k_scale_pages=None,
                         v_scale_pages=None, scale=None, max_new: int = 0, out=None, lse=None, want_lse=False, ws=None,
                         stream=None):
     """misa_attention_paged of trees of drafted tokens: a sequence's new token i sees
     its cached tokens and those new tokens j whose bit j its mask row has
-    (int32 [tokens, words], as misa_plan_tree gives it or any other)."""
+    (int32 [tokens, words], as misa_plan_tree gives it or any other).  There is no
+    backward pass: where q, keys or values require a gradient, asking a new out or
+    lse for one raises (a given one has none)."""
+    if out is None and torch.is_grad_enabled() and (_wants_grad(q) or _wants_grad(k_pages) or _wants_grad(v_pages)):
+        def call():
+            o, l = misa_attention_tree(q, k_pages, v_pages, block_table, q_start, kv_lens, mask, k_scale_pages,
+                                       v_scale_pages, scale, max_new, None, lse, want_lse, ws, stream)
+            return o, (l if lse is None else None)
+        o, l = _NoBackward.apply("misa_attention_tree", call, q, k_pages, v_pages)
+        return o, (l if lse is None else lse)
     return _attention("misa_attention_tree", q, k_pages, v_pages, block_table, q_start, kv_lens, mask, k_scale_pages,
                       v_scale_pages, scale, max_new, out, lse, want_lse, ws, stream)
 
@@ -554,7 +581,8 @@ def misa_quantize_blocks(x, block_rows: int = 1, codes=None, scale=None, stream=
     """e4m3 codes (uint8) of x [rows, columns] (bf16, fp16 or fp32; any row stride that
     keeps rows 16-byte aligned; columns a multiple of 16) and the fp32 scales of its
     blocks of block_rows x 128, [ceil(rows / block_rows), ceil(columns / 128)]:
-    block_rows = 1 for activations, 128 for weights."""
+    block_rows = 1 for activations, 128 for weights.  Codes are whole numbers: no
+    gradient passes them, nor the scales."""
     if stream is not None:
         return _on(stream, x, "x", misa_quantize_blocks, x, block_rows, codes, scale)
     dev = _dev(x, "x")
@@ -583,7 +611,7 @@ def misa_matmul_q8_workspace_bytes(m: int, n: int, k: int) -> int:
 def misa_matmul_q8(x, x_scale, w, w_scale, out=None, ws=None, stream=None):
     """x w^T in bf16 of e4m3 codes x [m, k] with a scale for each 1 x 128 block and w [n, k] with one for each
     128 x 128 (misa_quantize_blocks; uint8 or float8_e4m3fn, rows 16-byte aligned, k a
-    multiple of 16).  out: bf16 [m, n], its last dimension dense."""
+    multiple of 16).  out: bf16 [m, n], its last dimension dense; it has no gradient."""
     if stream is not None:
         return _on(stream, x, "x", misa_matmul_q8, x, x_scale, w, w_scale, out, ws)
     dev = _dev(x, "x")
