@@ -339,7 +339,10 @@ __global__ void __launch_bounds__(8 * kWave, 2) k_matmul_rows(const MatmulArgs a
   struct Codes {
     i32x4 w[NT][2];
   };
-  // scales of four blocks: a lane's of one block are as many lines apart as of four
+  // scales of four blocks: a lane's of one block are as many lines apart as of four.  Past the last block they are the
+  // next row's, or, behind the last row's, 0 without a read: the unit's bounds check takes in the scalar offset (the
+  // builtin's documentation leaves it out) and goes by single dwords, as measured on buffers that end before their
+  // memory does, with offsets before and past the end, to registers and to LDS.
   struct Scales {
     f32x4 x[MT], w;
   };

@@ -225,3 +225,18 @@ def test_few_rows_past_4_gib():
     got = misa.misa_matmul_q8(*(t.cuda() for t in ops), out=out[:, :n])
     th.check_product(got, *ops)
     assert (out[:, n:n + 64] == 7).all() and (out[:, -64:] == 7).all()
+
+
+@pytest.mark.parametrize("m,n,k,stride", [(70, 40, 256, 16), (300, 130, 528, 144), (33, 70, 400, 0), (131, 300, 272, 0), (77, 4099, 272, 256)])
+def test_products_of_rows_that_share_codes(m, n, k, stride):
+    """x as windows of one run of codes, or one row for all; the codes behind the last window are NaN."""
+    size = (m - 1) * stride + k
+    x8 = th.quantize(torch.randn((1, -(-size // 16) * 16), generator=torch.Generator().manual_seed(m)), 1)[0]
+    _, _, w8, ws = operands(m + n, 1, n, k)
+    xs = 0.5 + torch.rand((m, -(-k // 128)), generator=torch.Generator().manual_seed(n))
+    run = torch.full((size + 65536,), 0x7F, dtype=torch.uint8, device="cuda")
+    run[:size] = x8[0, :size].cuda()
+    rows = x8[0].as_strided((m, k), (stride, 1))
+    got = misa.misa_matmul_q8(run.as_strided((m, k), (stride, 1)), xs.cuda(), w8.cuda(), ws.cuda())
+    th.check_product(got, rows.contiguous(), xs, w8, ws)
+    assert torch.equal(got, misa.misa_matmul_q8(rows.contiguous().cuda(), xs.cuda(), w8.cuda(), ws.cuda()))
