@@ -662,6 +662,10 @@ size_t misa_attention_selected_workspace_bytes(const misa_attn_shape* shape, con
  *                 text that it is drafted for, which misa_rope turns it by
  * Rows that are no sequence's (in front of q_start[0], from q_start[n_seq] on)
  * get an empty mask and position -1.
+ * A token takes a step for each of its ancestors: a chain of 256 tokens 23 us, of
+ * 1024 85, of 8192 1070, and where a sequence has more than 32 * words tokens
+ * a thread has several of its walks to make.  A prompt's chunk is not planned as a
+ * chain: misa_attention_paged takes it as it is.
  * parents: int32 [n_tokens]; q_start, kv_lens as misa_plan_pages writes them.
  * mask: uint32 [n_tokens][words], positions: int32 [n_tokens]; they overlap
  * nothing else.  1 <= words <= 1024, 1 <= n_seq <= 65535, n_tokens <= 2^26.
@@ -677,6 +681,8 @@ misa_status misa_plan_tree(int32_t n_seq, const int32_t* parents, const int32_t*
  * out = 0, lse = -inf.  All else is as in misa_attention_paged, its limits too.
  * NaN and infinity in a value among a sequence's new tokens may reach others of
  * its new tokens, never another sequence.
+ * Over picked tokens there is no such call: misa_attention_selected takes no mask, and
+ * a node's picks may name other branches' tokens, which the caller makes -1 first.
  * ws: misa_attention_tree_workspace_bytes() bytes, as misa_attention_paged's.
  * mask: uint32 [n_tokens][words], 1 <= words <= 1024 (MISA_ERR_UNSUPPORTED past it).
  */

@@ -25,7 +25,7 @@
 // are set: a word or two of the mask row a tile) cost what a chain costs: 64 tokens
 // over 8192 keys 24.3 us (24.1 as a chain; the call, of which the join 5), 64 trees of
 // 16 over 8..16K 655-670 us (5 TB/s of keys and values), nine of 1 to 257 over e4m3
-// pages, heads of 64, 59-64 us.
+// pages, heads of 64, 58-66 us by card.
 // 32 rows a wave: with 64, or with scores formed a tile ahead, the registers
 // leave one wave a SIMD, and both were slower (1.17 to 1.6 ms).  NW = 2 where a
 // unit has at most 64 rows: half the rows of 4 would be empty.

@@ -11,10 +11,10 @@
 // a lane's results are one row of x, whose scale is one factor a lane.
 //
 // Measured: 8192 x 8192 x 4096 272-282 us by card (1952 to 2018 TFLOP/s; the library's
-// product of the same codes with one scale for all 227 us), 8192 x 4096 x 8192 258 us
+// product of the same codes with one scale for all 211-227 us), 8192 x 4096 x 8192 258 us
 // (2129); the clock falls to 1.75-1.9 GHz there, MFMA is busy 0.50-0.56 of the time, the
-// vector unit 0.36-0.45.  515 x 4099 x 1504 13-14 us, 64 x 8192 x 2048 7.6-8.4 us, 1 x 8192 x
-// 4096 7.9 us (33.6 MB, 4.3 TB/s).
+// vector unit 0.36-0.45.  515 x 4099 x 1504 12.5-14 us, 64 x 8192 x 2048 7.4-8.4 us, 1 x 8192 x
+// 4096 7.1-7.9 us (33.6 MB, 4.3 to 4.7 TB/s).
 // Tried on the large tiles and not kept: a workgroup that goes on to the next tile with
 // its first block on the way (286 us; the results leave in smaller pieces, 18
 // registers are spilled), a second barrier in the middle of a block to ask for the
@@ -468,6 +468,8 @@ namespace {
 // (256 tiles of 64 x 64 against four parts of 128 x 128) 22.5 and 20.0, 1024 x 1024 x 8192 26.6
 // and 22.5; 515 x 1003 x 3600 and what is shorter stays whole.  Few rows: 64 x 1024 x 16384 by
 // k_matmul_rows 22.4, in parts of tiles 10.4, 64 x 128 x 8192 12.4 and 9.1, 64 x 128 x 4096 8.1 and 8.3.
+// (Few rows' times here are those of up to some 4096 columns: of more, of long rows, a workgroup's reading of x and
+// the card's of w come on top, 64 x 8192 x 8192 19.4-19.8 us for the 12.5 that are reckoned.)
 enum Form { kRows, kTile64, kTile128x64, kTile128, kTwo128, kTile256 };
 struct Choice {
   Form form;

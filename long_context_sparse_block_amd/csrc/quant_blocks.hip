@@ -6,7 +6,7 @@
 // input.  (At a scale below the smallest normal number the quotients would lose
 // bits, or pass 448.)
 //
-// Bound by HBM, the quotients close behind (8192 x 4096 in bf16: 16.7-17.3 us, 101 MB,
+// Bound by HBM, the quotients close behind (8192 x 4096 in bf16: 16.5-17.3 us, 101 MB,
 // the vector unit busy 0.86 of it; with true divisions 19.9).  64 x 2048: 2.8 us,
 // a launch's.
 #include "misa_common.h"

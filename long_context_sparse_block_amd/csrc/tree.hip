@@ -5,9 +5,9 @@
 //
 // Both move a few KB: what bounds them is the launch and a chain of dependent
 // loads (lengths, then parents or path and table, then the rows).  Measured: the plan
-// of 64 trees of 32 3.4 us, of 500 trees of up to 256 8.2 us (a walk of some 60 steps);
-// kept paths of up to 8 of 32 nodes, 64 sequences, 8 + 8 heads of 128 5.9 us, of up to
-// 12 of 64, 500 sequences' index keys 6.2 us.
+// of 64 trees of 32 3.4 us, of 500 trees of up to 256 7.2 to 8.6 us (a walk of some 60 steps);
+// kept paths of up to 8 of 32 nodes, 64 sequences, 8 + 8 heads of 128 5.4-6.2 us, of up to
+// 12 of 64, 500 sequences' index keys 5.8-6.5 us.
 #include <algorithm>
 
 #include "misa_common.h"
